@@ -629,6 +629,69 @@ LA_API la_status la_decode_step(const void* q, const void* k, const void* v,
                          int B, int H, int Dk, int Dv,
                          la_dtype dtype, la_stream_t stream);
 
+/*
+ * The gated delta rule: linear attention whose update writes the error of
+ * the state's own prediction instead of the value.  Per (b, h), t = 1..T:
+ *
+ *     S'  = g_t S_{t-1}                        state, [Dk, Dv], fp32
+ *     e_t = v_t - S'^T k_t                     prediction error
+ *     S_t = S' + k_t (beta_t e_t)^T
+ *     y_t = q_scale * S_t^T q_t
+ *
+ * With keys of norm 1 and beta in (0, 1) the update overwrites a share beta
+ * of what the state holds along k_t; beta_t = 0 with log g_t = 0 leaves the
+ * state as it was (padding).  Keys and queries are used as given: normalise
+ * them before (la_gated_norm with LA_NORM_L2).  beta_t |k_t|^2 below 2 keeps
+ * the recurrence from growing; nothing here enforces it.
+ *
+ * Head layout: q and k have Hk heads, v, beta, the decay, the state and the
+ * output H heads, H a multiple of Hk: key head j serves value heads
+ * j H / Hk .. (j + 1) H / Hk - 1.  dq and dk are summed over those.
+ *
+ * la_delta_forward_ws - the whole sequence.
+ *
+ *   q, k           [B,Hk,T,Dk], `dtype`.
+ *   v, out         [B,H,T,Dv], `dtype`.
+ *   beta           [B,H,T] fp32, finite.
+ *   decay          NULL or a descriptor as for la_chunk_forward.  A log g below
+ *                  -128 (-infinity included) counts as -128: e^-128 is zero next to anything an
+ *                  fp32 state can hold.
+ *   q_scale        finite factor of the output.
+ *   init_state     NULL (zeros) or S_0; final_state NULL or S_T: [B,H,Dk,Dv] fp32.
+ *   workspace      la_delta_workspace_size(...) bytes of device memory, 16-byte
+ *                  aligned; it holds nothing between calls.  Two calls that may
+ *                  run at the same time (two streams, two captured graphs) need
+ *                  one each.
+ *
+ * bf16: Dk and Dv multiples of 16 up to 128; fp32: any width up to 128.  The
+ * state is carried with fp32 accuracy for both.  B*H == 0 is a no-op; T == 0
+ * copies init_state (or 0) to final_state.  Outputs must not overlap inputs.
+ *
+ * Errors (synchronous, nothing enqueued): LA_ERR_INVALID_ARG for a NULL or
+ * misaligned pointer (16 bytes; 4 for beta and log_g), bad sizes (H not a
+ * multiple of Hk among them), a bad decay or dtype, a q_scale that is not
+ * finite, a workspace that is NULL or too small; LA_ERR_UNSUPPORTED for other
+ * widths or more than 2^31 - 1 blocks; LA_ERR_CUDA if a launch fails.
+ */
+LA_API la_status la_delta_forward_ws(const void* q, const void* k, const void* v, const float* beta,
+                                     const la_decay* decay, float q_scale, const float* init_state,
+                                     void* out, float* final_state, int B, int H, int Hk, int T, int Dk,
+                                     int Dv, la_dtype dtype, void* workspace, size_t workspace_bytes,
+                                     la_stream_t stream);
+
+/* Bytes la_delta_forward_ws needs (0 for sizes it rejects or has nothing to do for). */
+LA_API size_t la_delta_workspace_size(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype);
+
+/*
+ * la_delta_decode_step - one token of the gated delta rule, `state` updated in
+ * place.  q, k [B,Hk,Dk], v, out [B,H,Dv], `dtype`; beta [B,H]; decay as for
+ * la_decode_step; state [B,H,Dk,Dv] fp32.  Any Dk, Dv up to 128.  Errors as for
+ * la_delta_forward_ws.
+ */
+LA_API la_status la_delta_decode_step(const void* q, const void* k, const void* v, const float* beta,
+                                      const la_decay* decay, float q_scale, float* state, void* out, int B,
+                                      int H, int Hk, int Dk, int Dv, la_dtype dtype, la_stream_t stream);
+
 /* A static string naming a status code. */
 LA_API const char* la_status_string(la_status status);
 

@@ -28,6 +28,7 @@ import subprocess
 
 import numpy as np
 
+from .delta import delta_backward, delta_decode_step, delta_forward  # noqa: F401
 from .parallel import parallel_forward, parallel_reverse  # noqa: F401
 
 _HERE = os.path.dirname(os.path.abspath(__file__))

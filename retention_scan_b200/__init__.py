@@ -17,6 +17,7 @@ __all__ = ["chunk_forward", "bidirectional", "chunk_backward", "chunk_backward_n
            "chunk_state", "state_combine", "state_workspace_size", "workspace_size",
            "backward_workspace_size",
            "decode_step", "device_error", "LAError", "lib", "library_path",
+           "delta_forward", "delta_workspace_size", "delta_decode_step",
            "DECAY_NONE", "DECAY_PER_HEAD", "DECAY_PER_STEP", "FEATURE_NONE", "FEATURE_ELU1", "EXPORTED_SYMBOLS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -31,6 +32,7 @@ EXPORTED_SYMBOLS = ("la_chunk_forward", "la_chunk_forward_ws", "la_chunk_forward
                     "la_wkv4_forward_ws", "la_wkv4_workspace_size", "la_chunk_forward_pro_ws",
                     "la_decode_step_pro", "la_chunk_backward_norm_ws", "la_chunk_backward_norm_workspace_size",
                     "la_ema_scan", "la_chunk_state_ws", "la_chunk_state_workspace_size", "la_state_combine",
+                    "la_delta_forward_ws", "la_delta_workspace_size", "la_delta_decode_step",
                     "la_decode_step", "la_status_string", "la_device_error", "la_version")
 
 
@@ -110,6 +112,14 @@ def lib():
         L.la_decode_step.argtypes = [vp, vp, vp, ctypes.POINTER(_Decay), i, vp, vp, vp,
                                      i, i, i, i, i, vp]
         L.la_decode_step.restype = i
+        f, sz = ctypes.c_float, ctypes.c_size_t
+        L.la_delta_forward_ws.argtypes = [vp, vp, vp, vp, ctypes.POINTER(_Decay), f, vp, vp, vp,
+                                          i, i, i, i, i, i, i, vp, sz, vp]
+        L.la_delta_forward_ws.restype = i
+        L.la_delta_workspace_size.argtypes = [i, i, i, i, i, i, i]
+        L.la_delta_workspace_size.restype = sz
+        L.la_delta_decode_step.argtypes = [vp, vp, vp, vp, ctypes.POINTER(_Decay), f, vp, vp, i, i, i, i, i, i, vp]
+        L.la_delta_decode_step.restype = i
         L.la_status_string.argtypes = [i]
         L.la_status_string.restype = ctypes.c_char_p
         L.la_device_error.argtypes = [ctypes.POINTER(ctypes.c_int), vp]
@@ -590,3 +600,6 @@ def device_error(device=None, stream=None):
     with torch.cuda.device(dev):
         _check(lib().la_device_error(ctypes.byref(code), _stream(stream, dev)))
     return code.value
+
+
+from .delta import delta_decode_step, delta_forward, delta_workspace_size  # noqa: E402

@@ -12,6 +12,7 @@
 #include <cstring>
 
 #include "la.h"
+#include "la_check.h"
 #include "la_internal.h"
 
 namespace la {
@@ -70,22 +71,12 @@ void* device_symbol_address(const void* symbol, int slot) {
 
 namespace {
 
+using namespace la::check;
+
 // Set by a kernel that gave up waiting on one of its barriers (kErr* codes).
 __device__ int g_err_word;
 
 int* err_word_for_current_device() { return static_cast<int*>(la::device_symbol_address(&g_err_word, la::kSymErrWord)); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-// Host-side fault injection for tests: LA_FAULT_INJECT=launch makes every
-// compute entry point report a failed launch without enqueuing anything.
-bool launch_fault_injected() {
-    const char* e = std::getenv("LA_FAULT_INJECT");
-    return e && std::strcmp(e, "launch") == 0;
-}
-
-bool fits_int(long long x) { return x >= 0 && x <= INT_MAX; }
 
 la_status check_prologue(const la_prologue* pro, int* fmap, float* qscale) {
     *fmap = LA_FEATURE_NONE;
@@ -95,19 +86,6 @@ la_status check_prologue(const la_prologue* pro, int* fmap, float* qscale) {
     if (!std::isfinite(pro->q_scale)) return LA_ERR_INVALID_ARG;
     *fmap = pro->feature_map;
     *qscale = pro->q_scale;
-    return LA_OK;
-}
-
-la_status check_decay(const la_decay* decay, int* kind, const float** log_g) {
-    *kind = LA_DECAY_NONE;
-    *log_g = nullptr;
-    if (!decay) return LA_OK;
-    if (decay->kind < LA_DECAY_NONE || decay->kind > LA_DECAY_PER_STEP) return LA_ERR_INVALID_ARG;
-    *kind = decay->kind;
-    if (*kind != LA_DECAY_NONE) {
-        if (!decay->log_g || !aligned4(decay->log_g)) return LA_ERR_INVALID_ARG;
-        *log_g = decay->log_g;
-    }
     return LA_OK;
 }
 
@@ -205,8 +183,6 @@ struct BwdLayout {
     size_t s0t, dsft, st, lsh, dlog, scan, scan_bytes, scan2, scan2_bytes, total;
     int shared_pieces;  // state pieces per (b, h) that the dk and dv scans share (0: none)
 };
-
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 // share_states (the unnormalised backward): the dk and dv reverse scans
 // compute the same state, transposed (sum q dy^T and sum dy q^T, with the

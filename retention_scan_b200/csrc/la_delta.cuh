@@ -1,0 +1,278 @@
+// la_delta.cuh - the gated delta rule's device code shared by its kernels.
+//
+//   S'  = g_t S_{t-1}                 e_t = v_t - S'^T k_t
+//   S_t = S' + k_t (beta_t e_t)^T     y_t = scale * S_t^T q_t
+//
+// Chunked form (C = 64 tokens, L_t the chunk's inclusive prefix of log g,
+// S the state before the chunk, A_ts = e^(L_t - L_s) k_t.k_s for s < t):
+//
+//   E = (I + A diag(beta))^-1 (V - diag(e^L) K S)        U = diag(beta) E
+//   Y = scale diag(e^L) Q S + P U,  P_ts = scale e^(L_t - L_s) q_t.k_s, s <= t
+//   S <- e^(L_C) S + (diag(e^(L_C - L)) K)^T U
+//
+// beta scales the columns of A, not its rows, so that E needs no division and
+// a token with beta = 0 (padding) still has its error e_t for the gradient.
+//
+// The state's Dv columns never mix, so one warp owns 16 of them and carries
+// S^T (16 x Dk, fp32) in the accumulator registers of mma.m16n8k16: the
+// accumulator of one product has the register layout of the next product's A
+// operand, and the whole chain S -> K S -> E -> U -> S runs without shared
+// memory, shuffles or block barriers between the products.  Only K, Q, P and
+// (I + A diag(beta))^-1 come through shared memory, as B operands, and are
+// shared by the block's warps.
+//
+// Precision: the tensor core takes bf16.  An fp32 operand x is passed as
+// x = x0 + x1 (+ x2), each x_i the bf16 rounding of what is left, and a product
+// of operands with planes i and j is accumulated for i + j < NM: with NM = 2
+// a product is within about 2^-16 of fp32's, with NM = 3 within 2^-23.  bf16
+// inputs are exact in one plane and run with NM = 2; fp32 inputs take three
+// planes and NM = 3.  Plain bf16 or tf32 operands (2^-9, 2^-12) would leave
+// the fp32 state and the fp32 gradients with three digits.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace la {
+namespace delta {
+
+constexpr int C = 64;            // tokens per chunk
+constexpr int kPad = 8;          // bf16 padding of a shared-memory row: ldmatrix without bank conflicts
+constexpr int kCS = C + kPad;    // row stride of a C-wide tile
+constexpr int kTok = 3 * C;      // floats per chunk of per-token factors: e^L, e^(L_C - L), beta
+constexpr float kLogFloor = -128.f;  // a decay below e^-128 is zero in fp32 next to anything it is added to
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t mov_trans(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16 bytes, or zeros where !valid (src stays a valid address either way).
+__device__ __forceinline__ void cp16(void* dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(valid ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float low_of(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float high_of(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// The bf16 planes of the fp32 pair (x, y): p[i] rounds what planes 0..i-1 left.
+template <int N>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        p[i] = pack(x, y);
+        x -= low_of(p[i]);
+        y -= high_of(p[i]);
+    }
+}
+
+// A operand (16 x 16) planes from two neighbouring accumulator tiles.
+template <int N>
+__device__ __forceinline__ void split_frag(const float (&x)[4], const float (&y)[4], uint32_t (&a)[N][4]) {
+    uint32_t t[N];
+    split2<N>(x[0], x[1], t);
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i][0] = t[i];
+    split2<N>(x[2], x[3], t);
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i][1] = t[i];
+    split2<N>(y[0], y[1], t);
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i][2] = t[i];
+    split2<N>(y[2], y[3], t);
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i][3] = t[i];
+}
+
+// Lane addresses of ldmatrix.x4 on a 16 x 16 block of a bf16 tile with
+// `stride` elements a row.  One lane order visits the four 8 x 8 matrices
+// along the columns first, the other along the rows first:
+//   B stored [n][k]: ldsm4 with off_cols;    B stored [k][n]: ldsm4t with off_rows
+//   A stored [m][k]: ldsm4 with off_rows;    A stored [k][m]: ldsm4t with off_cols
+// B registers 0, 1 are columns n..n+7, registers 2, 3 columns n+8..n+15.
+__device__ __forceinline__ int off_cols(int lane, int stride) {
+    return ((lane & 7) + ((lane >> 4) << 3)) * stride + ((lane >> 3) & 1) * 8;
+}
+__device__ __forceinline__ int off_rows(int lane, int stride) { return (lane & 15) * stride + (lane >> 4) * 8; }
+
+// acc[j][:] += A B for the 16-column block of B whose registers are b: A
+// planes NA, this B plane's index `pb`; keeps planes with pa + pb < NM.
+template <int NA, int NM>
+__device__ __forceinline__ void mma_planes(float (&d0)[4], float (&d1)[4], const uint32_t (&a)[NA][4], int pb,
+                                           const uint32_t (&b)[4]) {
+#pragma unroll
+    for (int pa = 0; pa < NA; ++pa)
+        if (pa + pb < NM) {
+            mma(d0, a[pa], b[0], b[1]);
+            mma(d1, a[pa], b[2], b[3]);
+        }
+}
+
+// q or k as bf16 planes: plane p of head hk, token t starts at
+// base + p * plane + hk * head + t * row; rows and cols hold data, the rest of
+// a tile is zero.
+struct Planes {
+    const __nv_bfloat16* base;
+    long long plane, head;
+    int row, rows, cols;
+};
+
+// One C x DKP tile of every plane into shared memory (rows of DKP + kPad).
+template <int DKP, int NI>
+__device__ __forceinline__ void load_tile(__nv_bfloat16* dst, const Planes& src, long long hk, int t0, int tid, int nthreads) {
+    constexpr int kVec = DKP / 8;
+#pragma unroll
+    for (int p = 0; p < NI; ++p) {
+        const __nv_bfloat16* s = src.base + p * src.plane + hk * src.head;
+        for (int i = tid; i < C * kVec; i += nthreads) {
+            const int r = i / kVec, c = (i % kVec) * 8;
+            const bool ok = t0 + r < src.rows && c < src.cols;
+            cp16(dst + (p * C + r) * (DKP + kPad) + c, ok ? s + static_cast<long long>(t0 + r) * src.row + c : src.base, ok);
+        }
+    }
+}
+
+// `rows` x 64 dense planes (64 bf16 a row) into rows of kCS.
+__device__ __forceinline__ void load_square(__nv_bfloat16* dst, const __nv_bfloat16* src, int rows, int tid, int nthreads) {
+    for (int i = tid; i < rows * (C / 8); i += nthreads) {
+        const int r = i / (C / 8), c = (i % (C / 8)) * 8;
+        cp16(dst + r * kCS + c, src + r * C + c, true);
+    }
+}
+
+// Value-side operand ([B,H,T,Dv], bf16 or fp32) of one chunk, transposed into
+// accumulator layout: x[j][0..1] = column v0 + g, tokens 8 j + 2 t', +1;
+// x[j][2..3] = column v0 + g + 8 (g = lane / 4, t' = lane % 4).
+// bf16: from the block's shared tile (row stride `stride`), v_local columns in.
+__device__ __forceinline__ void values_from_tile(float (&x)[8][4], const __nv_bfloat16* tile, int stride, int v_local,
+                                                 int lane) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        uint32_t r[4];
+        ldsm4t(r, smem_addr(tile + (16 * n) * stride + v_local + off_rows(lane, stride)));
+        // r0: tokens 0-7, columns 0-7; r1: tokens 8-15, columns 0-7; r2, r3: columns 8-15
+        x[2 * n][0] = low_of(r[0]);
+        x[2 * n][1] = high_of(r[0]);
+        x[2 * n + 1][0] = low_of(r[1]);
+        x[2 * n + 1][1] = high_of(r[1]);
+        x[2 * n][2] = low_of(r[2]);
+        x[2 * n][3] = high_of(r[2]);
+        x[2 * n + 1][2] = low_of(r[3]);
+        x[2 * n + 1][3] = high_of(r[3]);
+    }
+}
+// fp32: straight from global memory.
+__device__ __forceinline__ void values_from_global(float (&x)[8][4], const float* base, int t0, int T, int Dv, int v0,
+                                                   int lane) {
+    const int g = lane >> 2, tq = (lane & 3) * 2;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = t0 + 8 * j + tq + (i & 1), v = v0 + g + (i >> 1) * 8;
+            x[j][i] = t < T && v < Dv ? base[static_cast<long long>(t) * Dv + v] : 0.f;
+        }
+}
+
+// The same layout back to [T, Dv] rows.
+__device__ __forceinline__ void values_to_global(const float (&x)[8][4], __nv_bfloat16* base, int t0, int T, int Dv, int v0,
+                                                 int lane) {
+    const int g = lane >> 2, tq = (lane & 3) * 2;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t lo = mov_trans(pack(x[j][0], x[j][1])), hi = mov_trans(pack(x[j][2], x[j][3]));
+        const int t = t0 + 8 * j + g;
+        if (t < T) {
+            __nv_bfloat16* p = base + static_cast<long long>(t) * Dv + v0 + tq;
+            *reinterpret_cast<uint32_t*>(p) = lo;
+            *reinterpret_cast<uint32_t*>(p + 8) = hi;
+        }
+    }
+}
+__device__ __forceinline__ void values_to_global(const float (&x)[8][4], float* base, int t0, int T, int Dv, int v0,
+                                                 int lane) {
+    const int g = lane >> 2, tq = (lane & 3) * 2;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = t0 + 8 * j + tq + (i & 1), v = v0 + g + (i >> 1) * 8;
+            if (t < T && v < Dv) base[static_cast<long long>(t) * Dv + v] = x[j][i];
+        }
+}
+
+// S^T in accumulator tiles (s[j]: columns 8 j .. 8 j + 7 of Dk) from and to a
+// [Dk][Dv] fp32 state.
+template <int DKP>
+__device__ __forceinline__ void state_load(float (&s)[DKP / 8][4], const float* S, int Dk, int Dv, int v0, int lane) {
+    const int g = lane >> 2, tq = (lane & 3) * 2;
+#pragma unroll
+    for (int j = 0; j < DKP / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int d = 8 * j + tq + (i & 1), v = v0 + g + (i >> 1) * 8;
+            s[j][i] = S && d < Dk && v < Dv ? S[d * Dv + v] : 0.f;
+        }
+}
+template <int DKP>
+__device__ __forceinline__ void state_store(const float (&s)[DKP / 8][4], float* S, int Dk, int Dv, int v0, int lane) {
+    const int g = lane >> 2, tq = (lane & 3) * 2;
+#pragma unroll
+    for (int j = 0; j < DKP / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int d = 8 * j + tq + (i & 1), v = v0 + g + (i >> 1) * 8;
+            if (d < Dk && v < Dv) S[d * Dv + v] = s[j][i];
+        }
+}
+
+// Planes of an A operand to a [v][col] array of bf16 planes (`plane` apart),
+// rows v0.., columns col0..col0+15.
+template <int N>
+__device__ __forceinline__ void frag_to_planes(const uint32_t (&a)[N][4], __nv_bfloat16* base, long long plane, int width,
+                                               int v0, int col0, int lane) {
+    const int g = lane >> 2, tq = (lane & 3) * 2;
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        __nv_bfloat16* r = base + p * plane + (v0 + g) * width + col0 + tq;
+        *reinterpret_cast<uint32_t*>(r) = a[p][0];
+        *reinterpret_cast<uint32_t*>(r + 8 * width) = a[p][1];
+        *reinterpret_cast<uint32_t*>(r + 8) = a[p][2];
+        *reinterpret_cast<uint32_t*>(r + 8 * width + 8) = a[p][3];
+    }
+}
+
+}  // namespace delta
+}  // namespace la

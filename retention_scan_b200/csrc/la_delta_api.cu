@@ -1,0 +1,209 @@
+// la_delta_api.cu - the C ABI of the gated delta rule: argument checks, the
+// workspace's plan and the launches' order.  Nothing here allocates device
+// memory.
+#include <cmath>
+
+#include "la_check.h"
+#include "la_delta_internal.h"
+
+namespace la {
+namespace delta {
+
+bool supports(int Dk, int Dv, la_dtype dtype) {
+    if (Dk > 128 || Dv > 128) return false;
+    return dtype == LA_F32 || (Dk % 16 == 0 && Dv % 16 == 0);
+}
+
+// Value slices (16 columns, one warp each) per block: as many as still leave a
+// block for each SM, so that the tiles a block loads serve several warps.
+static int scan_warps(long long BH, int slices) {
+    int w = slices >= 4 ? 4 : slices >= 2 ? 2 : 1;
+    while (w > 1 && BH * ((slices + w - 1) / w) < 148) w /= 2;
+    return w;
+}
+
+Plan make_plan(const Args& a, bool backward, void* workspace) {
+    Plan p{};
+    p.BH = static_cast<long long>(a.B) * a.H;
+    p.n = static_cast<int>((static_cast<long long>(a.T) + C - 1) / C);
+    p.DKP = a.Dk <= 32 ? 32 : a.Dk <= 64 ? 64 : 128;
+    p.DVP = (a.Dv + 15) / 16 * 16;
+    p.warps = scan_warps(p.BH, p.DVP / 16);
+    const bool f32 = a.dtype == LA_F32;
+    const size_t nm = f32 ? 3 : 2, np = f32 ? 3 : backward ? 2 : 1, bf = sizeof(__nv_bfloat16);
+    const size_t chunks = static_cast<size_t>(p.BH) * p.n, keys = static_cast<size_t>(a.B) * a.Hk;
+    size_t at = 0;
+    auto region = [&](size_t bytes) {
+        void* r = workspace ? static_cast<char*>(workspace) + at : nullptr;
+        at += check::round256(bytes);
+        return r;
+    };
+    p.tok = static_cast<float*>(region(sizeof(float) * chunks * kTok));
+    p.E = static_cast<__nv_bfloat16*>(region(bf * chunks * nm * C * C));
+    p.P = static_cast<__nv_bfloat16*>(region(bf * chunks * np * C * C));
+    if (f32) {
+        const size_t plane = keys * p.n * C * p.DKP;
+        p.qs = static_cast<__nv_bfloat16*>(region(bf * 3 * plane));
+        p.ks = static_cast<__nv_bfloat16*>(region(bf * 3 * plane));
+        p.q = {p.qs, static_cast<long long>(plane), static_cast<long long>(p.n) * C * p.DKP, p.DKP, p.n * C, p.DKP};
+        p.k = p.q;
+        p.k.base = p.ks;
+    } else {
+        p.q = {static_cast<const __nv_bfloat16*>(a.q), 0, static_cast<long long>(a.T) * a.Dk, a.Dk, a.T, a.Dk};
+        p.k = p.q;
+        p.k.base = static_cast<const __nv_bfloat16*>(a.k);
+    }
+    if (backward) {
+        p.S = static_cast<__nv_bfloat16*>(region(bf * chunks * nm * p.DVP * p.DKP));
+        p.dS = static_cast<__nv_bfloat16*>(region(bf * chunks * nm * p.DVP * p.DKP));
+        p.Er = static_cast<__nv_bfloat16*>(region(bf * chunks * nm * p.DVP * C));
+        p.dR = static_cast<__nv_bfloat16*>(region(bf * chunks * nm * p.DVP * C));
+        if (a.H != a.Hk) {
+            const size_t bytes = sizeof(float) * static_cast<size_t>(p.BH) * a.T * a.Dk;
+            p.dqh = static_cast<float*>(region(bytes));
+            p.dkh = static_cast<float*>(region(bytes));
+        }
+        p.dlog = static_cast<double*>(region(sizeof(double) * chunks));
+    }
+    p.bytes = at;
+    return p;
+}
+
+cudaError_t launch_forward(const Plan& p, const Args& a, bool outputs) {
+    return p.DKP == 32 ? forward_w32(p, a, outputs) : p.DKP == 64 ? forward_w64(p, a, outputs) : forward_w128(p, a, outputs);
+}
+
+}  // namespace delta
+}  // namespace la
+
+namespace {
+
+using namespace la::check;
+namespace delta = la::delta;
+
+// As check_decay; with no token to decay (an empty log_g may have no address) only the kind counts.
+la_status check_decay_for(const la_decay* decay, bool tokens, int* kind, const float** log_g) {
+    if (tokens || !decay) return check_decay(decay, kind, log_g);
+    return decay->kind < LA_DECAY_NONE || decay->kind > LA_DECAY_PER_STEP ? LA_ERR_INVALID_ARG : LA_OK;
+}
+
+// Sizes, types and what every call of the family shares.
+la_status check_sizes(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype) {
+    if (B < 0 || H < 0 || T < 0 || Dk < 1 || Dv < 1 || Hk < 0) return LA_ERR_INVALID_ARG;
+    if (H > 0 && (Hk < 1 || H % Hk != 0)) return LA_ERR_INVALID_ARG;
+    if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
+    if (!delta::supports(Dk, Dv, dtype)) return LA_ERR_UNSUPPORTED;
+    const long long BH = static_cast<long long>(B) * H;
+    if (T > (1 << 30) || !fits_int(BH * 8)) return LA_ERR_INVALID_ARG;
+    // blocks are counted in 32 bits; fp32 inputs are split by one thread a column pair
+    if (!fits_int(BH * ((T + 63LL) / 64) * 8) || (T > 0 && BH > LLONG_MAX / 1024 / T)) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+delta::Args size_args(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype) {
+    delta::Args a{};
+    a.B = B;
+    a.H = H;
+    a.Hk = Hk;
+    a.T = T;
+    a.Dk = Dk;
+    a.Dv = Dv;
+    a.dtype = dtype;
+    return a;
+}
+
+size_t workspace_bytes(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype, bool backward) {
+    if (check_sizes(B, H, Hk, T, Dk, Dv, dtype) != LA_OK || B == 0 || H == 0 || T == 0) return 0;
+    return delta::make_plan(size_args(B, H, Hk, T, Dk, Dv, dtype), backward, nullptr).bytes;
+}
+
+cudaError_t copy_or_zero(float* dst, const float* src, size_t bytes, cudaStream_t s) {
+    if (!dst) return cudaSuccess;
+    return src ? cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(dst, 0, bytes, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t la_delta_workspace_size(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype) {
+    return workspace_bytes(B, H, Hk, T, Dk, Dv, dtype, false);
+}
+
+size_t la_delta_backward_workspace_size(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype) {
+    return workspace_bytes(B, H, Hk, T, Dk, Dv, dtype, true);
+}
+
+la_status la_delta_forward_ws(const void* q, const void* k, const void* v, const float* beta, const la_decay* decay,
+                              float q_scale, const float* init_state, void* out, float* final_state, int B, int H, int Hk,
+                              int T, int Dk, int Dv, la_dtype dtype, void* workspace, size_t workspace_bytes,
+                              la_stream_t stream) {
+    la_status st = check_sizes(B, H, Hk, T, Dk, Dv, dtype);
+    if (st != LA_OK) return st;
+    delta::Args a = size_args(B, H, Hk, T, Dk, Dv, dtype);
+    const long long BH = static_cast<long long>(B) * H;
+    if (check_decay_for(decay, BH > 0 && T > 0, &a.decay_kind, &a.log_g) != LA_OK || !std::isfinite(q_scale))
+        return LA_ERR_INVALID_ARG;
+    if ((init_state && !aligned16(init_state)) || (final_state && !aligned16(final_state))) return LA_ERR_INVALID_ARG;
+    if (BH > 0 && T > 0) {
+        for (const void* p : {q, k, v, static_cast<const void*>(out)})
+            if (!p || !aligned16(p)) return LA_ERR_INVALID_ARG;
+        if (!beta || !aligned4(beta)) return LA_ERR_INVALID_ARG;
+        if (!workspace || !aligned16(workspace) ||
+            workspace_bytes < la_delta_workspace_size(B, H, Hk, T, Dk, Dv, dtype))
+            return LA_ERR_INVALID_ARG;
+    }
+    if (BH == 0) return LA_OK;
+    if (launch_fault_injected()) return LA_ERR_CUDA;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    if (T == 0)
+        return copy_or_zero(final_state, init_state, sizeof(float) * BH * Dk * Dv, a.stream) == cudaSuccess ? LA_OK
+                                                                                                           : LA_ERR_CUDA;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.beta = beta;
+    a.scale = q_scale;
+    a.init_state = init_state;
+    a.out = out;
+    a.final_state = final_state;
+    return delta::launch_forward(delta::make_plan(a, false, workspace), a, true) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+la_status la_delta_decode_step(const void* q, const void* k, const void* v, const float* beta, const la_decay* decay,
+                               float q_scale, float* state, void* out, int B, int H, int Hk, int Dk, int Dv,
+                               la_dtype dtype, la_stream_t stream) {
+    if (B < 0 || H < 0 || Hk < 0 || Dk < 1 || Dv < 1) return LA_ERR_INVALID_ARG;
+    if (H > 0 && (Hk < 1 || H % Hk != 0)) return LA_ERR_INVALID_ARG;
+    if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
+    delta::DecodeArgs a{};
+    const long long BH = static_cast<long long>(B) * H;
+    if (check_decay_for(decay, BH > 0, &a.decay_kind, &a.log_g) != LA_OK || !std::isfinite(q_scale))
+        return LA_ERR_INVALID_ARG;
+    if (!fits_int(BH * 8)) return LA_ERR_INVALID_ARG;
+    if (BH > 0) {
+        for (const void* p : {q, k, v, static_cast<const void*>(out), static_cast<const void*>(state)})
+            if (!p || !aligned16(p)) return LA_ERR_INVALID_ARG;
+        if (!beta || !aligned4(beta)) return LA_ERR_INVALID_ARG;
+    }
+    if (Dk > 128 || Dv > 128) return LA_ERR_UNSUPPORTED;
+    if (BH == 0) return LA_OK;
+    if (launch_fault_injected()) return LA_ERR_CUDA;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.beta = beta;
+    a.scale = q_scale;
+    a.state = state;
+    a.out = out;
+    a.B = B;
+    a.H = H;
+    a.Hk = Hk;
+    a.Dk = Dk;
+    a.Dv = Dv;
+    a.dtype = dtype;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    return delta::launch_decode(a) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+}  // extern "C"

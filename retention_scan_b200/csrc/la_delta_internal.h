@@ -1,0 +1,123 @@
+// la_delta_internal.h - the gated delta rule's host-side plan: sizes, the
+// workspace's regions, and the launchers that la_delta_api.cu calls.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "la.h"
+#include "la_delta.cuh"
+
+namespace la {
+namespace delta {
+
+struct Args {
+    const void* q;             // [B,Hk,T,Dk]
+    const void* k;
+    const void* v;             // [B,H,T,Dv]
+    const float* beta;         // [B,H,T]
+    int decay_kind;
+    const float* log_g;
+    float scale;
+    const float* init_state;   // [B,H,Dk,Dv] or null
+    void* out;                 // forward: y; backward: unused
+    float* final_state;        // or null
+    int B, H, Hk, T, Dk, Dv;
+    la_dtype dtype;
+    cudaStream_t stream;
+    // backward only
+    const void* dy;
+    const float* d_final_state;  // or null
+    void* dq;
+    void* dk;
+    void* dv;
+    float* dbeta;
+    float* d_log_g;              // or null
+    float* d_init_state;         // or null
+};
+
+// Where the workspace's regions start; everything a launch needs beyond Args.
+struct Plan {
+    long long BH;
+    int n;        // chunks per sequence
+    int DKP, DVP; // key width of the kernels, value width in whole 16-column slices
+    int warps;    // 16-column slices per block of the scans
+    Planes q, k;
+    float* tok;                 // [BH][n][kTok]
+    __nv_bfloat16 *E, *P;       // [BH][n][planes][C][C]
+    __nv_bfloat16 *qs, *ks;     // fp32 inputs' planes
+    // backward only
+    __nv_bfloat16 *S, *dS;      // [BH][n][planes][DVP][DKP]: states before, gradients after each chunk
+    __nv_bfloat16 *Er, *dR;     // [BH][n][planes][DVP][C]
+    float *dqh, *dkh;           // [BH][T][Dk] per value head, where key heads are shared
+    double* dlog;               // [BH][n]: a chunk's sum of d log g (per-head decay)
+    size_t bytes;
+};
+
+struct ScanArgs {
+    Planes qp, kp;
+    const void* v;
+    const __nv_bfloat16 *E, *P;
+    const float* tok;
+    const float* init_state;
+    void* out;
+    float* final_state;
+    __nv_bfloat16 *Sst, *Est;
+    float scale;
+    int H, Hk, T, Dk, Dv, DVP, n, vblocks;
+};
+
+inline ScanArgs scan_args(const Plan& p, const Args& a) {
+    ScanArgs s{};
+    s.qp = p.q;
+    s.kp = p.k;
+    s.v = a.v;
+    s.E = p.E;
+    s.P = p.P;
+    s.tok = p.tok;
+    s.init_state = a.init_state;
+    s.out = a.out;
+    s.final_state = a.final_state;
+    s.Sst = p.S;
+    s.Est = p.Er;
+    s.scale = a.scale;
+    s.H = a.H;
+    s.Hk = a.Hk;
+    s.T = a.T;
+    s.Dk = a.Dk;
+    s.Dv = a.Dv;
+    s.DVP = p.DVP;
+    s.n = p.n;
+    return s;
+}
+
+bool supports(int Dk, int Dv, la_dtype dtype);
+// Regions from `workspace` on (null: sizes only).
+Plan make_plan(const Args& a, bool backward, void* workspace);
+
+// prep and the scan over the chunks; outputs: y and the final state, else
+// (backward) every chunk's incoming state and errors.
+cudaError_t launch_forward(const Plan& p, const Args& a, bool outputs);
+cudaError_t forward_w32(const Plan& p, const Args& a, bool outputs);
+cudaError_t forward_w64(const Plan& p, const Args& a, bool outputs);
+cudaError_t forward_w128(const Plan& p, const Args& a, bool outputs);
+// After launch_forward(..., false): the reverse scan and the gradients.
+cudaError_t launch_backward(const Plan& p, const Args& a);
+
+struct DecodeArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* beta;
+    int decay_kind;
+    const float* log_g;
+    float scale;
+    float* state;
+    void* out;
+    int B, H, Hk, Dk, Dv;
+    la_dtype dtype;
+    cudaStream_t stream;
+};
+cudaError_t launch_decode(const DecodeArgs& a);
+
+}  // namespace delta
+}  // namespace la

@@ -1,0 +1,104 @@
+"""The gated delta rule: whole sequence, gradients, one token (include/la.h,
+la_delta_*).  Argument checks and output allocation only; every step runs in
+the library's kernels.
+
+    S' = g_t S_{t-1}    e_t = v_t - S'^T k_t    S_t = S' + k_t (beta_t e_t)^T    y_t = q_scale S_t^T q_t
+"""
+import ctypes
+
+import torch
+
+from . import (DECAY_NONE, DECAY_PER_HEAD, DECAY_PER_STEP, _check, _decay, _dtype_code, _need, _ptr, _stream, lib)
+
+
+def _heads(q, k, v, beta, decay_kind, log_g, token):
+    """Sizes (B, H, Hk, T, Dk, Dv) after the shape, dtype and device checks;
+    token: one-token tensors, without the T dimension."""
+    want = 3 if token else 4
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.dim() != want:
+            raise ValueError(f"{name}: expected {want} dimensions, got shape {tuple(t.shape)}")
+    if not q.is_cuda:
+        raise ValueError(f"q: expected a CUDA tensor, got {q.device}")
+    B, Hk, Dk = q.shape[0], q.shape[1], q.shape[-1]
+    H, Dv = v.shape[1], v.shape[-1]
+    T = () if token else (q.shape[2],)
+    if H and (Hk == 0 or H % Hk):
+        raise ValueError(f"v has {H} heads, which is not a multiple of q's {Hk}")
+    _dtype_code(q.dtype)
+    _need(q, "q", (B, Hk, *T, Dk), q.dtype, q.device)
+    _need(k, "k", (B, Hk, *T, Dk), q.dtype, q.device)
+    _need(v, "v", (B, H, *T, Dv), q.dtype, q.device)
+    _need(beta, "beta", (B, H, *T), torch.float32, q.device)
+    if decay_kind == DECAY_PER_HEAD:
+        _need(log_g, "log_g", (H,), torch.float32, q.device)
+    elif decay_kind == DECAY_PER_STEP:
+        _need(log_g, "log_g", (B, H, *T), torch.float32, q.device)
+    elif decay_kind != DECAY_NONE:
+        raise ValueError(f"unknown decay kind {decay_kind}")
+    return B, H, Hk, (1 if token else T[0]), Dk, Dv
+
+
+def _scratch(workspace, nbytes, dev, stream):
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        if stream is not None:
+            workspace.record_stream(stream)
+    elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous uint8 tensor on the inputs' device")
+    return workspace
+
+
+def delta_workspace_size(B, H, T, Dk, Dv, dtype=torch.bfloat16, key_heads=None):
+    """Scratch bytes delta_forward needs (la_delta_workspace_size)."""
+    return int(lib().la_delta_workspace_size(B, H, key_heads or H, T, Dk, Dv, _dtype_code(dtype)))
+
+
+def delta_forward(q, k, v, beta, decay_kind=DECAY_NONE, log_g=None, init_state=None, q_scale=1.0, out=None,
+                  final_state=None, return_final=True, stream=None, workspace=None):
+    """Whole-sequence gated delta rule (la_delta_forward_ws).
+
+    q, k: [B,Hk,T,Dk]; v: [B,H,T,Dv], H a multiple of Hk (key head j serves
+    value heads j H / Hk and the ones after it); float32 or bfloat16 CUDA
+    tensors.  beta [B,H,T] fp32; decay_kind / log_g as chunk_forward;
+    init_state [B,H,Dk,Dv] fp32 or None.  Returns (out [B,H,T,Dv],
+    final_state or None).  workspace: None allocates it with torch on the
+    call's stream, or a CUDA uint8 tensor of at least
+    delta_workspace_size(...) bytes."""
+    B, H, Hk, T, Dk, Dv = _heads(q, k, v, beta, decay_kind, log_g, token=False)
+    dev = q.device
+    _need(init_state, "init_state", (B, H, Dk, Dv), torch.float32, dev)
+    if out is None:
+        out = torch.empty((B, H, T, Dv), dtype=q.dtype, device=dev)
+    _need(out, "out", (B, H, T, Dv), q.dtype, dev)
+    if final_state is None and return_final:
+        final_state = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
+    _need(final_state, "final_state", (B, H, Dk, Dv), torch.float32, dev)
+    d = _decay(decay_kind, log_g)
+    with torch.cuda.device(dev):
+        workspace = _scratch(workspace, delta_workspace_size(B, H, T, Dk, Dv, q.dtype, Hk), dev, stream)
+        _check(lib().la_delta_forward_ws(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(beta), ctypes.byref(d) if d is not None else None, float(q_scale),
+            _ptr(init_state), _ptr(out), _ptr(final_state), B, H, Hk, T, Dk, Dv, _dtype_code(q.dtype),
+            _ptr(workspace), workspace.numel(), _stream(stream, dev)))
+    return out, final_state
+
+
+def delta_decode_step(q, k, v, beta, state, decay_kind=DECAY_NONE, log_g=None, q_scale=1.0, out=None, stream=None):
+    """One token of the gated delta rule (la_delta_decode_step); state
+    [B,H,Dk,Dv] fp32 is updated in place.  q, k: [B,Hk,Dk]; v: [B,H,Dv];
+    beta [B,H] fp32; log_g [H] or [B,H].  Returns out [B,H,Dv]."""
+    B, H, Hk, _, Dk, Dv = _heads(q, k, v, beta, decay_kind, log_g, token=True)
+    dev = q.device
+    if state is None:
+        raise ValueError("state is required")
+    _need(state, "state", (B, H, Dk, Dv), torch.float32, dev)
+    if out is None:
+        out = torch.empty((B, H, Dv), dtype=q.dtype, device=dev)
+    _need(out, "out", (B, H, Dv), q.dtype, dev)
+    d = _decay(decay_kind, log_g)
+    with torch.cuda.device(dev):
+        _check(lib().la_delta_decode_step(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(beta), ctypes.byref(d) if d is not None else None, float(q_scale),
+            _ptr(state), _ptr(out), B, H, Hk, Dk, Dv, _dtype_code(q.dtype), _stream(stream, dev)))
+    return out

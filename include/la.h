@@ -683,6 +683,40 @@ LA_API la_status la_delta_forward_ws(const void* q, const void* k, const void* v
 LA_API size_t la_delta_workspace_size(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype);
 
 /*
+ * la_delta_backward_ws - gradients of la_delta_forward_ws for the loss
+ * sum(dy * y) + sum(d_final_state * final_state).
+ *
+ *   q .. init_state   the forward's inputs.
+ *   dy                [B,H,T,Dv], `dtype`.
+ *   d_final_state     NULL (zeros) or [B,H,Dk,Dv] fp32.
+ *   dq, dk            [B,Hk,T,Dk], `dtype`, summed over the value heads a key
+ *                     head serves, in fp32 and in their order.
+ *   dv                [B,H,T,Dv], `dtype`.
+ *   dbeta             [B,H,T] fp32.
+ *   d_log_g           NULL, or fp32 with log_g's shape (needs a decay): with
+ *                     respect to the natural log of each g_t, for a per-head
+ *                     decay summed over b and t.  Where log g is below -128 it is
+ *                     the gradient at -128.
+ *   d_init_state      NULL or [B,H,Dk,Dv] fp32.
+ *   workspace         la_delta_backward_workspace_size(...) bytes: the
+ *                     states and their gradients at every 64th token among them
+ *                     (about 3.8 KB a token and head at Dk = Dv = 128, bf16).
+ *
+ * Every output is written whole; no atomics, the same bits on every run.
+ * T == 0 copies d_final_state (or 0) to d_init_state and writes zeros to a
+ * per-head d_log_g.  Errors as for la_delta_forward_ws.
+ */
+LA_API la_status la_delta_backward_ws(const void* q, const void* k, const void* v, const float* beta,
+                                      const la_decay* decay, float q_scale, const float* init_state,
+                                      const void* dy, const float* d_final_state, void* dq, void* dk,
+                                      void* dv, float* dbeta, float* d_log_g, float* d_init_state, int B,
+                                      int H, int Hk, int T, int Dk, int Dv, la_dtype dtype, void* workspace,
+                                      size_t workspace_bytes, la_stream_t stream);
+
+/* Bytes la_delta_backward_ws needs. */
+LA_API size_t la_delta_backward_workspace_size(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype);
+
+/*
  * la_delta_decode_step - one token of the gated delta rule, `state` updated in
  * place.  q, k [B,Hk,Dk], v, out [B,H,Dv], `dtype`; beta [B,H]; decay as for
  * la_decode_step; state [B,H,Dk,Dv] fp32.  Any Dk, Dv up to 128.  Errors as for

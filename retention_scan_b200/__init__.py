@@ -17,7 +17,8 @@ __all__ = ["chunk_forward", "bidirectional", "chunk_backward", "chunk_backward_n
            "chunk_state", "state_combine", "state_workspace_size", "workspace_size",
            "backward_workspace_size",
            "decode_step", "device_error", "LAError", "lib", "library_path",
-           "delta_forward", "delta_workspace_size", "delta_decode_step",
+           "delta_forward", "delta_workspace_size", "delta_backward", "delta_backward_workspace_size",
+           "delta_decode_step",
            "DECAY_NONE", "DECAY_PER_HEAD", "DECAY_PER_STEP", "FEATURE_NONE", "FEATURE_ELU1", "EXPORTED_SYMBOLS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -33,6 +34,7 @@ EXPORTED_SYMBOLS = ("la_chunk_forward", "la_chunk_forward_ws", "la_chunk_forward
                     "la_decode_step_pro", "la_chunk_backward_norm_ws", "la_chunk_backward_norm_workspace_size",
                     "la_ema_scan", "la_chunk_state_ws", "la_chunk_state_workspace_size", "la_state_combine",
                     "la_delta_forward_ws", "la_delta_workspace_size", "la_delta_decode_step",
+                    "la_delta_backward_ws", "la_delta_backward_workspace_size",
                     "la_decode_step", "la_status_string", "la_device_error", "la_version")
 
 
@@ -118,6 +120,11 @@ def lib():
         L.la_delta_forward_ws.restype = i
         L.la_delta_workspace_size.argtypes = [i, i, i, i, i, i, i]
         L.la_delta_workspace_size.restype = sz
+        L.la_delta_backward_ws.argtypes = [vp, vp, vp, vp, ctypes.POINTER(_Decay), f, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                           i, i, i, i, i, i, i, vp, sz, vp]
+        L.la_delta_backward_ws.restype = i
+        L.la_delta_backward_workspace_size.argtypes = [i, i, i, i, i, i, i]
+        L.la_delta_backward_workspace_size.restype = sz
         L.la_delta_decode_step.argtypes = [vp, vp, vp, vp, ctypes.POINTER(_Decay), f, vp, vp, i, i, i, i, i, i, vp]
         L.la_delta_decode_step.restype = i
         L.la_status_string.argtypes = [i]
@@ -602,4 +609,5 @@ def device_error(device=None, stream=None):
     return code.value
 
 
-from .delta import delta_decode_step, delta_forward, delta_workspace_size  # noqa: E402
+from .delta import (delta_backward, delta_backward_workspace_size, delta_decode_step, delta_forward,  # noqa: E402
+                    delta_workspace_size)

@@ -73,6 +73,26 @@ cudaError_t launch_forward(const Plan& p, const Args& a, bool outputs) {
     return p.DKP == 32 ? forward_w32(p, a, outputs) : p.DKP == 64 ? forward_w64(p, a, outputs) : forward_w128(p, a, outputs);
 }
 
+// d log g of a head: its chunks' sums over every sequence, in a fixed order.
+__global__ void head_decay_kernel(const double* __restrict__ part, float* __restrict__ out, int B, int H, int n) {
+    const int h = blockIdx.x, lane = threadIdx.x;
+    double s = 0.0;
+    for (int b = 0; b < B; ++b)
+        for (int c = lane; c < n; c += 32) s += part[(static_cast<long long>(b) * H + h) * n + c];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) out[h] = static_cast<float>(s);
+}
+
+cudaError_t launch_backward(const Plan& p, const Args& a) {
+    cudaError_t e = p.DKP == 32 ? backward_w32(p, a) : p.DKP == 64 ? backward_w64(p, a) : backward_w128(p, a);
+    if (e == cudaSuccess && a.d_log_g && a.decay_kind == LA_DECAY_PER_HEAD) {
+        head_decay_kernel<<<a.H, 32, 0, a.stream>>>(p.dlog, a.d_log_g, a.B, a.H, p.n);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
 }  // namespace delta
 }  // namespace la
 
@@ -168,6 +188,58 @@ la_status la_delta_forward_ws(const void* q, const void* k, const void* v, const
     a.out = out;
     a.final_state = final_state;
     return delta::launch_forward(delta::make_plan(a, false, workspace), a, true) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+la_status la_delta_backward_ws(const void* q, const void* k, const void* v, const float* beta, const la_decay* decay,
+                               float q_scale, const float* init_state, const void* dy, const float* d_final_state, void* dq,
+                               void* dk, void* dv, float* dbeta, float* d_log_g, float* d_init_state, int B, int H, int Hk,
+                               int T, int Dk, int Dv, la_dtype dtype, void* workspace, size_t workspace_bytes,
+                               la_stream_t stream) {
+    la_status st = check_sizes(B, H, Hk, T, Dk, Dv, dtype);
+    if (st != LA_OK) return st;
+    delta::Args a = size_args(B, H, Hk, T, Dk, Dv, dtype);
+    const long long BH = static_cast<long long>(B) * H;
+    if (check_decay_for(decay, BH > 0 && T > 0, &a.decay_kind, &a.log_g) != LA_OK || !std::isfinite(q_scale))
+        return LA_ERR_INVALID_ARG;
+    const int kind = decay ? decay->kind : LA_DECAY_NONE;
+    if (d_log_g && (kind == LA_DECAY_NONE || !aligned4(d_log_g))) return LA_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(init_state), static_cast<const void*>(d_final_state),
+                          static_cast<const void*>(d_init_state)})
+        if (p && !aligned16(p)) return LA_ERR_INVALID_ARG;
+    if (BH > 0 && T > 0) {
+        for (const void* p : {q, k, v, dy, static_cast<const void*>(dq), static_cast<const void*>(dk), static_cast<const void*>(dv)})
+            if (!p || !aligned16(p)) return LA_ERR_INVALID_ARG;
+        if (!beta || !aligned4(beta) || !dbeta || !aligned4(dbeta)) return LA_ERR_INVALID_ARG;
+        if (!workspace || !aligned16(workspace) ||
+            workspace_bytes < la_delta_backward_workspace_size(B, H, Hk, T, Dk, Dv, dtype))
+            return LA_ERR_INVALID_ARG;
+    }
+    if (H == 0 || (BH == 0 && !(d_log_g && kind == LA_DECAY_PER_HEAD))) return LA_OK;
+    if (launch_fault_injected()) return LA_ERR_CUDA;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    if (T == 0 || BH == 0) {  // no token: the state's gradient passes through, a head's decay has none
+        cudaError_t e = copy_or_zero(BH ? d_init_state : nullptr, d_final_state, sizeof(float) * BH * Dk * Dv, a.stream);
+        if (e == cudaSuccess && kind == LA_DECAY_PER_HEAD) e = copy_or_zero(d_log_g, nullptr, sizeof(float) * H, a.stream);
+        return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+    }
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.beta = beta;
+    a.scale = q_scale;
+    a.init_state = init_state;
+    a.dy = dy;
+    a.d_final_state = d_final_state;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.dbeta = dbeta;
+    a.d_log_g = d_log_g;
+    a.d_init_state = d_init_state;
+    const delta::Plan p = delta::make_plan(a, true, workspace);
+    cudaError_t e = delta::launch_forward(p, a, false);
+    if (e == cudaSuccess) e = delta::launch_backward(p, a);
+    return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 
 la_status la_delta_decode_step(const void* q, const void* k, const void* v, const float* beta, const la_decay* decay,

@@ -1,0 +1,748 @@
+// la_delta_bwd.cuh - the gated delta rule's gradients.  After the forward's
+// kernels have left every chunk's incoming state S, errors E, P and
+// T = (I + A diag(beta))^-1 in the workspace:
+//
+//   reverse scan, dS the gradient of the state after the chunk (C tokens):
+//     dU = P^T dY + diag(e^(L_C - L)) K dS         U = diag(beta) E
+//     dR = T^T diag(beta) dU                       (= dV)
+//     dS <- e^(L_C) dS + scale Q^T diag(e^L) dY - K^T diag(e^L) dR
+//
+//   every chunk by itself, with M = dY E^T, N = dR E^T (both C x C) and
+//   Z = diag(e^(L_C - L)) E dS^T:
+//     dP' = scale e^(L_t - L_s) beta_s M_ts  (s <= t)
+//     dA' = -e^(L_t - L_s) beta_s N_ts       (s < t)
+//     dQ  = scale diag(e^L) dY S^T + dP' K
+//     dK  = [dA' K - diag(e^L) dR S^T] + [dP'^T Q + dA'^T K + diag(beta) Z] = dKrow + dKcol
+//     dbeta_s = k_s.Z_s + sum_t P_ts M_ts - sum_t A_ts N_ts
+//     dL_t = q_t.dQ_t + k_t.dKrow_t - k_t.dKcol_t, and <S_C, dS> for t = C,
+//     where <S_C, dS> = e^(L_C) <S, dS> + sum_s beta_s k_s.Z_s
+//     d log g_t = sum over the chunk's tokens from t on of dL
+//
+// dL's sums stay within a chunk: what later chunks contribute is all in
+// <S_C, dS>, so that no difference of long sums enters the decay's gradient.
+#pragma once
+#include "la_delta.cuh"
+#include "la_delta_internal.h"
+
+namespace la {
+namespace delta {
+namespace {
+
+// ---------------------------------------------------------------- reverse scan
+// Warp = 16 value columns, dS^T in its accumulators, as in the forward scan.
+template <int DKP, int NI, int NM, int NW, bool kF32>
+struct RevTiles {
+    static constexpr int kRow = DKP + kPad, kV = 16 * NW + kPad;
+    static constexpr int k = 0;
+    static constexpr int q = k + 2 * NI * C * kRow;
+    static constexpr int e = q + 2 * NI * C * kRow;
+    static constexpr int p = e + 2 * NM * C * kCS;
+    static constexpr int v = p + 2 * NM * C * kCS;
+    static constexpr int tok = v + (kF32 ? 0 : 2 * C * kV);
+    static constexpr int bytes = tok + 4 * kTok;
+    static constexpr int stages = 2 * bytes <= 227 * 1024 ? 2 : 1;
+};
+
+struct RevArgs {
+    Planes qp, kp;
+    const void* dy;
+    const __nv_bfloat16 *E, *P;
+    const float* tok;
+    const float* d_final;
+    float* d_init;
+    void* dv;
+    __nv_bfloat16 *dSst, *dRst;
+    float scale;
+    int H, Hk, T, Dk, Dv, DVP, n, vblocks;
+};
+
+template <int DKP, int NI, int NM, int NW, typename TIn>
+__global__ void __launch_bounds__(32 * NW) reverse_kernel(RevArgs a) {
+    constexpr bool kF32 = sizeof(TIn) == 4;
+    using Tl = RevTiles<DKP, NI, NM, NW, kF32>;
+    constexpr int kRow = Tl::kRow, kS = Tl::stages;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long bh = blockIdx.x / a.vblocks;
+    const int vb = blockIdx.x % a.vblocks * 16 * NW, v0 = vb + 16 * warp;
+    const bool active = v0 < a.Dv;
+    const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
+    const long long hk = static_cast<long long>(b) * a.Hk + h / (a.H / a.Hk);
+    const TIn* ysrc = static_cast<const TIn*>(a.dy) + bh * a.T * a.Dv;
+    const int tq = (lane & 3) * 2;
+
+    auto load = [&](int c) {  // c counts down
+        if (c >= 0) {
+            unsigned char* st = smem + static_cast<size_t>(c % kS) * Tl::bytes;
+            const long long cid = bh * a.n + c;
+            load_tile<DKP, NI>(reinterpret_cast<__nv_bfloat16*>(st + Tl::k), a.kp, hk, c * C, tid, 32 * NW);
+            load_tile<DKP, NI>(reinterpret_cast<__nv_bfloat16*>(st + Tl::q), a.qp, hk, c * C, tid, 32 * NW);
+            load_square(reinterpret_cast<__nv_bfloat16*>(st + Tl::e), a.E + cid * NM * C * C, NM * C, tid, 32 * NW);
+            load_square(reinterpret_cast<__nv_bfloat16*>(st + Tl::p), a.P + cid * NM * C * C, NM * C, tid, 32 * NW);
+            if constexpr (!kF32) {
+                constexpr int kVec = 2 * NW;
+                for (int i = tid; i < C * kVec; i += 32 * NW) {
+                    const int r = i / kVec, col = (i % kVec) * 8, t = c * C + r;
+                    const bool ok = t < a.T && vb + col < a.Dv;
+                    cp16(reinterpret_cast<__nv_bfloat16*>(st + Tl::v) + r * Tl::kV + col,
+                         ok ? ysrc + static_cast<long long>(t) * a.Dv + vb + col : ysrc, ok);
+                }
+            }
+            for (int i = tid; i < kTok / 4; i += 32 * NW) cp16(st + Tl::tok + 16 * i, a.tok + cid * kTok + 4 * i, true);
+        }
+        cp_commit();
+    };
+
+    float S[DKP / 8][4];
+    state_load<DKP>(S, a.d_final ? a.d_final + bh * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, v0, lane);
+    if constexpr (kS > 1) load(a.n - 1);
+
+    for (int c = a.n - 1; c >= 0; --c) {
+        if constexpr (kS > 1) {
+            load(c - 1);
+            cp_wait<1>();
+        } else {
+            load(c);
+            cp_wait<0>();
+        }
+        __syncthreads();
+        if (active) {
+            unsigned char* st = smem + static_cast<size_t>(c % kS) * Tl::bytes;
+            const __nv_bfloat16* kt = reinterpret_cast<const __nv_bfloat16*>(st + Tl::k);
+            const __nv_bfloat16* qt = reinterpret_cast<const __nv_bfloat16*>(st + Tl::q);
+            const __nv_bfloat16* et = reinterpret_cast<const __nv_bfloat16*>(st + Tl::e);
+            const __nv_bfloat16* pt = reinterpret_cast<const __nv_bfloat16*>(st + Tl::p);
+            const float* gam = reinterpret_cast<const float*>(st + Tl::tok);
+            const float* rest = gam + C;
+            const float* beta = gam + 2 * C;
+            const long long cid = bh * a.n + c;
+
+            // X = (K dS)^T, then dU = e^(L_C - L) X + (P^T dY)
+            float X[8][4] = {};
+#pragma unroll
+            for (int d = 0; d < DKP / 16; ++d) {
+                uint32_t s[NM][4];
+                split_frag<NM>(S[2 * d], S[2 * d + 1], s);
+                frag_to_planes<NM>(s, a.dSst + cid * NM * a.DVP * DKP, static_cast<long long>(a.DVP) * DKP, DKP, v0, 16 * d, lane);
+#pragma unroll
+                for (int nn = 0; nn < 4; ++nn)
+#pragma unroll
+                    for (int p = 0; p < NI; ++p) {
+                        uint32_t r[4];
+                        ldsm4(r, smem_addr(kt + (p * C + 16 * nn) * kRow + 16 * d + off_cols(lane, kRow)));
+                        mma_planes<NM, NM>(X[2 * nn], X[2 * nn + 1], s, p, r);
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 rs = *reinterpret_cast<const float2*>(rest + 8 * j + tq);
+                X[j][0] *= rs.x;
+                X[j][1] *= rs.y;
+                X[j][2] *= rs.x;
+                X[j][3] *= rs.y;
+            }
+            float Y[8][4];
+            if constexpr (kF32)
+                values_from_global(Y, ysrc, c * C, a.T, a.Dv, v0, lane);
+            else
+                values_from_tile(Y, reinterpret_cast<const __nv_bfloat16*>(st + Tl::v), Tl::kV, 16 * warp, lane);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {  // tokens t of P's rows; columns s <= t
+                uint32_t y[NI][4];
+                split_frag<NI>(Y[2 * m], Y[2 * m + 1], y);
+#pragma unroll
+                for (int nn = 0; nn <= m; ++nn)
+#pragma unroll
+                    for (int p = 0; p < NM; ++p) {
+                        uint32_t r[4];
+                        ldsm4t(r, smem_addr(pt + (p * C + 16 * m) * kCS + 16 * nn + off_rows(lane, kCS)));
+                        mma_planes<NI, NM>(X[2 * nn], X[2 * nn + 1], y, p, r);
+                    }
+            }
+            // dR = T^T diag(beta) dU
+            float R[8][4] = {};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 bt = *reinterpret_cast<const float2*>(beta + 8 * j + tq);
+                X[j][0] *= bt.x;
+                X[j][1] *= bt.y;
+                X[j][2] *= bt.x;
+                X[j][3] *= bt.y;
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                uint32_t x[NM][4];
+                split_frag<NM>(X[2 * m], X[2 * m + 1], x);
+#pragma unroll
+                for (int nn = 0; nn <= m; ++nn)
+#pragma unroll
+                    for (int p = 0; p < NM; ++p) {
+                        uint32_t r[4];
+                        ldsm4t(r, smem_addr(et + (p * C + 16 * m) * kCS + 16 * nn + off_rows(lane, kCS)));
+                        mma_planes<NM, NM>(R[2 * nn], R[2 * nn + 1], x, p, r);
+                    }
+            }
+            values_to_global(R, static_cast<TIn*>(a.dv) + bh * a.T * a.Dv, c * C, a.T, a.Dv, v0, lane);
+            uint32_t y[4][NM][4], w[4][NM][4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                split_frag<NM>(R[2 * m], R[2 * m + 1], w[m]);
+                frag_to_planes<NM>(w[m], a.dRst + cid * NM * a.DVP * C, static_cast<long long>(a.DVP) * C, C, v0, 16 * m, lane);
+#pragma unroll
+                for (int j = 2 * m; j < 2 * m + 2; ++j) {
+                    const float2 gm = *reinterpret_cast<const float2*>(gam + 8 * j + tq);
+                    R[j][0] *= -gm.x;
+                    R[j][1] *= -gm.y;
+                    R[j][2] *= -gm.x;
+                    R[j][3] *= -gm.y;
+                    Y[j][0] *= a.scale * gm.x;
+                    Y[j][1] *= a.scale * gm.y;
+                    Y[j][2] *= a.scale * gm.x;
+                    Y[j][3] *= a.scale * gm.y;
+                }
+                split_frag<NM>(R[2 * m], R[2 * m + 1], w[m]);
+                split_frag<NM>(Y[2 * m], Y[2 * m + 1], y[m]);
+            }
+            const float total = gam[C - 1];
+#pragma unroll
+            for (int d = 0; d < DKP / 16; ++d) {
+                float acc[2][4] = {};
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int p = 0; p < NI; ++p) {
+                        uint32_t r[4];
+                        ldsm4t(r, smem_addr(qt + (p * C + 16 * m) * kRow + 16 * d + off_rows(lane, kRow)));
+                        mma_planes<NM, NM>(acc[0], acc[1], y[m], p, r);
+                        ldsm4t(r, smem_addr(kt + (p * C + 16 * m) * kRow + 16 * d + off_rows(lane, kRow)));
+                        mma_planes<NM, NM>(acc[0], acc[1], w[m], p, r);
+                    }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) S[2 * d + j][i] = fmaf(total, S[2 * d + j][i], acc[j][i]);
+            }
+        }
+        __syncthreads();
+    }
+    if (active && a.d_init) state_store<DKP>(S, a.d_init + bh * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane);
+}
+
+// ---------------------------------------------------------------- gradients of a chunk
+// One block of 8 warps per (b, h, chunk): warp (r, c) = (w % 4, w / 4) holds rows
+// 16 r .. of every product and column half c.  The contraction over the value
+// columns streams 16 of them at a time (S, dS, E, dR, dY slices); then the
+// C x C gradients go through shared memory as A operands of the products with
+// K and Q.
+constexpr int kGradThreads = 256;
+constexpr int kVS = 16;  // value columns per streamed slice
+
+template <int DKP, int NI, int NM>
+struct GradTiles {
+    static constexpr int kRow = DKP + kPad, kY = kVS + kPad;
+    static constexpr int k = 0;
+    static constexpr int q = k + 2 * NI * C * kRow;
+    static constexpr int s = q + 2 * NI * C * kRow;         // [NM][kVS][kRow]
+    static constexpr int ds = s + 2 * NM * kVS * kRow;
+    static constexpr int e = ds + 2 * NM * kVS * kRow;      // [NM][kVS][kCS]
+    static constexpr int r = e + 2 * NM * kVS * kCS;
+    static constexpr int y = r + 2 * NM * kVS * kCS;        // [NI][C][kY]
+    static constexpr int slice = y + 2 * NI * C * kY - s;   // one streamed slice
+    static constexpr int stages = 2;
+    static constexpr int dp = s;                            // [NM][C][kCS], over the slices once they are done
+    static constexpr int da = dp + 2 * NM * C * kCS;
+    static constexpr int after = (2 * slice > 4 * NM * C * kCS ? 2 * slice : 4 * NM * C * kCS) + s;
+    static constexpr int tok = after;                       // kTok floats, L as doubles, sums
+    static constexpr int L = tok + 4 * kTok;
+    static constexpr int sums = L + 8 * C;                  // floats: [4][2][C] row sums, [4][C] column sums
+    static constexpr int bytes = sums + 4 * (8 * C + 4 * C + 64);
+};
+
+struct GradArgs {
+    Planes qp, kp;
+    const void* dy;
+    const __nv_bfloat16 *S, *dS, *E, *dR;
+    const float* tok;
+    const float* log_g;
+    int decay_kind;
+    float scale;
+    void *dq, *dk;         // final, where key heads are not shared
+    float *dqh, *dkh;      // else per value head
+    float* dbeta;
+    float* d_log_g;        // per step, or null
+    double* dlog;          // per chunk (per-head decay), or null
+    int H, Hk, T, Dk, Dv, DVP, n;
+};
+
+template <int DKP, int NI, int NM, typename TIn>
+__global__ void __launch_bounds__(kGradThreads) grad_kernel(GradArgs a) {
+    using Tl = GradTiles<DKP, NI, NM>;
+    constexpr int kRow = Tl::kRow, kY = Tl::kY, kHalf = DKP / 2, kJ = kHalf / 8;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __nv_bfloat16* kt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::k);
+    __nv_bfloat16* qt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::q);
+    float* tok = reinterpret_cast<float*>(smem + Tl::tok);
+    double* L = reinterpret_cast<double*>(smem + Tl::L);
+    float* rowsum = reinterpret_cast<float*>(smem + Tl::sums);  // [4 kinds][2 halves][C]
+    float* colsum = rowsum + 8 * C;                             // [4 row groups][C]
+    float* wsum = colsum + 4 * C;                               // per warp
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int wr = warp & 3, wc = warp >> 2;
+    const int g = lane >> 2, tq = (lane & 3) * 2;
+    const long long bh = blockIdx.x / a.n;
+    const int chunk = blockIdx.x % a.n, t0 = chunk * C;
+    const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
+    const long long hk = static_cast<long long>(b) * a.Hk + h / (a.H / a.Hk);
+    const long long cid = bh * a.n + chunk;
+    const TIn* ysrc = static_cast<const TIn*>(a.dy) + bh * a.T * a.Dv;
+    const __nv_bfloat16* Sg = a.S + cid * NM * a.DVP * DKP;
+    const __nv_bfloat16* dSg = a.dS + cid * NM * a.DVP * DKP;
+    const __nv_bfloat16* Eg = a.E + cid * NM * a.DVP * C;
+    const __nv_bfloat16* Rg = a.dR + cid * NM * a.DVP * C;
+
+    auto load = [&](int sl) {
+        if (sl * kVS < a.DVP) {
+            unsigned char* st = smem + (sl & 1) * Tl::slice;
+            const int v0 = sl * kVS;
+#pragma unroll
+            for (int p = 0; p < NM; ++p) {
+                for (int i = tid; i < kVS * (DKP / 8); i += kGradThreads) {
+                    const int r = i / (DKP / 8), col = i % (DKP / 8) * 8;
+                    const long long o = (static_cast<long long>(p) * a.DVP + v0 + r) * DKP + col;
+                    cp16(reinterpret_cast<__nv_bfloat16*>(st + Tl::s) + (p * kVS + r) * kRow + col, Sg + o, true);
+                    cp16(reinterpret_cast<__nv_bfloat16*>(st + Tl::ds) + (p * kVS + r) * kRow + col, dSg + o, true);
+                }
+                for (int i = tid; i < kVS * (C / 8); i += kGradThreads) {
+                    const int r = i / (C / 8), col = i % (C / 8) * 8;
+                    const long long o = (static_cast<long long>(p) * a.DVP + v0 + r) * C + col;
+                    cp16(reinterpret_cast<__nv_bfloat16*>(st + Tl::e) + (p * kVS + r) * kCS + col, Eg + o, true);
+                    cp16(reinterpret_cast<__nv_bfloat16*>(st + Tl::r) + (p * kVS + r) * kCS + col, Rg + o, true);
+                }
+            }
+            __nv_bfloat16* yt = reinterpret_cast<__nv_bfloat16*>(st + Tl::y);
+            if constexpr (sizeof(TIn) == 2) {
+                for (int i = tid; i < C * (kVS / 8); i += kGradThreads) {
+                    const int r = i / (kVS / 8), col = i % (kVS / 8) * 8, t = t0 + r;
+                    const bool ok = t < a.T && v0 + col < a.Dv;
+                    cp16(yt + r * kY + col, ok ? ysrc + static_cast<long long>(t) * a.Dv + v0 + col : ysrc, ok);
+                }
+            } else {
+                for (int i = tid; i < C * (kVS / 2); i += kGradThreads) {
+                    const int r = i / (kVS / 2), col = i % (kVS / 2) * 2, t = t0 + r;
+                    float x = 0.f, y = 0.f;
+                    if (t < a.T && v0 + col < a.Dv) x = ysrc[static_cast<long long>(t) * a.Dv + v0 + col];
+                    if (t < a.T && v0 + col + 1 < a.Dv) y = ysrc[static_cast<long long>(t) * a.Dv + v0 + col + 1];
+                    uint32_t p[NI];
+                    split2<NI>(x, y, p);
+#pragma unroll
+                    for (int j = 0; j < NI; ++j) *reinterpret_cast<uint32_t*>(yt + (j * C + r) * kY + col) = p[j];
+                }
+            }
+        }
+        cp_commit();
+    };
+
+    load_tile<DKP, NI>(kt, a.kp, hk, t0, tid, kGradThreads);
+    load_tile<DKP, NI>(qt, a.qp, hk, t0, tid, kGradThreads);
+    for (int i = tid; i < kTok / 4; i += kGradThreads) cp16(tok + 4 * i, a.tok + cid * kTok + 4 * i, true);
+    load(0);
+    if (warp == 0) {  // as in prep_kernel
+        double x[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + 2 * lane + i;
+            float lg = 0.f;
+            if (t < a.T) {
+                if (a.decay_kind == LA_DECAY_PER_HEAD) lg = a.log_g[h];
+                if (a.decay_kind == LA_DECAY_PER_STEP) lg = a.log_g[bh * a.T + t];
+            }
+            x[i] = lg < kLogFloor ? kLogFloor : lg;
+        }
+        double s = x[0] + x[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        L[2 * lane + 1] = s;
+        L[2 * lane] = s - x[1];
+    }
+
+    float M[4][4] = {}, N[4][4] = {};
+    float dQ[kJ][4] = {}, Kr[kJ][4] = {}, Z[kJ][4] = {};
+    float inner = 0.f;  // <S, dS>
+    const int slices = a.DVP / kVS;
+    for (int sl = 0; sl < slices; ++sl) {
+        load(sl + 1);
+        cp_wait<1>();
+        __syncthreads();
+        unsigned char* st = smem + (sl & 1) * Tl::slice;
+        const __nv_bfloat16* s_t = reinterpret_cast<const __nv_bfloat16*>(st + Tl::s);
+        const __nv_bfloat16* ds_t = reinterpret_cast<const __nv_bfloat16*>(st + Tl::ds);
+        const __nv_bfloat16* e_t = reinterpret_cast<const __nv_bfloat16*>(st + Tl::e);
+        const __nv_bfloat16* r_t = reinterpret_cast<const __nv_bfloat16*>(st + Tl::r);
+        const __nv_bfloat16* y_t = reinterpret_cast<const __nv_bfloat16*>(st + Tl::y);
+        uint32_t ay[NI][4], ae[NM][4], ar[NM][4];
+#pragma unroll
+        for (int p = 0; p < NI; ++p) ldsm4(ay[p], smem_addr(y_t + (p * C + 16 * wr) * kY + off_rows(lane, kY)));
+#pragma unroll
+        for (int p = 0; p < NM; ++p) {
+            ldsm4t(ae[p], smem_addr(e_t + p * kVS * kCS + 16 * wr + off_cols(lane, kCS)));
+            ldsm4t(ar[p], smem_addr(r_t + p * kVS * kCS + 16 * wr + off_cols(lane, kCS)));
+        }
+#pragma unroll
+        for (int nn = 0; nn < 2; ++nn)
+            if (32 * wc + 16 * nn <= 16 * wr) {
+#pragma unroll
+                for (int p = 0; p < NM; ++p) {
+                    uint32_t r[4];
+                    ldsm4t(r, smem_addr(e_t + p * kVS * kCS + 32 * wc + 16 * nn + off_rows(lane, kCS)));
+                    mma_planes<NI, NM>(M[2 * nn], M[2 * nn + 1], ay, p, r);
+                    mma_planes<NM, NM>(N[2 * nn], N[2 * nn + 1], ar, p, r);
+                }
+            }
+#pragma unroll
+        for (int d = 0; d < kHalf / 16; ++d)
+#pragma unroll
+            for (int p = 0; p < NM; ++p) {
+                uint32_t r[4];
+                ldsm4t(r, smem_addr(s_t + p * kVS * kRow + kHalf * wc + 16 * d + off_rows(lane, kRow)));
+                mma_planes<NI, NM>(dQ[2 * d], dQ[2 * d + 1], ay, p, r);
+                mma_planes<NM, NM>(Kr[2 * d], Kr[2 * d + 1], ar, p, r);
+                ldsm4t(r, smem_addr(ds_t + p * kVS * kRow + kHalf * wc + 16 * d + off_rows(lane, kRow)));
+                mma_planes<NM, NM>(Z[2 * d], Z[2 * d + 1], ae, p, r);
+            }
+        for (int i = tid; i < kVS * (DKP / 2); i += kGradThreads) {
+            const int r = i / (DKP / 2), col = i % (DKP / 2) * 2;
+            float x0 = 0.f, x1 = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+            for (int p = NM - 1; p >= 0; --p) {
+                const uint32_t u = *reinterpret_cast<const uint32_t*>(s_t + (p * kVS + r) * kRow + col);
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(ds_t + (p * kVS + r) * kRow + col);
+                x0 += low_of(u);
+                x1 += high_of(u);
+                y0 += low_of(w);
+                y1 += high_of(w);
+            }
+            inner = fmaf(x0, y0, fmaf(x1, y1, inner));
+        }
+        __syncthreads();
+    }
+    cp_wait<0>();
+
+    // The chunk's scores again (exact operands), in the layout of M and N.
+    const float* gam = tok;
+    const float* rest = tok + C;
+    const float* beta = tok + 2 * C;
+    float qk[4][4] = {}, kk[4][4] = {};
+#pragma unroll
+    for (int d = 0; d < DKP / 16; ++d) {
+        uint32_t aq[NI][4], ak[NI][4];
+#pragma unroll
+        for (int p = 0; p < NI; ++p) {
+            ldsm4(aq[p], smem_addr(qt + (p * C + 16 * wr) * kRow + 16 * d + off_rows(lane, kRow)));
+            ldsm4(ak[p], smem_addr(kt + (p * C + 16 * wr) * kRow + 16 * d + off_rows(lane, kRow)));
+        }
+#pragma unroll
+        for (int nn = 0; nn < 2; ++nn)
+            if (32 * wc + 16 * nn <= 16 * wr) {
+#pragma unroll
+                for (int p = 0; p < NI; ++p) {
+                    uint32_t r[4];
+                    ldsm4(r, smem_addr(kt + (p * C + 32 * wc + 16 * nn) * kRow + 16 * d + off_cols(lane, kRow)));
+                    mma_planes<NI, NM>(qk[2 * nn], qk[2 * nn + 1], aq, p, r);
+                    mma_planes<NI, NM>(kk[2 * nn], kk[2 * nn + 1], ak, p, r);
+                }
+            }
+    }
+    // dP', dA' as planes in shared memory; dbeta's column sums.
+    __nv_bfloat16* dpt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::dp);
+    __nv_bfloat16* dat = reinterpret_cast<__nv_bfloat16*>(smem + Tl::da);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float cs[2] = {0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t = 16 * wr + g + 8 * r;
+            float p2[2], a2[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int s = 32 * wc + 8 * j + tq + x;
+                const float d = s <= t ? expf(static_cast<float>(L[t] - L[s])) : 0.f;
+                const float m = a.scale * d * M[j][2 * r + x], w = s < t ? -d * N[j][2 * r + x] : 0.f;
+                cs[x] += (s <= t ? m * qk[j][2 * r + x] : 0.f) + (s < t ? w * kk[j][2 * r + x] : 0.f);
+                p2[x] = s <= t ? m * beta[s] : 0.f;
+                a2[x] = w * beta[s];
+            }
+            uint32_t pl[NM];
+            split2<NM>(p2[0], p2[1], pl);
+#pragma unroll
+            for (int p = 0; p < NM; ++p) *reinterpret_cast<uint32_t*>(dpt + (p * C + t) * kCS + 32 * wc + 8 * j + tq) = pl[p];
+            split2<NM>(a2[0], a2[1], pl);
+#pragma unroll
+            for (int p = 0; p < NM; ++p) *reinterpret_cast<uint32_t*>(dat + (p * C + t) * kCS + 32 * wc + 8 * j + tq) = pl[p];
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) cs[x] += __shfl_xor_sync(0xffffffffu, cs[x], o);
+            if (g == 0) colsum[wr * C + 32 * wc + 8 * j + tq + x] = cs[x];
+        }
+    }
+    __syncthreads();
+
+    // Row factors of the parts from the states, then the products with K and Q.
+    float Kc[kJ][4];
+    float zk[2] = {0.f, 0.f};  // k_t . Z_t over this warp's columns
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int t = 16 * wr + g + 8 * r;
+        const float gm = gam[t], rs = rest[t], bt = beta[t];
+#pragma unroll
+        for (int j = 0; j < kJ; ++j)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int col = kHalf * wc + 8 * j + tq + x;
+                float kv = 0.f;
+#pragma unroll
+                for (int p = NI - 1; p >= 0; --p) kv += __bfloat162float(kt[(p * C + t) * kRow + col]);
+                dQ[j][2 * r + x] *= a.scale * gm;
+                Kr[j][2 * r + x] *= -gm;
+                const float z = rs * Z[j][2 * r + x];
+                zk[r] = fmaf(kv, z, zk[r]);
+                Kc[j][2 * r + x] = bt * z;
+            }
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        uint32_t x[NM][4], y[NM][4], xt[NM][4], yt[NM][4];
+        const bool below = m <= wr, above = m >= wr;  // blocks of dP'[rows, 16 m] and dP'[16 m, rows]^T
+#pragma unroll
+        for (int p = 0; p < NM; ++p) {
+            if (below) {
+                ldsm4(x[p], smem_addr(dpt + (p * C + 16 * wr) * kCS + 16 * m + off_rows(lane, kCS)));
+                ldsm4(y[p], smem_addr(dat + (p * C + 16 * wr) * kCS + 16 * m + off_rows(lane, kCS)));
+            }
+            if (above) {
+                ldsm4t(xt[p], smem_addr(dpt + (p * C + 16 * m) * kCS + 16 * wr + off_cols(lane, kCS)));
+                ldsm4t(yt[p], smem_addr(dat + (p * C + 16 * m) * kCS + 16 * wr + off_cols(lane, kCS)));
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < kHalf / 16; ++d)
+#pragma unroll
+            for (int p = 0; p < NI; ++p) {
+                uint32_t r[4];
+                ldsm4t(r, smem_addr(kt + (p * C + 16 * m) * kRow + kHalf * wc + 16 * d + off_rows(lane, kRow)));
+                if (below) {
+                    mma_planes<NM, NM>(dQ[2 * d], dQ[2 * d + 1], x, p, r);
+                    mma_planes<NM, NM>(Kr[2 * d], Kr[2 * d + 1], y, p, r);
+                }
+                if (above) {
+                    mma_planes<NM, NM>(Kc[2 * d], Kc[2 * d + 1], yt, p, r);
+                    ldsm4t(r, smem_addr(qt + (p * C + 16 * m) * kRow + kHalf * wc + 16 * d + off_rows(lane, kRow)));
+                    mma_planes<NM, NM>(Kc[2 * d], Kc[2 * d + 1], xt, p, r);
+                }
+            }
+    }
+
+    // Outputs and the row sums of dL.
+    const long long base = a.dqh ? bh : hk;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int t = 16 * wr + g + 8 * r;
+        float dl = 0.f;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+            const int col = kHalf * wc + 8 * j + tq;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float kv = 0.f, qv = 0.f;
+#pragma unroll
+                for (int p = NI - 1; p >= 0; --p) {
+                    kv += __bfloat162float(kt[(p * C + t) * kRow + col + x]);
+                    qv += __bfloat162float(qt[(p * C + t) * kRow + col + x]);
+                }
+                dl = fmaf(qv, dQ[j][2 * r + x], dl);
+                dl = fmaf(kv, Kr[j][2 * r + x] - Kc[j][2 * r + x], dl);
+            }
+            if (t0 + t < a.T) {
+                const long long o = (base * a.T + t0 + t) * a.Dk + col;
+                const float q0 = dQ[j][2 * r], q1 = dQ[j][2 * r + 1];
+                const float k0 = Kr[j][2 * r] + Kc[j][2 * r], k1 = Kr[j][2 * r + 1] + Kc[j][2 * r + 1];
+                if (a.dqh || sizeof(TIn) == 4) {
+                    float* dq = a.dqh ? a.dqh : static_cast<float*>(a.dq);
+                    float* dk = a.dkh ? a.dkh : static_cast<float*>(a.dk);
+                    if (col < a.Dk) {
+                        dq[o] = q0;
+                        dk[o] = k0;
+                    }
+                    if (col + 1 < a.Dk) {
+                        dq[o + 1] = q1;
+                        dk[o + 1] = k1;
+                    }
+                } else if (col < a.Dk) {
+                    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.dq) + o) = pack(q0, q1);
+                    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.dk) + o) = pack(k0, k1);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            dl += __shfl_xor_sync(0xffffffffu, dl, o);
+            zk[r] += __shfl_xor_sync(0xffffffffu, zk[r], o);
+        }
+        if ((lane & 3) == 0) {
+            rowsum[(0 + wc) * C + t] = dl;
+            rowsum[(2 + wc) * C + t] = zk[r];
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
+    if (lane == 0) wsum[warp] = inner;
+    __syncthreads();
+
+    if (warp == 0) {
+        float in = 0.f;
+        for (int i = 0; i < kGradThreads / 32; ++i) in += wsum[i];
+        double end = static_cast<double>(gam[C - 1]) * in, dl[2];
+        float cz = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            const float z = rowsum[2 * C + t] + rowsum[3 * C + t];
+            float db = z;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) db += colsum[r * C + t];
+            if (t0 + t < a.T) a.dbeta[bh * a.T + t0 + t] = db;
+            cz = fmaf(beta[t], z, cz);
+            dl[i] = static_cast<double>(rowsum[t]) + rowsum[C + t];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) cz += __shfl_xor_sync(0xffffffffu, cz, o);
+        end += cz;
+        double s = dl[0] + dl[1];  // suffix sums: this lane's two tokens and all after them
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_down_sync(0xffffffffu, s, o);
+            if (lane + o < 32) s += y;
+        }
+        const double d0 = s + end, d1 = s - dl[0] + end;
+        const int t = t0 + 2 * lane;
+        if (a.d_log_g) {
+            if (t < a.T) a.d_log_g[bh * a.T + t] = static_cast<float>(d0);
+            if (t + 1 < a.T) a.d_log_g[bh * a.T + t + 1] = static_cast<float>(d1);
+        }
+        if (a.dlog) {
+            double c = (t < a.T ? d0 : 0.0) + (t + 1 < a.T ? d1 : 0.0);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+            if (lane == 0) a.dlog[cid] = c;
+        }
+    }
+}
+
+// Sum over the value heads of a key head, in their order.
+template <typename TOut>
+__global__ void group_sum_kernel(const float* __restrict__ x, TOut* __restrict__ out, int rep, long long inner, long long total) {
+    const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i >= total) return;
+    const long long key = i / inner, at = i % inner;
+    float s = 0.f;
+    for (int r = 0; r < rep; ++r) s += x[(key * rep + r) * inner + at];
+    if constexpr (sizeof(TOut) == 2)
+        out[i] = __float2bfloat16_rn(s);
+    else
+        out[i] = s;
+}
+
+template <int DKP, int NI, int NM, int NW, typename TIn>
+cudaError_t reverse_run(const Plan& p, const Args& a, RevArgs r) {
+    auto kern = reverse_kernel<DKP, NI, NM, NW, TIn>;
+    using Tl = RevTiles<DKP, NI, NM, NW, sizeof(TIn) == 4>;
+    static_assert(Tl::stages * Tl::bytes <= 227 * 1024, "the reverse scan's tiles have to fit an SM");
+    constexpr int smem = Tl::stages * Tl::bytes;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    r.vblocks = (a.Dv + 16 * NW - 1) / (16 * NW);
+    kern<<<static_cast<unsigned>(p.BH * r.vblocks), 32 * NW, smem, a.stream>>>(r);
+    return cudaGetLastError();
+}
+
+template <int DKP, int NI, int NM, typename TIn>
+cudaError_t backward_typed(const Plan& p, const Args& a) {
+    RevArgs r{};
+    r.qp = p.q;
+    r.kp = p.k;
+    r.dy = a.dy;
+    r.E = p.E;
+    r.P = p.P;
+    r.tok = p.tok;
+    r.d_final = a.d_final_state;
+    r.d_init = a.d_init_state;
+    r.dv = a.dv;
+    r.dSst = p.dS;
+    r.dRst = p.dR;
+    r.scale = a.scale;
+    r.H = a.H;
+    r.Hk = a.Hk;
+    r.T = a.T;
+    r.Dk = a.Dk;
+    r.Dv = a.Dv;
+    r.DVP = p.DVP;
+    r.n = p.n;
+    cudaError_t e = p.warps == 1   ? reverse_run<DKP, NI, NM, 1, TIn>(p, a, r)
+                    : p.warps == 2 ? reverse_run<DKP, NI, NM, 2, TIn>(p, a, r)
+                                   : reverse_run<DKP, NI, NM, 4, TIn>(p, a, r);
+    if (e != cudaSuccess) return e;
+
+    GradArgs g{};
+    g.qp = p.q;
+    g.kp = p.k;
+    g.dy = a.dy;
+    g.S = p.S;
+    g.dS = p.dS;
+    g.E = p.Er;
+    g.dR = p.dR;
+    g.tok = p.tok;
+    g.log_g = a.log_g;
+    g.decay_kind = a.decay_kind;
+    g.scale = a.scale;
+    g.dq = a.dq;
+    g.dk = a.dk;
+    g.dqh = p.dqh;
+    g.dkh = p.dkh;
+    g.dbeta = a.dbeta;
+    g.d_log_g = a.decay_kind == LA_DECAY_PER_STEP ? a.d_log_g : nullptr;
+    g.dlog = a.decay_kind == LA_DECAY_PER_HEAD && a.d_log_g ? p.dlog : nullptr;
+    g.H = a.H;
+    g.Hk = a.Hk;
+    g.T = a.T;
+    g.Dk = a.Dk;
+    g.Dv = a.Dv;
+    g.DVP = p.DVP;
+    g.n = p.n;
+    auto kern = grad_kernel<DKP, NI, NM, TIn>;
+    using Tl = GradTiles<DKP, NI, NM>;
+    static_assert(Tl::bytes <= 227 * 1024, "the gradient kernel's tiles have to fit an SM");
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tl::bytes)) != cudaSuccess) return e;
+    kern<<<static_cast<unsigned>(p.BH * p.n), kGradThreads, Tl::bytes, a.stream>>>(g);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (p.dqh) {
+        const long long inner = static_cast<long long>(a.T) * a.Dk, total = static_cast<long long>(a.B) * a.Hk * inner;
+        const unsigned grid = static_cast<unsigned>((total + 255) / 256);
+        group_sum_kernel<<<grid, 256, 0, a.stream>>>(p.dqh, static_cast<TIn*>(a.dq), a.H / a.Hk, inner, total);
+        group_sum_kernel<<<grid, 256, 0, a.stream>>>(p.dkh, static_cast<TIn*>(a.dk), a.H / a.Hk, inner, total);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+template <int DKP>
+cudaError_t backward_width(const Plan& p, const Args& a) {
+    return a.dtype == LA_F32 ? backward_typed<DKP, 3, 3, float>(p, a) : backward_typed<DKP, 1, 2, __nv_bfloat16>(p, a);
+}
+
+}  // namespace
+}  // namespace delta
+}  // namespace la

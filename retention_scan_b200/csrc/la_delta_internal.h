@@ -102,6 +102,9 @@ cudaError_t forward_w64(const Plan& p, const Args& a, bool outputs);
 cudaError_t forward_w128(const Plan& p, const Args& a, bool outputs);
 // After launch_forward(..., false): the reverse scan and the gradients.
 cudaError_t launch_backward(const Plan& p, const Args& a);
+cudaError_t backward_w32(const Plan& p, const Args& a);
+cudaError_t backward_w64(const Plan& p, const Args& a);
+cudaError_t backward_w128(const Plan& p, const Args& a);
 
 struct DecodeArgs {
     const void* q;

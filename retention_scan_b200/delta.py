@@ -26,6 +26,10 @@ def _heads(q, k, v, beta, decay_kind, log_g, token):
     if H and (Hk == 0 or H % Hk):
         raise ValueError(f"v has {H} heads, which is not a multiple of q's {Hk}")
     _dtype_code(q.dtype)
+    if beta is None:
+        raise ValueError("beta is required")
+    if decay_kind != DECAY_NONE and log_g is None:
+        raise ValueError("log_g is required for a per-head or per-step decay")
     _need(q, "q", (B, Hk, *T, Dk), q.dtype, q.device)
     _need(k, "k", (B, Hk, *T, Dk), q.dtype, q.device)
     _need(v, "v", (B, H, *T, Dv), q.dtype, q.device)
@@ -82,6 +86,59 @@ def delta_forward(q, k, v, beta, decay_kind=DECAY_NONE, log_g=None, init_state=N
             _ptr(init_state), _ptr(out), _ptr(final_state), B, H, Hk, T, Dk, Dv, _dtype_code(q.dtype),
             _ptr(workspace), workspace.numel(), _stream(stream, dev)))
     return out, final_state
+
+
+def delta_backward_workspace_size(B, H, T, Dk, Dv, dtype=torch.bfloat16, key_heads=None):
+    """Scratch bytes delta_backward needs (la_delta_backward_workspace_size)."""
+    return int(lib().la_delta_backward_workspace_size(B, H, key_heads or H, T, Dk, Dv, _dtype_code(dtype)))
+
+
+def delta_backward(q, k, v, beta, dy, decay_kind=DECAY_NONE, log_g=None, init_state=None, d_final_state=None,
+                   q_scale=1.0, need_log_g=True, need_init_state=True, stream=None, workspace=None, out=None):
+    """Gradients of delta_forward (la_delta_backward_ws) for the loss
+    sum(dy * y) + sum(d_final_state * final_state).
+
+    Arguments as delta_forward, plus dy [B,H,T,Dv] in the inputs' dtype and
+    d_final_state [B,H,Dk,Dv] fp32 or None.  Returns (dq, dk, dv, dbeta,
+    d_log_g, d_init_state): dq, dk (summed over shared heads) and dv in the
+    input dtype, dbeta fp32, d_log_g fp32 with log_g's shape (None without a
+    decay or need_log_g=False), d_init_state fp32 (None with
+    need_init_state=False).  workspace: None, or a CUDA uint8 tensor of at
+    least delta_backward_workspace_size(...) bytes.  out: None, or a tuple of
+    the six outputs preallocated (the last two may be None to skip them)."""
+    B, H, Hk, T, Dk, Dv = _heads(q, k, v, beta, decay_kind, log_g, token=False)
+    dev = q.device
+    if dy is None:
+        raise ValueError("dy is required")
+    _need(dy, "dy", (B, H, T, Dv), q.dtype, dev)
+    _need(init_state, "init_state", (B, H, Dk, Dv), torch.float32, dev)
+    _need(d_final_state, "d_final_state", (B, H, Dk, Dv), torch.float32, dev)
+    if out is None:
+        dq, dk, dv, dbeta = (torch.empty_like(x) for x in (q, k, v, beta))
+        d_log_g = torch.empty_like(log_g) if decay_kind != DECAY_NONE and need_log_g else None
+        d_init = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev) if need_init_state else None
+    else:
+        dq, dk, dv, dbeta, d_log_g, d_init = out
+        if any(x is None for x in (dq, dk, dv, dbeta)):
+            raise ValueError("out: dq, dk, dv and dbeta are always written")
+        if d_log_g is not None and decay_kind == DECAY_NONE:
+            raise ValueError("d_log_g: there is no decay")
+        _need(dq, "dq", (B, Hk, T, Dk), q.dtype, dev)
+        _need(dk, "dk", (B, Hk, T, Dk), q.dtype, dev)
+        _need(dv, "dv", (B, H, T, Dv), q.dtype, dev)
+        _need(dbeta, "dbeta", (B, H, T), torch.float32, dev)
+        if d_log_g is not None:
+            _need(d_log_g, "d_log_g", tuple(log_g.shape), torch.float32, dev)
+        _need(d_init, "d_init_state", (B, H, Dk, Dv), torch.float32, dev)
+    d = _decay(decay_kind, log_g)
+    with torch.cuda.device(dev):
+        workspace = _scratch(workspace, delta_backward_workspace_size(B, H, T, Dk, Dv, q.dtype, Hk), dev, stream)
+        _check(lib().la_delta_backward_ws(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(beta), ctypes.byref(d) if d is not None else None, float(q_scale),
+            _ptr(init_state), _ptr(dy), _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbeta), _ptr(d_log_g),
+            _ptr(d_init), B, H, Hk, T, Dk, Dv, _dtype_code(q.dtype), _ptr(workspace), workspace.numel(),
+            _stream(stream, dev)))
+    return dq, dk, dv, dbeta, d_log_g, d_init
 
 
 def delta_decode_step(q, k, v, beta, state, decay_kind=DECAY_NONE, log_g=None, q_scale=1.0, out=None, stream=None):

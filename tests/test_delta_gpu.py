@@ -192,6 +192,155 @@ def test_forward_on_another_stream_and_in_a_graph():
         assert torch.equal(out, ye) and torch.equal(fin, Se)
 
 
+# ------------------------------------------------------------------ gradients
+# Bars: dq, dk, dv in bf16 carry their own rounding, 2^-8, next to fp32 sums of split
+# operands.  An fp32 gradient of bf16 inputs goes through the forward's four split operands
+# and the reverse scan's four: twice the states' bar.  d log g and dbeta are what is left of
+# sums whose terms are larger than they are (k.dk of the rows that push a state and the rows
+# that draw on it); they are held to the same bar against the 2-norm of those terms, which the
+# oracle's own dq and dk give.  fp32 inputs: likewise, twice the forward's bar.
+def check_backward(args, kind, scale=0.25, dtype=torch.bfloat16, d_final=True, seed=0):
+    q, k, v, beta, lg, S0 = args
+    g = torch.Generator().manual_seed(seed + 100)
+    dy = torch.randn(v.shape, generator=g).to(dtype)
+    B, H, Dk, Dv = v.shape[0], v.shape[1], q.shape[-1], v.shape[-1]
+    dS = 0.3 * torch.randn(B, H, Dk, Dv, generator=g) if d_final else None
+    got = la().delta_backward(*dev(q, k, v, beta, dy), kind, *dev(lg, S0, dS), q_scale=scale)
+    want = oracle.delta_backward(q, k, v, beta, dy, kind, lg, S0, dS, scale)
+    low = 2 * (BAR_STATE if dtype == torch.bfloat16 else BAR32)
+    own = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    for name, x, r in zip(("dq", "dk", "dv"), got[:3], want[:3]):
+        assert slice_err(x, r) <= own + low, name
+    if S0 is not None:
+        assert slice_err(got[5], want[5]) <= low, "d_init_state"
+    rep = H // q.shape[1]
+    f64 = lambda x: np.asarray(x.double().numpy()) if hasattr(x, "double") else np.asarray(x)  # noqa: E731
+    qd = np.repeat((f64(q) * want[0]).sum(-1), rep, 1)
+    kd = np.repeat(np.linalg.norm(f64(k), axis=-1) * np.linalg.norm(want[1], axis=-1), rep, 1)
+    terms = np.abs(qd) + kd + np.linalg.norm(f64(v), axis=-1) * np.linalg.norm(want[2], axis=-1)
+    size = np.sqrt((terms ** 2).sum(-1)) + 1e-30
+    db = got[3].cpu().double().numpy()
+    assert (np.linalg.norm(db - want[3], axis=-1) <= low * (size + np.linalg.norm(want[3], axis=-1))).all(), "dbeta"
+    if kind == 2:
+        dl = got[4].cpu().double().numpy()
+        ends = np.linalg.norm(want[4], axis=-1)
+        assert (np.linalg.norm(dl - want[4], axis=-1) <= low * (size + ends)).all(), "d_log_g"
+    elif kind == 1:
+        dl = got[4].cpu().double().numpy()
+        assert (np.abs(dl - want[4]) <= low * (terms.sum((0, 2)) + np.abs(want[4]))).all(), "d_log_g per head"
+    else:
+        assert got[4] is None
+    return dy, dS, got
+
+
+@pytest.mark.parametrize("T", [1, 2, 63, 64, 65, 130, 257])
+@pytest.mark.parametrize("kind", [0, 1, 2])
+def test_backward_lengths(T, kind):
+    check_backward(make(2, 2, 2, T, 64, 64, kind=kind, seed=T), kind)
+
+
+@pytest.mark.parametrize("Dk,Dv", [(16, 16), (32, 48), (48, 32), (64, 112), (80, 64), (96, 80), (112, 16), (128, 128)])
+def test_backward_widths(Dk, Dv):
+    check_backward(make(1, 3, 3, 150, Dk, Dv, seed=Dk + Dv), 2)
+
+
+@pytest.mark.parametrize("Dk,Dv", [(1, 1), (3, 127), (17, 33), (40, 7), (64, 64), (100, 60), (128, 128)])
+@pytest.mark.parametrize("T", [1, 70, 140])
+def test_backward_fp32(Dk, Dv, T):
+    check_backward(make(1, 2, 1, T, Dk, Dv, torch.float32, seed=Dk), 2, dtype=torch.float32)
+
+
+@pytest.mark.parametrize("B,H,Hk", [(1, 1, 1), (2, 6, 2), (3, 8, 1), (1, 4, 4), (40, 4, 2), (150, 2, 1)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_backward_head_layouts(B, H, Hk, dtype):
+    check_backward(make(B, H, Hk, 100, 32, 64, dtype, seed=B + H), 2, dtype=dtype)
+
+
+def test_backward_without_states_and_with_correlated_keys():
+    check_backward(make(2, 2, 2, 200, 64, 64, init=False, correlated=2.0, seed=5), 2, d_final=False)
+    check_backward(make(2, 2, 2, 200, 64, 64, kind=1, init=False, seed=6), 1, d_final=False)
+
+
+def test_backward_of_zero_beta_and_hard_resets():
+    # beta = 0 writes nothing, but its gradient is the error it would have written
+    q, k, v, beta, lg, S0 = make(1, 2, 2, 150, 64, 64, seed=9)
+    beta[:, :, ::3] = 0
+    lg[:, :, [0, 70, 71, 128]] = -1e30
+    check_backward((q, k, v, beta, lg, S0), 2)
+
+
+def test_backward_against_differences():
+    # fp32, along a random direction of every input, by central differences of the library's forward
+    q, k, v, beta, lg, S0 = make(1, 2, 1, 75, 24, 20, torch.float32, seed=21)
+    dy, dS, got = check_backward((q, k, v, beta, lg, S0), 2, dtype=torch.float32, seed=3)
+    g = torch.Generator().manual_seed(77)
+    leaves = [q, k, v, beta, lg, S0]
+
+    def loss(xs):
+        y, S = oracle.delta_forward(*xs[:4], 2, xs[4], xs[5], 0.25)
+        return float((y * dy.double().numpy()).sum() + (S * dS.double().numpy()).sum())
+    for i, x in enumerate(leaves):
+        d = torch.randn(x.shape, generator=g, dtype=torch.float64)
+        h = 1e-5
+        up = [t.double() + h * d if j == i else t.double() for j, t in enumerate(leaves)]
+        dn = [t.double() - h * d if j == i else t.double() for j, t in enumerate(leaves)]
+        slope = (loss(up) - loss(dn)) / (2 * h)
+        mine = float((got[i].cpu().double() * d).sum())
+        size = float(got[i].cpu().double().norm() * d.norm())
+        # differences are off by h^2 and the forward's 64-bit noise / h; fp32 gradients by 2 BAR32
+        assert abs(mine - slope) <= 2 * BAR32 * size + 1e-7 * size + 1e-8, i
+
+
+def test_backward_padding_shared_outputs_and_determinism():
+    q, k, v, beta, lg, S0 = dev(*make(2, 4, 2, 200, 64, 64, seed=3))
+    n = 137
+    beta[:, :, n:] = 0
+    lg[:, :, n:] = 0
+    dy = torch.randn(v.shape, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    dy[:, :, n:] = 0
+    got = la().delta_backward(q, k, v, beta, dy, 2, lg, S0)
+    cut = [x[:, :, :n].contiguous() for x in (q, k, v, beta, dy)]
+    want = la().delta_backward(*cut, 2, lg[:, :, :n].contiguous(), S0)
+    for a, b in zip(got[:3], want[:3]):
+        assert torch.equal(a[:, :, :n], b)
+    assert torch.equal(got[3][:, :, :n], want[3]) and torch.equal(got[5], want[5])
+    assert not got[0][:, :, n:].any() and not got[2][:, :, n:].any()
+    ws = torch.full((la().delta_backward_workspace_size(2, 4, 200, 64, 64, key_heads=2),), 255, dtype=torch.uint8, device="cuda")
+    outs = tuple(torch.full_like(x, float("nan")) for x in got)
+    again = la().delta_backward(q, k, v, beta, dy, 2, lg, S0, workspace=ws, out=outs)
+    for a, b, o in zip(again, got, outs):
+        assert a is o and torch.equal(a, b)
+    some = la().delta_backward(q, k, v, beta, dy, 2, lg, S0, need_log_g=False, need_init_state=False)
+    assert some[4] is None and some[5] is None and torch.equal(some[1], got[1])
+
+
+def test_backward_empty():
+    q, k, v, beta, lg, S0 = dev(*make(2, 2, 2, 0, 64, 64))
+    got = la().delta_backward(q, k, v, beta, v, 2, lg, S0, S0)
+    assert torch.equal(got[5], S0) and got[4].shape == (2, 2, 0)
+    got = la().delta_backward(q, k, v, beta, v, 1, torch.zeros(2, device="cuda"), S0)
+    assert not got[5].any() and not got[4].any()
+    e = dev(*make(0, 2, 2, 9, 64, 64, kind=1))
+    assert not la().delta_backward(e[0], e[1], e[2], e[3], e[2], 1, e[4])[4].any()
+
+
+def test_backward_in_a_graph():
+    q, k, v, beta, lg, S0 = dev(*make(2, 4, 2, 130, 64, 64, seed=8))
+    dy = torch.randn(v.shape, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    outs = tuple(torch.empty_like(x) for x in (q, k, v, beta, lg, S0))
+    ws = torch.empty(la().delta_backward_workspace_size(2, 4, 130, 64, 64, key_heads=2), dtype=torch.uint8, device="cuda")
+    la().delta_backward(q, k, v, beta, dy, 2, lg, S0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        la().delta_backward(q, k, v, beta, dy, 2, lg, S0, S0, workspace=ws, out=outs)
+    for _ in range(2):
+        dy.neg_()
+        ws.fill_(255)
+        graph.replay()
+        for a, b in zip(outs, la().delta_backward(q, k, v, beta, dy, 2, lg, S0, S0)):
+            assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------ one token
 @pytest.mark.parametrize("B,H,Hk", [(1, 1, 1), (3, 6, 2), (200, 4, 4)])
 @pytest.mark.parametrize("Dk,Dv,dtype", [(16, 16, torch.bfloat16), (64, 80, torch.bfloat16), (128, 128, torch.bfloat16),

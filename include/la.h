@@ -726,6 +726,103 @@ LA_API la_status la_delta_decode_step(const void* q, const void* k, const void* 
                                       const la_decay* decay, float q_scale, float* state, void* out, int B,
                                       int H, int Hk, int Dk, int Dv, la_dtype dtype, la_stream_t stream);
 
+/* A view of n0 x n1 x n2 rows of D dense elements: row (i0, i1, i2) starts at
+ * data + i0 stride[0] + i1 stride[1] + i2 stride[2] (in elements, >= 0).  So
+ * [B,H,T,D] and [B,T,H,D] tensors, slices of a fused projection and broadcast
+ * (stride 0) inputs are read where they lie. */
+typedef struct {
+    void* data;
+    long long stride[3];
+} la_view;
+
+typedef enum {
+    LA_NORM_RMS = 0,          /* n = x (mean x^2 + eps)^-1/2 */
+    LA_NORM_LAYER = 1,        /* n = (x - mean x) (mean (x - mean x)^2 + eps)^-1/2 */
+    LA_NORM_L2 = 2            /* n = x (sum x^2 + eps)^-1/2: keys and queries of the delta rule */
+} la_norm_kind;
+
+typedef enum {
+    LA_GATE_SILU = 0,         /* a(z) = z / (1 + e^-z) */
+    LA_GATE_SIGMOID = 1       /* a(z) = 1 / (1 + e^-z) */
+} la_gate_activation;
+
+/*
+ * la_gated_norm - the norm before or after a block, with what follows it:
+ *
+ *     out = residual + scale * n(x) * weight * a(gate)
+ *
+ * over rows of D elements, in fp32, rounded once.  The scan's output [B,H,T,Dv]
+ * goes through it to [B,T,H,Dv] for the output projection (retention's head
+ * norm and swish gate), a block's input through it to the projections.
+ *
+ *   x, out         views, `dtype`.  out may be x, gate or residual itself.
+ *   gate, residual views, `dtype`, or NULL (factor 1, no residual).
+ *   weight         [D] fp32 or NULL (ones).
+ *   eps            >= 0; with 0 a row of zeros gives NaN, as 0 / 0.
+ *   scale          finite; applies to the normalised part only.
+ *
+ * D up to 8192.  n0 n1 n2 == 0 is a no-op.  Errors (synchronous):
+ * LA_ERR_INVALID_ARG for a NULL view or data, an address that is not a multiple
+ * of the element, negative strides, an output with stride 0 along a
+ * size above 1, bad sizes, kinds or numbers; LA_ERR_UNSUPPORTED for D > 8192 or
+ * more than 2^31 - 1 rows; LA_ERR_CUDA if a launch fails.
+ */
+LA_API la_status la_gated_norm(const la_view* x, const la_view* gate, const float* weight,
+                               const la_view* residual, const la_view* out, int n0, int n1, int n2, int D,
+                               int kind, int activation, float eps, float scale, la_dtype dtype,
+                               la_stream_t stream);
+
+/*
+ * la_gated_norm_backward - gradients of la_gated_norm for the loss sum(dout * out).
+ *
+ *   dout, x        views, `dtype`; gate, weight as given to the forward.
+ *   dx             view, `dtype`.  dgate: view with a gate, else NULL.  Outputs must not
+ *                  overlap inputs.
+ *   dweight        [D] fp32, summed over all rows (in a fixed order: the same bits on
+ *                  every run), or NULL.
+ *   workspace      la_gated_norm_backward_workspace_size(...) bytes, 16-byte
+ *                  aligned, where dweight is asked for.
+ *
+ * The residual's gradient is dout itself.  A broadcast x or gate gets its
+ * gradient row by row; the caller sums it.
+ */
+LA_API la_status la_gated_norm_backward(const la_view* dout, const la_view* x, const la_view* gate,
+                                        const float* weight, const la_view* dx, const la_view* dgate,
+                                        float* dweight, int n0, int n1, int n2, int D, int kind,
+                                        int activation, float eps, float scale, la_dtype dtype,
+                                        void* workspace, size_t workspace_bytes, la_stream_t stream);
+
+LA_API size_t la_gated_norm_backward_workspace_size(int n0, int n1, int n2, int D);
+
+typedef enum {
+    LA_ROTARY_HALF = 0,        /* pairs (i, i + R/2) */
+    LA_ROTARY_INTERLEAVED = 1  /* pairs (2 i, 2 i + 1) */
+} la_rotary_layout;
+
+/*
+ * la_rotary - rotary positions of queries and keys, in one launch: pair i of the
+ * first R elements of token (b, t)'s rows turns by the angle pos(b, t) * freq[i],
+ *
+ *     (a, b) <- mscale * (a cos - b sin, a sin + b cos),
+ *
+ * the other D - R elements are copied.  Angles are reduced in 64 bits.
+ *
+ *   x, out         views of [B,H,T] rows; x2, out2: of [B,H2,T] rows, or NULL with H2 = 0.
+ *                  out may be x itself, out2 x2 itself.
+ *   freq           [R/2] fp32, whatever scaling for long contexts it carries.
+ *   positions      NULL: token t is at start + t; else int64 on the device, position of
+ *                  (b, t) at positions[b * positions_stride + t] (stride 0: one for all).
+ *                  Magnitudes up to 2^53.
+ *   backward       0, or 1 for the transposed map (angles negated, mscale kept):
+ *                  the gradient with respect to x.
+ *
+ * R even, 2 <= R <= D <= 8192.  Errors as for la_gated_norm.
+ */
+LA_API la_status la_rotary(const la_view* x, int H, const la_view* x2, int H2, const la_view* out,
+                           const la_view* out2, const float* freq, const long long* positions,
+                           long long positions_stride, long long start, int B, int T, int D, int R,
+                           int layout, float mscale, int backward, la_dtype dtype, la_stream_t stream);
+
 /* A static string naming a status code. */
 LA_API const char* la_status_string(la_status status);
 

@@ -16,6 +16,10 @@ cpu_baseline / reference legs may import this package.  The CUDA library
   wkv4_direct(...)       the same output from its definition, O(T^2), numpy
   ema(...)               the cumulative EMA of RetNet issue 21 (values,
                          factors, reverse), per channel (ema_ref.c)
+  delta_forward(...), delta_backward(...), delta_decode_step(...)
+                         the gated delta rule token by token, numpy (delta.py)
+  gated_norm(...), gated_norm_backward(...), rotary(...)
+                         what stands around a scan in a block, numpy (block.py)
   parallel_forward(...)  brute-force O(T^2) parallel form, numpy (parallel.py)
   parallel_reverse(...)  brute-force O(T^2) anti-causal form, numpy (parallel.py)
 
@@ -28,6 +32,7 @@ import subprocess
 
 import numpy as np
 
+from .block import gated_norm, gated_norm_backward, rotary  # noqa: F401
 from .delta import delta_backward, delta_decode_step, delta_forward  # noqa: F401
 from .parallel import parallel_forward, parallel_reverse  # noqa: F401
 

@@ -18,7 +18,8 @@ __all__ = ["chunk_forward", "bidirectional", "chunk_backward", "chunk_backward_n
            "backward_workspace_size",
            "decode_step", "device_error", "LAError", "lib", "library_path",
            "delta_forward", "delta_workspace_size", "delta_backward", "delta_backward_workspace_size",
-           "delta_decode_step",
+           "delta_decode_step", "gated_norm", "gated_norm_backward", "rotary", "rotary_frequencies",
+           "NORM_RMS", "NORM_LAYER", "NORM_L2", "GATE_SILU", "GATE_SIGMOID", "ROTARY_HALF", "ROTARY_INTERLEAVED",
            "DECAY_NONE", "DECAY_PER_HEAD", "DECAY_PER_STEP", "FEATURE_NONE", "FEATURE_ELU1", "EXPORTED_SYMBOLS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -26,6 +27,9 @@ library_path = os.path.join(_HERE, "libla.so")
 
 DECAY_NONE, DECAY_PER_HEAD, DECAY_PER_STEP = 0, 1, 2
 FEATURE_NONE, FEATURE_ELU1 = 0, 1
+NORM_RMS, NORM_LAYER, NORM_L2 = 0, 1, 2
+GATE_SILU, GATE_SIGMOID = 0, 1
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
 LA_F32, LA_BF16 = 0, 1
 EXPORTED_SYMBOLS = ("la_chunk_forward", "la_chunk_forward_ws", "la_chunk_forward_workspace_size",
                     "la_chunk_reverse_ws", "la_chunk_bidirectional_ws",
@@ -35,6 +39,7 @@ EXPORTED_SYMBOLS = ("la_chunk_forward", "la_chunk_forward_ws", "la_chunk_forward
                     "la_ema_scan", "la_chunk_state_ws", "la_chunk_state_workspace_size", "la_state_combine",
                     "la_delta_forward_ws", "la_delta_workspace_size", "la_delta_decode_step",
                     "la_delta_backward_ws", "la_delta_backward_workspace_size",
+                    "la_gated_norm", "la_gated_norm_backward", "la_gated_norm_backward_workspace_size", "la_rotary",
                     "la_decode_step", "la_status_string", "la_device_error", "la_version")
 
 
@@ -52,6 +57,10 @@ class _Decay(ctypes.Structure):
 
 class _Prologue(ctypes.Structure):
     _fields_ = [("feature_map", ctypes.c_int), ("q_scale", ctypes.c_float)]
+
+
+class _View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_longlong * 3)]
 
 
 _lib = None
@@ -127,6 +136,15 @@ def lib():
         L.la_delta_backward_workspace_size.restype = sz
         L.la_delta_decode_step.argtypes = [vp, vp, vp, vp, ctypes.POINTER(_Decay), f, vp, vp, i, i, i, i, i, i, vp]
         L.la_delta_decode_step.restype = i
+        vw = ctypes.POINTER(_View)
+        L.la_gated_norm.argtypes = [vw, vw, vp, vw, vw, i, i, i, i, i, i, f, f, i, vp]
+        L.la_gated_norm.restype = i
+        L.la_gated_norm_backward.argtypes = [vw, vw, vw, vp, vw, vw, vp, i, i, i, i, i, i, f, f, i, vp, sz, vp]
+        L.la_gated_norm_backward.restype = i
+        L.la_gated_norm_backward_workspace_size.argtypes = [i, i, i, i]
+        L.la_gated_norm_backward_workspace_size.restype = sz
+        L.la_rotary.argtypes = [vw, i, vw, i, vw, vw, vp, vp, ll, ll, i, i, i, i, i, f, i, i, vp]
+        L.la_rotary.restype = i
         L.la_status_string.argtypes = [i]
         L.la_status_string.restype = ctypes.c_char_p
         L.la_device_error.argtypes = [ctypes.POINTER(ctypes.c_int), vp]
@@ -611,3 +629,4 @@ def device_error(device=None, stream=None):
 
 from .delta import (delta_backward, delta_backward_workspace_size, delta_decode_step, delta_forward,  # noqa: E402
                     delta_workspace_size)
+from .block import gated_norm, gated_norm_backward, rotary, rotary_frequencies  # noqa: E402

@@ -311,6 +311,10 @@ PanelLayout panel_layout(int B, int H, int T, int Dk, int Dv, la_dtype dtype, in
 
 }  // namespace
 
+namespace la {
+int* device_error_word() { return err_word_for_current_device(); }
+}  // namespace la
+
 extern "C" {
 
 const char* la_status_string(la_status status) {

@@ -34,6 +34,9 @@
 
 #include <cstdint>
 
+#include "la_internal.h"
+#include "la_sm100.cuh"
+
 namespace la {
 namespace delta {
 
@@ -41,9 +44,67 @@ constexpr int C = 64;            // tokens per chunk
 constexpr int kPad = 8;          // bf16 padding of a shared-memory row: ldmatrix without bank conflicts
 constexpr int kCS = C + kPad;    // row stride of a C-wide tile
 constexpr int kTok = 3 * C;      // floats per chunk of per-token factors: e^L, e^(L_C - L), beta
+constexpr int kSq = 2 * C * C;   // bytes of a C x C bf16 plane
+constexpr uint64_t kWaitLimitNs = 1000000000ull;  // every barrier wait gives up after this long
 constexpr float kLogFloor = -128.f;  // a decay below e^-128 is zero in fp32 next to anything it is added to
 
+// What prep leaves for each chunk: [planes of (I + A diag(beta))^-1][planes of P]
+// [kTok floats], the matrices as the 128-byte-row swizzled tiles the scans
+// read, so that one bulk copy brings them into shared memory.
+constexpr long long record_bytes(int planes) { return static_cast<long long>(planes) * kSq + sizeof(float) * kTok; }
+
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+// Byte offset of (row, col) of a 64-column bf16 tile whose 16-byte pieces are
+// swizzled within each 128-byte row (TMA's 128-byte pattern).
+__device__ __forceinline__ uint32_t swz64(int row, int col) {
+    return row * 128 + ((((col >> 3) ^ row) & 7) << 4) + (col & 7) * 2;
+}
+
+// A lane's byte offsets of ldmatrix.x4 on the four 16-column blocks of a
+// 16-row band of such a tile; band b, panel p: + 2048 b + 8192 p.  The lane
+// orders are those of off_cols and off_rows below.
+struct LaneOffsets {
+    uint32_t o[4];
+};
+__device__ __forceinline__ LaneOffsets swz_cols(int lane) {
+    const int row = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+    LaneOffsets r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.o[j] = row * 128 + (((2 * j + half) ^ (row & 7)) << 4);
+    return r;
+}
+__device__ __forceinline__ LaneOffsets swz_rows(int lane) {
+    const int row = lane & 15, half = lane >> 4;
+    LaneOffsets r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.o[j] = row * 128 + (((2 * j + half) ^ (row & 7)) << 4);
+    return r;
+}
+
+// One box of a 3-D tensor map.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// Contiguous copy into shared memory (16-byte aligned, a multiple of 16 bytes), completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
+}
+// Contiguous copy out of shared memory; returns once the source may be reused.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)), "r"(src),
+                 "r"(bytes)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -164,24 +225,15 @@ __device__ __forceinline__ void load_tile(__nv_bfloat16* dst, const Planes& src,
     }
 }
 
-// `rows` x 64 dense planes (64 bf16 a row) into rows of kCS.
-__device__ __forceinline__ void load_square(__nv_bfloat16* dst, const __nv_bfloat16* src, int rows, int tid, int nthreads) {
-    for (int i = tid; i < rows * (C / 8); i += nthreads) {
-        const int r = i / (C / 8), c = (i % (C / 8)) * 8;
-        cp16(dst + r * kCS + c, src + r * C + c, true);
-    }
-}
-
 // Value-side operand ([B,H,T,Dv], bf16 or fp32) of one chunk, transposed into
 // accumulator layout: x[j][0..1] = column v0 + g, tokens 8 j + 2 t', +1;
 // x[j][2..3] = column v0 + g + 8 (g = lane / 4, t' = lane % 4).
-// bf16: from the block's shared tile (row stride `stride`), v_local columns in.
-__device__ __forceinline__ void values_from_tile(float (&x)[8][4], const __nv_bfloat16* tile, int stride, int v_local,
-                                                 int lane) {
+// bf16: from the warp's shared tile of 16 columns (32-byte rows).
+__device__ __forceinline__ void values_from_tile(float (&x)[8][4], uint32_t tile, int lane) {
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
         uint32_t r[4];
-        ldsm4t(r, smem_addr(tile + (16 * n) * stride + v_local + off_rows(lane, stride)));
+        ldsm4t(r, tile + 512 * n + (lane & 15) * 32 + (lane >> 4) * 16);
         // r0: tokens 0-7, columns 0-7; r1: tokens 8-15, columns 0-7; r2, r3: columns 8-15
         x[2 * n][0] = low_of(r[0]);
         x[2 * n][1] = high_of(r[0]);
@@ -272,6 +324,124 @@ __device__ __forceinline__ void frag_to_planes(const uint32_t (&a)[N][4], __nv_b
         *reinterpret_cast<uint32_t*>(r + 8) = a[p][2];
         *reinterpret_cast<uint32_t*>(r + 8 * width + 8) = a[p][3];
     }
+}
+
+// ---------------------------------------------------------------- the scans' pipeline
+// Shared memory of one stage: the chunk's K (and Q) tiles as 64-column panels,
+// the record's matrices and factors, the warps' value tiles.
+template <int DKP, int NI, int kPlanes, int NW, bool kQ, bool kV>
+struct ScanTiles {
+    static constexpr int kPanels = (DKP + 63) / 64;
+    static constexpr int kTile = kPanels * 8192;  // one plane of K or Q
+    static constexpr int k = 0;
+    static constexpr int q = k + NI * kTile;
+    static constexpr int rec = q + (kQ ? NI * kTile : 0);
+    static constexpr int tok = rec + kPlanes * kSq;
+    static constexpr int v = tok + 1024;
+    static constexpr int bytes = (v + (kV ? 2048 * NW : 0) + 1023) / 1024 * 1024;
+    static constexpr int kMost = (227 * 1024 - 1024 - 256) / bytes;
+    static constexpr int stages = kMost > 3 ? 3 : kMost;
+    static constexpr int smem = 1024 + stages * bytes + 256;  // alignment, stages, barriers
+    static_assert(stages >= 1, "a chunk's tiles have to fit an SM");
+};
+
+// The stages' barriers and counts, behind the stages.
+template <int kS>
+struct Ring {
+    uint64_t full[kS];  // completes when a stage's copies have landed
+    int left[kS];       // warps that have not yet released the stage
+    int issued[kS];     // chunks brought into the stage so far
+    int abort;
+};
+
+// What brings a chunk into a stage.  No warp is a producer of its own (a ninth
+// warp would halve the registers of eight): the warp that releases a stage last
+// refills it, kS chunks on.
+template <typename Tl, int NI, bool kQ, bool kV>
+struct Feed {
+    const CUtensorMap *mk, *mq, *mv;
+    const unsigned char* records;  // of this (b, h)
+    long long rec_bytes;
+    int rec_used, hk, planes_apart, bh, v0, nv;
+
+    __device__ __forceinline__ void issue(uint32_t base, Ring<Tl::stages>* ring, int s, int c) const {
+        uint64_t* bar = &ring->full[s];
+        const uint32_t st = base + s * Tl::bytes;
+        ring->issued[s] = ring->issued[s] + 1;
+        mbar_arrive_expect_tx(bar, (kQ ? 2 : 1) * NI * Tl::kTile + rec_used + 4 * kTok + (kV ? 2048 * nv : 0));
+        for (int p = 0; p < NI; ++p)
+            for (int i = 0; i < Tl::kPanels; ++i) {
+                tma_load(st + Tl::k + p * Tl::kTile + 8192 * i, mk, bar, 64 * i, c * C, hk + p * planes_apart);
+                if (kQ) tma_load(st + Tl::q + p * Tl::kTile + 8192 * i, mq, bar, 64 * i, c * C, hk + p * planes_apart);
+            }
+        const unsigned char* rec = records + c * rec_bytes;
+        bulk_load(st + Tl::rec, rec, rec_used, bar);
+        bulk_load(st + Tl::tok, rec + rec_bytes - 4 * kTok, 4 * kTok, bar);
+        if (kV)
+            for (int w = 0; w < nv; ++w) tma_load(st + Tl::v + 2048 * w, mv, bar, v0 + 16 * w, c * C, bh);
+    }
+};
+
+// A warp's wait for a stage's `use`-th chunk; false once any warp of the block
+// gave up, and then no copy of the block is still in flight (or none of them
+// lands within the limit).
+template <int kS>
+__device__ __forceinline__ bool wait_stage(Ring<kS>* ring, int s, int use, int* err) {
+    uint64_t* bar = &ring->full[s];
+    bool got = mbar_try_wait(bar, use & 1);
+    if (__all_sync(0xffffffffu, got)) return true;
+    const uint64_t t0 = global_timer_ns();
+    volatile int* abort = &ring->abort;
+    while (true) {
+        if (!got) got = mbar_try_wait_sleep(bar, use & 1, 20000);
+        if (__all_sync(0xffffffffu, got)) return true;
+        const bool late = *abort != 0 || global_timer_ns() - t0 > kWaitLimitNs;
+        if (__any_sync(0xffffffffu, late)) {
+            if ((threadIdx.x & 31) == 0) {
+                *abort = 1;
+                if (err) atomicCAS(err, 0, kErrTmaWait);
+                for (int i = 0; i < kS; ++i) {
+                    const int n = *static_cast<volatile int*>(&ring->issued[i]);
+                    if (n > 0) mbar_wait_bounded(&ring->full[i], (n - 1) & 1, kWaitLimitNs);
+                }
+            }
+            __syncwarp();
+            return false;
+        }
+    }
+}
+
+// A warp has read all it needs of stage s; the last one brings chunk `next` in (or none: next < 0).
+template <typename Tl, typename F>
+__device__ __forceinline__ void release_stage(const F& feed, uint32_t base, Ring<Tl::stages>* ring, int s, int next) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        __threadfence_block();  // this warp's reads come before the count
+        if (atomicSub(&ring->left[s], 1) == 1) {
+            __threadfence_block();  // and every other's before the copies
+            ring->left[s] = feed.nv;
+            if (next >= 0 && *static_cast<volatile int*>(&ring->abort) == 0) {
+                fence_async_smem();
+                feed.issue(base, ring, s, next);
+            }
+        }
+    }
+}
+
+template <typename Tl, typename F>
+__device__ __forceinline__ void start_ring(const F& feed, uint32_t base, Ring<Tl::stages>* ring, int n, int first, int step) {
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Tl::stages; ++s) {
+            mbar_init(&ring->full[s], 1);
+            ring->left[s] = feed.nv;
+            ring->issued[s] = 0;
+        }
+        ring->abort = 0;
+        fence_barrier_init();
+        fence_async_smem();
+        for (int s = 0; s < Tl::stages && s < n; ++s) feed.issue(base, ring, s, first + s * step);
+    }
+    __syncthreads();
 }
 
 }  // namespace delta

@@ -14,12 +14,44 @@ bool supports(int Dk, int Dv, la_dtype dtype) {
     return dtype == LA_F32 || (Dk % 16 == 0 && Dv % 16 == 0);
 }
 
-// Value slices (16 columns, one warp each) per block: as many as still leave a
-// block for each SM, so that the tiles a block loads serve several warps.
+// Value slices (16 columns, one warp each) per block of the scans.  A block
+// fills an SM's shared memory, so blocks beyond the SMs run in another round;
+// up to four warps have a tensor core each, eight share them and take about
+// 1.7 times as long.  The fewest rounds win, then the wider block.
 static int scan_warps(long long BH, int slices) {
-    int w = slices >= 4 ? 4 : slices >= 2 ? 2 : 1;
-    while (w > 1 && BH * ((slices + w - 1) / w) < 148) w /= 2;
-    return w;
+    int best = 1;
+    double least = 0;
+    for (int w = 1; w <= 8; w *= 2) {
+        if (w > 1 && w / 2 >= slices) break;
+        const long long blocks = BH * ((slices + w - 1) / w);
+        const double t = static_cast<double>((blocks + 147) / 148) * (w == 8 ? 1.7 : 1.0);
+        if (w == 1 || t <= least) {
+            best = w;
+            least = t;
+        }
+    }
+    return best;
+}
+
+static bool make_map(CUtensorMap* map, const void* base, int width, long long rows, long long outer, long long row_elems,
+                     int box_cols, bool swizzle) {
+    EncodeTiledFn f = encode_tiled();
+    if (!f) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(outer)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_elems) * 2, static_cast<cuuint64_t>(row_elems) * rows * 2};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), C, 1}, elem[3] = {1, 1, 1};
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, elem,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool scan_maps(const Plan& p, const Args& a, const void* values, ScanMaps* m) {
+    const long long keys = static_cast<long long>(a.B) * a.Hk * (a.dtype == LA_F32 ? 3 : 1);
+    if (!make_map(&m->k, p.k.base, p.k.cols, p.k.rows, keys, p.k.row, 64, true)) return false;
+    if (!make_map(&m->q, p.q.base, p.q.cols, p.q.rows, keys, p.q.row, 64, true)) return false;
+    // fp32 values are read without a map; any valid one stands in
+    m->v = m->k;
+    return a.dtype == LA_F32 || make_map(&m->v, values, a.Dv, a.T, p.BH, a.Dv, 16, false);
 }
 
 Plan make_plan(const Args& a, bool backward, void* workspace) {
@@ -38,9 +70,7 @@ Plan make_plan(const Args& a, bool backward, void* workspace) {
         at += check::round256(bytes);
         return r;
     };
-    p.tok = static_cast<float*>(region(sizeof(float) * chunks * kTok));
-    p.E = static_cast<__nv_bfloat16*>(region(bf * chunks * nm * C * C));
-    p.P = static_cast<__nv_bfloat16*>(region(bf * chunks * np * C * C));
+    p.records = static_cast<unsigned char*>(region(chunks * record_bytes(static_cast<int>(nm + np))));
     if (f32) {
         const size_t plane = keys * p.n * C * p.DKP;
         p.qs = static_cast<__nv_bfloat16*>(region(bf * 3 * plane));

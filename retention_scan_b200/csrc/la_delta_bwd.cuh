@@ -30,180 +30,122 @@ namespace {
 
 // ---------------------------------------------------------------- reverse scan
 // Warp = 16 value columns, dS^T in its accumulators, as in the forward scan.
-template <int DKP, int NI, int NM, int NW, bool kF32>
-struct RevTiles {
-    static constexpr int kRow = DKP + kPad, kV = 16 * NW + kPad;
-    static constexpr int k = 0;
-    static constexpr int q = k + 2 * NI * C * kRow;
-    static constexpr int e = q + 2 * NI * C * kRow;
-    static constexpr int p = e + 2 * NM * C * kCS;
-    static constexpr int v = p + 2 * NM * C * kCS;
-    static constexpr int tok = v + (kF32 ? 0 : 2 * C * kV);
-    static constexpr int bytes = tok + 4 * kTok;
-    static constexpr int stages = 2 * bytes <= 227 * 1024 ? 2 : 1;
-};
-
 struct RevArgs {
-    Planes qp, kp;
     const void* dy;
-    const __nv_bfloat16 *E, *P;
-    const float* tok;
+    const unsigned char* records;
     const float* d_final;
     float* d_init;
     void* dv;
     __nv_bfloat16 *dSst, *dRst;
+    int* err;
     float scale;
+    int planes_apart;
     int H, Hk, T, Dk, Dv, DVP, n, vblocks;
 };
 
 template <int DKP, int NI, int NM, int NW, typename TIn>
-__global__ void __launch_bounds__(32 * NW) reverse_kernel(RevArgs a) {
+__global__ void __launch_bounds__(32 * NW) reverse_kernel(const __grid_constant__ CUtensorMap mk,
+                                                                const __grid_constant__ CUtensorMap mq,
+                                                                const __grid_constant__ CUtensorMap my, RevArgs a) {
     constexpr bool kF32 = sizeof(TIn) == 4;
-    using Tl = RevTiles<DKP, NI, NM, NW, kF32>;
-    constexpr int kRow = Tl::kRow, kS = Tl::stages;
-    extern __shared__ __align__(16) unsigned char smem[];
+    using Tl = ScanTiles<DKP, NI, 2 * NM, NW, true, !kF32>;
+    constexpr int kS = Tl::stages;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+    unsigned char* smem = smem_raw + (base - smem_addr(smem_raw));
+    Ring<kS>* ring = reinterpret_cast<Ring<kS>*>(smem + kS * Tl::bytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long bh = blockIdx.x / a.vblocks;
+    const int bh = blockIdx.x / a.vblocks;
     const int vb = blockIdx.x % a.vblocks * 16 * NW, v0 = vb + 16 * warp;
-    const bool active = v0 < a.Dv;
-    const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
-    const long long hk = static_cast<long long>(b) * a.Hk + h / (a.H / a.Hk);
-    const TIn* ysrc = static_cast<const TIn*>(a.dy) + bh * a.T * a.Dv;
+    const int nv = min(NW, (a.Dv - vb + 15) / 16);
+    const int b = bh / a.H, h = bh % a.H;
+
+    Feed<Tl, NI, true, !kF32> feed;
+    feed.mk = &mk;
+    feed.mq = &mq;
+    feed.mv = &my;
+    feed.rec_bytes = record_bytes(2 * NM);
+    feed.records = a.records + static_cast<long long>(bh) * a.n * feed.rec_bytes;
+    feed.rec_used = 2 * NM * kSq;
+    feed.hk = b * a.Hk + h / (a.H / a.Hk);
+    feed.planes_apart = a.planes_apart;
+    feed.bh = bh;
+    feed.v0 = vb;
+    feed.nv = nv;
+    start_ring<Tl>(feed, base, ring, a.n, a.n - 1, -1);
+    if (warp >= nv) return;
+
+    const TIn* ysrc = static_cast<const TIn*>(a.dy) + static_cast<long long>(bh) * a.T * a.Dv;
     const int tq = (lane & 3) * 2;
-
-    auto load = [&](int c) {  // c counts down
-        if (c >= 0) {
-            unsigned char* st = smem + static_cast<size_t>(c % kS) * Tl::bytes;
-            const long long cid = bh * a.n + c;
-            load_tile<DKP, NI>(reinterpret_cast<__nv_bfloat16*>(st + Tl::k), a.kp, hk, c * C, tid, 32 * NW);
-            load_tile<DKP, NI>(reinterpret_cast<__nv_bfloat16*>(st + Tl::q), a.qp, hk, c * C, tid, 32 * NW);
-            load_square(reinterpret_cast<__nv_bfloat16*>(st + Tl::e), a.E + cid * NM * C * C, NM * C, tid, 32 * NW);
-            load_square(reinterpret_cast<__nv_bfloat16*>(st + Tl::p), a.P + cid * NM * C * C, NM * C, tid, 32 * NW);
-            if constexpr (!kF32) {
-                constexpr int kVec = 2 * NW;
-                for (int i = tid; i < C * kVec; i += 32 * NW) {
-                    const int r = i / kVec, col = (i % kVec) * 8, t = c * C + r;
-                    const bool ok = t < a.T && vb + col < a.Dv;
-                    cp16(reinterpret_cast<__nv_bfloat16*>(st + Tl::v) + r * Tl::kV + col,
-                         ok ? ysrc + static_cast<long long>(t) * a.Dv + vb + col : ysrc, ok);
-                }
-            }
-            for (int i = tid; i < kTok / 4; i += 32 * NW) cp16(st + Tl::tok + 16 * i, a.tok + cid * kTok + 4 * i, true);
-        }
-        cp_commit();
-    };
-
+    const LaneOffsets oc = swz_cols(lane), orow = swz_rows(lane);
     float S[DKP / 8][4];
-    state_load<DKP>(S, a.d_final ? a.d_final + bh * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, v0, lane);
-    if constexpr (kS > 1) load(a.n - 1);
+    state_load<DKP>(S, a.d_final ? a.d_final + static_cast<long long>(bh) * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, v0, lane);
 
-    for (int c = a.n - 1; c >= 0; --c) {
-        if constexpr (kS > 1) {
-            load(c - 1);
-            cp_wait<1>();
-        } else {
-            load(c);
-            cp_wait<0>();
+    for (int i = 0; i < a.n; ++i) {
+        const int stage = i % kS, c = a.n - 1 - i;
+        if (!wait_stage(ring, stage, i / kS, a.err)) return;
+        const uint32_t st = base + stage * Tl::bytes;
+        const uint32_t kt = st + Tl::k, qt = st + Tl::q, et = st + Tl::rec, pt = et + NM * kSq;
+        const float* gam = reinterpret_cast<const float*>(smem + stage * Tl::bytes + Tl::tok);
+        const float* rest = gam + C;
+        const float* beta = gam + 2 * C;
+        const long long cid = static_cast<long long>(bh) * a.n + c;
+
+        // X = (K dS)^T, then dU = e^(L_C - L) X + (P^T dY)
+        float X[8][4] = {};
+#pragma unroll
+        for (int d = 0; d < DKP / 16; ++d) {
+            uint32_t s[NM][4];
+            split_frag<NM>(S[2 * d], S[2 * d + 1], s);
+            frag_to_planes<NM>(s, a.dSst + cid * NM * a.DVP * DKP, static_cast<long long>(a.DVP) * DKP, DKP, v0, 16 * d, lane);
+#pragma unroll
+            for (int nn = 0; nn < 4; ++nn)
+#pragma unroll
+                for (int p = 0; p < NI; ++p) {
+                    uint32_t r[4];
+                    ldsm4(r, kt + p * Tl::kTile + 8192 * (d / 4) + 2048 * nn + oc.o[d % 4]);
+                    mma_planes<NM, NM>(X[2 * nn], X[2 * nn + 1], s, p, r);
+                }
         }
-        __syncthreads();
-        if (active) {
-            unsigned char* st = smem + static_cast<size_t>(c % kS) * Tl::bytes;
-            const __nv_bfloat16* kt = reinterpret_cast<const __nv_bfloat16*>(st + Tl::k);
-            const __nv_bfloat16* qt = reinterpret_cast<const __nv_bfloat16*>(st + Tl::q);
-            const __nv_bfloat16* et = reinterpret_cast<const __nv_bfloat16*>(st + Tl::e);
-            const __nv_bfloat16* pt = reinterpret_cast<const __nv_bfloat16*>(st + Tl::p);
-            const float* gam = reinterpret_cast<const float*>(st + Tl::tok);
-            const float* rest = gam + C;
-            const float* beta = gam + 2 * C;
-            const long long cid = bh * a.n + c;
-
-            // X = (K dS)^T, then dU = e^(L_C - L) X + (P^T dY)
-            float X[8][4] = {};
 #pragma unroll
-            for (int d = 0; d < DKP / 16; ++d) {
-                uint32_t s[NM][4];
-                split_frag<NM>(S[2 * d], S[2 * d + 1], s);
-                frag_to_planes<NM>(s, a.dSst + cid * NM * a.DVP * DKP, static_cast<long long>(a.DVP) * DKP, DKP, v0, 16 * d, lane);
-#pragma unroll
-                for (int nn = 0; nn < 4; ++nn)
-#pragma unroll
-                    for (int p = 0; p < NI; ++p) {
-                        uint32_t r[4];
-                        ldsm4(r, smem_addr(kt + (p * C + 16 * nn) * kRow + 16 * d + off_cols(lane, kRow)));
-                        mma_planes<NM, NM>(X[2 * nn], X[2 * nn + 1], s, p, r);
-                    }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 rs = *reinterpret_cast<const float2*>(rest + 8 * j + tq);
-                X[j][0] *= rs.x;
-                X[j][1] *= rs.y;
-                X[j][2] *= rs.x;
-                X[j][3] *= rs.y;
-            }
+        for (int j = 0; j < 8; ++j) {
+            const float2 rs = *reinterpret_cast<const float2*>(rest + 8 * j + tq);
+            X[j][0] *= rs.x;
+            X[j][1] *= rs.y;
+            X[j][2] *= rs.x;
+            X[j][3] *= rs.y;
+        }
+        const float total = gam[C - 1];
+        {
             float Y[8][4];
             if constexpr (kF32)
                 values_from_global(Y, ysrc, c * C, a.T, a.Dv, v0, lane);
             else
-                values_from_tile(Y, reinterpret_cast<const __nv_bfloat16*>(st + Tl::v), Tl::kV, 16 * warp, lane);
+                values_from_tile(Y, st + Tl::v + 2048 * warp, lane);
+            uint32_t y[4][NM][4];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {  // tokens t of P's rows; columns s <= t
-                uint32_t y[NI][4];
-                split_frag<NI>(Y[2 * m], Y[2 * m + 1], y);
+                uint32_t x[NI][4];
+                split_frag<NI>(Y[2 * m], Y[2 * m + 1], x);
 #pragma unroll
                 for (int nn = 0; nn <= m; ++nn)
 #pragma unroll
                     for (int p = 0; p < NM; ++p) {
                         uint32_t r[4];
-                        ldsm4t(r, smem_addr(pt + (p * C + 16 * m) * kCS + 16 * nn + off_rows(lane, kCS)));
-                        mma_planes<NI, NM>(X[2 * nn], X[2 * nn + 1], y, p, r);
+                        ldsm4t(r, pt + p * kSq + 2048 * m + orow.o[nn]);
+                        mma_planes<NI, NM>(X[2 * nn], X[2 * nn + 1], x, p, r);
                     }
-            }
-            // dR = T^T diag(beta) dU
-            float R[8][4] = {};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 bt = *reinterpret_cast<const float2*>(beta + 8 * j + tq);
-                X[j][0] *= bt.x;
-                X[j][1] *= bt.y;
-                X[j][2] *= bt.x;
-                X[j][3] *= bt.y;
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                uint32_t x[NM][4];
-                split_frag<NM>(X[2 * m], X[2 * m + 1], x);
-#pragma unroll
-                for (int nn = 0; nn <= m; ++nn)
-#pragma unroll
-                    for (int p = 0; p < NM; ++p) {
-                        uint32_t r[4];
-                        ldsm4t(r, smem_addr(et + (p * C + 16 * m) * kCS + 16 * nn + off_rows(lane, kCS)));
-                        mma_planes<NM, NM>(R[2 * nn], R[2 * nn + 1], x, p, r);
-                    }
-            }
-            values_to_global(R, static_cast<TIn*>(a.dv) + bh * a.T * a.Dv, c * C, a.T, a.Dv, v0, lane);
-            uint32_t y[4][NM][4], w[4][NM][4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                split_frag<NM>(R[2 * m], R[2 * m + 1], w[m]);
-                frag_to_planes<NM>(w[m], a.dRst + cid * NM * a.DVP * C, static_cast<long long>(a.DVP) * C, C, v0, 16 * m, lane);
 #pragma unroll
                 for (int j = 2 * m; j < 2 * m + 2; ++j) {
                     const float2 gm = *reinterpret_cast<const float2*>(gam + 8 * j + tq);
-                    R[j][0] *= -gm.x;
-                    R[j][1] *= -gm.y;
-                    R[j][2] *= -gm.x;
-                    R[j][3] *= -gm.y;
                     Y[j][0] *= a.scale * gm.x;
                     Y[j][1] *= a.scale * gm.y;
                     Y[j][2] *= a.scale * gm.x;
                     Y[j][3] *= a.scale * gm.y;
                 }
-                split_frag<NM>(R[2 * m], R[2 * m + 1], w[m]);
                 split_frag<NM>(Y[2 * m], Y[2 * m + 1], y[m]);
             }
-            const float total = gam[C - 1];
+            // dS <- e^(L_C) dS + scale (Q^T e^L dY); dR's part follows
 #pragma unroll
             for (int d = 0; d < DKP / 16; ++d) {
                 float acc[2][4] = {};
@@ -212,20 +154,73 @@ __global__ void __launch_bounds__(32 * NW) reverse_kernel(RevArgs a) {
 #pragma unroll
                     for (int p = 0; p < NI; ++p) {
                         uint32_t r[4];
-                        ldsm4t(r, smem_addr(qt + (p * C + 16 * m) * kRow + 16 * d + off_rows(lane, kRow)));
+                        ldsm4t(r, qt + p * Tl::kTile + 8192 * (d / 4) + 2048 * m + orow.o[d % 4]);
                         mma_planes<NM, NM>(acc[0], acc[1], y[m], p, r);
-                        ldsm4t(r, smem_addr(kt + (p * C + 16 * m) * kRow + 16 * d + off_rows(lane, kRow)));
-                        mma_planes<NM, NM>(acc[0], acc[1], w[m], p, r);
                     }
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) S[2 * d + j][i] = fmaf(total, S[2 * d + j][i], acc[j][i]);
+                    for (int x = 0; x < 4; ++x) S[2 * d + j][x] = fmaf(total, S[2 * d + j][x], acc[j][x]);
             }
         }
-        __syncthreads();
+        // dR = T^T diag(beta) dU
+        float R[8][4] = {};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 bt = *reinterpret_cast<const float2*>(beta + 8 * j + tq);
+            X[j][0] *= bt.x;
+            X[j][1] *= bt.y;
+            X[j][2] *= bt.x;
+            X[j][3] *= bt.y;
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            uint32_t x[NM][4];
+            split_frag<NM>(X[2 * m], X[2 * m + 1], x);
+#pragma unroll
+            for (int nn = 0; nn <= m; ++nn)
+#pragma unroll
+                for (int p = 0; p < NM; ++p) {
+                    uint32_t r[4];
+                    ldsm4t(r, et + p * kSq + 2048 * m + orow.o[nn]);
+                    mma_planes<NM, NM>(R[2 * nn], R[2 * nn + 1], x, p, r);
+                }
+        }
+        values_to_global(R, static_cast<TIn*>(a.dv) + static_cast<long long>(bh) * a.T * a.Dv, c * C, a.T, a.Dv, v0, lane);
+        uint32_t w[4][NM][4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            split_frag<NM>(R[2 * m], R[2 * m + 1], w[m]);
+            frag_to_planes<NM>(w[m], a.dRst + cid * NM * a.DVP * C, static_cast<long long>(a.DVP) * C, C, v0, 16 * m, lane);
+#pragma unroll
+            for (int j = 2 * m; j < 2 * m + 2; ++j) {
+                const float2 gm = *reinterpret_cast<const float2*>(gam + 8 * j + tq);
+                R[j][0] *= -gm.x;
+                R[j][1] *= -gm.y;
+                R[j][2] *= -gm.x;
+                R[j][3] *= -gm.y;
+            }
+            split_frag<NM>(R[2 * m], R[2 * m + 1], w[m]);
+        }
+#pragma unroll
+        for (int d = 0; d < DKP / 16; ++d) {
+            float acc[2][4] = {};
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int p = 0; p < NI; ++p) {
+                    uint32_t r[4];
+                    ldsm4t(r, kt + p * Tl::kTile + 8192 * (d / 4) + 2048 * m + orow.o[d % 4]);
+                    mma_planes<NM, NM>(acc[0], acc[1], w[m], p, r);
+                }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) S[2 * d + j][x] += acc[j][x];
+        }
+        release_stage<Tl>(feed, base, ring, stage, c - kS);
     }
-    if (active && a.d_init) state_store<DKP>(S, a.d_init + bh * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane);
+    if (a.d_init) state_store<DKP>(S, a.d_init + static_cast<long long>(bh) * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane);
 }
 
 // ---------------------------------------------------------------- gradients of a chunk
@@ -262,7 +257,7 @@ struct GradArgs {
     Planes qp, kp;
     const void* dy;
     const __nv_bfloat16 *S, *dS, *E, *dR;
-    const float* tok;
+    const unsigned char* records;
     const float* log_g;
     int decay_kind;
     float scale;
@@ -344,7 +339,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(GradArgs a) {
 
     load_tile<DKP, NI>(kt, a.kp, hk, t0, tid, kGradThreads);
     load_tile<DKP, NI>(qt, a.qp, hk, t0, tid, kGradThreads);
-    for (int i = tid; i < kTok / 4; i += kGradThreads) cp16(tok + 4 * i, a.tok + cid * kTok + 4 * i, true);
+    for (int i = tid; i < kTok / 4; i += kGradThreads) cp16(tok + 4 * i, a.records + (cid + 1) * record_bytes(2 * NM) - 4 * kTok + 16 * i, true);
     load(0);
     if (warp == 0) {  // as in prep_kernel
         double x[2];
@@ -659,25 +654,23 @@ __global__ void group_sum_kernel(const float* __restrict__ x, TOut* __restrict__
 template <int DKP, int NI, int NM, int NW, typename TIn>
 cudaError_t reverse_run(const Plan& p, const Args& a, RevArgs r) {
     auto kern = reverse_kernel<DKP, NI, NM, NW, TIn>;
-    using Tl = RevTiles<DKP, NI, NM, NW, sizeof(TIn) == 4>;
-    static_assert(Tl::stages * Tl::bytes <= 227 * 1024, "the reverse scan's tiles have to fit an SM");
-    constexpr int smem = Tl::stages * Tl::bytes;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    using Tl = ScanTiles<DKP, NI, 2 * NM, NW, true, sizeof(TIn) == 2>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tl::smem);
     if (e != cudaSuccess) return e;
+    ScanMaps m;
+    if (!scan_maps(p, a, a.dy, &m)) return cudaErrorUnknown;
     r.vblocks = (a.Dv + 16 * NW - 1) / (16 * NW);
-    kern<<<static_cast<unsigned>(p.BH * r.vblocks), 32 * NW, smem, a.stream>>>(r);
+    kern<<<static_cast<unsigned>(p.BH * r.vblocks), 32 * NW, Tl::smem, a.stream>>>(m.k, m.q, m.v, r);
     return cudaGetLastError();
 }
 
 template <int DKP, int NI, int NM, typename TIn>
 cudaError_t backward_typed(const Plan& p, const Args& a) {
     RevArgs r{};
-    r.qp = p.q;
-    r.kp = p.k;
     r.dy = a.dy;
-    r.E = p.E;
-    r.P = p.P;
-    r.tok = p.tok;
+    r.records = p.records;
+    r.err = device_error_word();
+    r.planes_apart = a.B * a.Hk;
     r.d_final = a.d_final_state;
     r.d_init = a.d_init_state;
     r.dv = a.dv;
@@ -693,7 +686,8 @@ cudaError_t backward_typed(const Plan& p, const Args& a) {
     r.n = p.n;
     cudaError_t e = p.warps == 1   ? reverse_run<DKP, NI, NM, 1, TIn>(p, a, r)
                     : p.warps == 2 ? reverse_run<DKP, NI, NM, 2, TIn>(p, a, r)
-                                   : reverse_run<DKP, NI, NM, 4, TIn>(p, a, r);
+                    : p.warps == 4 ? reverse_run<DKP, NI, NM, 4, TIn>(p, a, r)
+                                   : reverse_run<DKP, NI, NM, 8, TIn>(p, a, r);
     if (e != cudaSuccess) return e;
 
     GradArgs g{};
@@ -704,7 +698,7 @@ cudaError_t backward_typed(const Plan& p, const Args& a) {
     g.dS = p.dS;
     g.E = p.Er;
     g.dR = p.dR;
-    g.tok = p.tok;
+    g.records = p.records;
     g.log_g = a.log_g;
     g.decay_kind = a.decay_kind;
     g.scale = a.scale;

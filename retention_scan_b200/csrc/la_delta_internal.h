@@ -42,8 +42,7 @@ struct Plan {
     int DKP, DVP; // key width of the kernels, value width in whole 16-column slices
     int warps;    // 16-column slices per block of the scans
     Planes q, k;
-    float* tok;                 // [BH][n][kTok]
-    __nv_bfloat16 *E, *P;       // [BH][n][planes][C][C]
+    unsigned char* records;     // [BH][n][record_bytes(planes of both matrices)]
     __nv_bfloat16 *qs, *ks;     // fp32 inputs' planes
     // backward only
     __nv_bfloat16 *S, *dS;      // [BH][n][planes][DVP][DKP]: states before, gradients after each chunk
@@ -54,26 +53,31 @@ struct Plan {
 };
 
 struct ScanArgs {
-    Planes qp, kp;
     const void* v;
-    const __nv_bfloat16 *E, *P;
-    const float* tok;
+    const unsigned char* records;
     const float* init_state;
     void* out;
     float* final_state;
     __nv_bfloat16 *Sst, *Est;
+    int* err;
     float scale;
+    int planes_apart;  // key heads of a plane (fp32 inputs)
     int H, Hk, T, Dk, Dv, DVP, n, vblocks;
 };
 
+// Tensor maps of the scans' tiles: K and Q by 64 columns of 64 tokens (128-byte
+// swizzle), the value-side operand (v, dy; bf16 only) by 16 columns.
+struct ScanMaps {
+    CUtensorMap k, q, v;
+};
+bool scan_maps(const Plan& p, const Args& a, const void* values, ScanMaps* m);
+
 inline ScanArgs scan_args(const Plan& p, const Args& a) {
     ScanArgs s{};
-    s.qp = p.q;
-    s.kp = p.k;
     s.v = a.v;
-    s.E = p.E;
-    s.P = p.P;
-    s.tok = p.tok;
+    s.records = p.records;
+    s.err = device_error_word();
+    s.planes_apart = a.B * a.Hk;
     s.init_state = a.init_state;
     s.out = a.out;
     s.final_state = a.final_state;

@@ -23,6 +23,10 @@ EncodeTiledFn encode_tiled();
 enum SymbolSlot : int { kSymErrWord = 0, kSymStaticScratch = 1, kSymSlots = 2 };
 void* device_symbol_address(const void* symbol, int slot);
 
+// The device error word of the current device (la_device_error), null if its
+// address cannot be had.
+int* device_error_word();
+
 // Device error codes written by kernels that give up waiting on a barrier.
 enum DeviceError : int {
     kErrNone = 0,

@@ -29,6 +29,8 @@ def built():
     from retention_scan_b200 import build
     build.build()
     assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    yield
+    assert la().device_error() == 0, "a kernel gave up waiting on a barrier"
 
 
 def la():

@@ -175,7 +175,7 @@ def _dtype_code(dt):
 def _need(t, name, shape, dtype, device):
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -191,6 +191,29 @@ def _decay(kind, log_g):
     if log_g is None:
         raise ValueError("log_g is required for a per-head or per-step decay")
     return _Decay(kind, log_g.data_ptr())
+
+
+class _Here:
+    """Stands for the device context of the device that is current already."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_here = _Here()
+
+
+def _device(dev):
+    """torch.cuda.device(dev), which costs a small call's launch again, only where it changes the device."""
+    return _here if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _raw_stream(stream, dev):
+    """The call's stream as a plain handle: the given one, or dev's current one."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _stream(stream, device):

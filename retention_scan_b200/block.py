@@ -12,15 +12,21 @@ import math
 
 import torch
 
-from . import (GATE_SIGMOID, GATE_SILU, NORM_L2, NORM_LAYER, NORM_RMS, ROTARY_HALF, ROTARY_INTERLEAVED, _check, _dtype_code,
-               _need, _ptr, _stream, _View, lib)
+from . import (GATE_SIGMOID, GATE_SILU, NORM_L2, NORM_LAYER, NORM_RMS, ROTARY_HALF, ROTARY_INTERLEAVED, _check, _device,
+               _dtype_code, _need, _raw_stream, _View, lib)
+
+_Strides = ctypes.c_longlong * 3
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _view(t, name, shape, dtype, device, output=False):
     """The tensor as a view of rows (its leading dimensions padded to three)."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -28,10 +34,10 @@ def _view(t, name, shape, dtype, device, output=False):
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the last dimension must be dense")
-    lead = [s if n > 1 else 0 for n, s in zip(t.shape[:-1], t.stride()[:-1])]
-    if output and any(n > 1 and s == 0 for n, s in zip(t.shape[:-1], lead)):
+    lead = [s if n > 1 else 0 for n, s in zip(t.shape[:-1], t.stride())]
+    if output and 0 in lead and any(n > 1 and s == 0 for n, s in zip(t.shape[:-1], lead)):
         raise ValueError(f"{name}: an output's rows must not share memory")
-    return _View(t.data_ptr(), (ctypes.c_longlong * 3)(*([0] * (3 - len(lead)) + lead)))
+    return _View(t.data_ptr(), _Strides(*([0] * (3 - len(lead)) + lead)))
 
 
 def _ref(v):
@@ -69,9 +75,9 @@ def gated_norm(x, gate=None, weight=None, residual=None, kind=NORM_RMS, activati
     gv, rv = (_view(t, name, x.shape, x.dtype, dev) for t, name in ((gate, "gate"), (residual, "residual")))
     ov = _view(out, "out", x.shape, x.dtype, dev, output=True)
     _need(weight, "weight", (D,), torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _device(dev):
         _check(lib().la_gated_norm(_ref(xv), _ref(gv), _ptr(weight), _ref(rv), _ref(ov), *n, D, int(kind), int(activation),
-                                   float(eps), float(scale), code, _stream(stream, dev)))
+                                   float(eps), float(scale), code, _raw_stream(stream, dev)))
     return out
 
 
@@ -102,7 +108,7 @@ def gated_norm_backward(dout, x, gate=None, weight=None, kind=NORM_RMS, activati
     dxv, dgv = (_view(t, name, x.shape, x.dtype, dev, output=True) for t, name in ((dx, "dx"), (dgate, "dgate")))
     _need(weight, "weight", (D,), torch.float32, dev)
     _need(dweight, "dweight", (D,), torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _device(dev):
         if dweight is not None and workspace is None:
             nbytes = int(lib().la_gated_norm_backward_workspace_size(*n, D))
             workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
@@ -114,7 +120,7 @@ def gated_norm_backward(dout, x, gate=None, weight=None, kind=NORM_RMS, activati
         _check(lib().la_gated_norm_backward(
             _ref(dv), _ref(xv), _ref(gv), _ptr(weight), _ref(dxv), _ref(dgv), _ptr(dweight), *n, D, int(kind),
             int(activation), float(eps), float(scale), code, _ptr(workspace),
-            0 if workspace is None else workspace.numel(), _stream(stream, dev)))
+            0 if workspace is None else workspace.numel(), _raw_stream(stream, dev)))
     return dx, dgate, dweight
 
 
@@ -168,10 +174,10 @@ def rotary(x, freq, positions=None, x2=None, start=0, layout=ROTARY_HALF, mscale
     xv, ov = _view(x, "x", (B, H, T, D), x.dtype, dev), _view(out, "out", (B, H, T, D), x.dtype, dev, output=True)
     xv2 = _view(x2, "x2", (B, H2, T, D), x.dtype, dev)
     ov2 = _view(out2, "out2", (B, H2, T, D), x.dtype, dev, output=True)
-    with torch.cuda.device(dev):
+    with _device(dev):
         _check(lib().la_rotary(_ref(xv), H, _ref(xv2), H2, _ref(ov), _ref(ov2), _ptr(freq), _ptr(positions), pstride,
                                int(start), B, T, D, R, int(layout), float(mscale), int(bool(backward)), code,
-                               _stream(stream, dev)))
+                               _raw_stream(stream, dev)))
     return (out, out2) if x2 is not None else out
 
 

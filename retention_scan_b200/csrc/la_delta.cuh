@@ -326,6 +326,37 @@ __device__ __forceinline__ void frag_to_planes(const uint32_t (&a)[N][4], __nv_b
     }
 }
 
+// ---------------------------------------------------------------- decays within a chunk
+// One warp: the inclusive prefix L of log2 g over the chunk's tokens, summed in
+// 64 bits and kept as the fp32 pair (L rounded, what that left), so that a
+// difference of two of them is as good as one taken in 64 bits.
+__device__ __forceinline__ void decay_prefix(float2* L, int lane, const float* __restrict__ log_g, int decay_kind, int h,
+                                             long long bh, int t0, int T) {
+    double a[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = t0 + 2 * lane + i;
+        float g = 0.f;
+        if (t < T) {
+            if (decay_kind == LA_DECAY_PER_HEAD) g = log_g[h];
+            if (decay_kind == LA_DECAY_PER_STEP) g = log_g[bh * T + t];
+        }
+        a[i] = static_cast<double>(g < kLogFloor ? kLogFloor : g) * 1.4426950408889634074;
+    }
+    double s = a[0] + a[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += x;
+    }
+    const double first = s - a[1];
+    const float f = static_cast<float>(first), l = static_cast<float>(s);
+    L[2 * lane] = make_float2(f, static_cast<float>(first - f));
+    L[2 * lane + 1] = make_float2(l, static_cast<float>(s - l));
+}
+// 2^(L_t - L_s)
+__device__ __forceinline__ float decay_between(float2 t, float2 s) { return ex2_approx((t.x - s.x) + (t.y - s.y)); }
+
 // ---------------------------------------------------------------- the scans' pipeline
 // Shared memory of one stage: the chunk's K (and Q) tiles as 64-column panels,
 // the record's matrices and factors, the warps' value tiles.

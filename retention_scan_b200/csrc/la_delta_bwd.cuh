@@ -247,7 +247,7 @@ struct GradTiles {
     static constexpr int dp = s;                            // [NM][C][kCS], over the slices once they are done
     static constexpr int da = dp + 2 * NM * C * kCS;
     static constexpr int after = (2 * slice > 4 * NM * C * kCS ? 2 * slice : 4 * NM * C * kCS) + s;
-    static constexpr int tok = after;                       // kTok floats, L as doubles, sums
+    static constexpr int tok = after;                       // kTok floats, L, sums
     static constexpr int L = tok + 4 * kTok;
     static constexpr int sums = L + 8 * C;                  // floats: [4][2][C] row sums, [4][C] column sums
     static constexpr int bytes = sums + 4 * (8 * C + 4 * C + 64);
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(GradArgs a) {
     __nv_bfloat16* kt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::k);
     __nv_bfloat16* qt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::q);
     float* tok = reinterpret_cast<float*>(smem + Tl::tok);
-    double* L = reinterpret_cast<double*>(smem + Tl::L);
+    float2* L = reinterpret_cast<float2*>(smem + Tl::L);
     float* rowsum = reinterpret_cast<float*>(smem + Tl::sums);  // [4 kinds][2 halves][C]
     float* colsum = rowsum + 8 * C;                             // [4 row groups][C]
     float* wsum = colsum + 4 * C;                               // per warp
@@ -341,27 +341,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(GradArgs a) {
     load_tile<DKP, NI>(qt, a.qp, hk, t0, tid, kGradThreads);
     for (int i = tid; i < kTok / 4; i += kGradThreads) cp16(tok + 4 * i, a.records + (cid + 1) * record_bytes(2 * NM) - 4 * kTok + 16 * i, true);
     load(0);
-    if (warp == 0) {  // as in prep_kernel
-        double x[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = t0 + 2 * lane + i;
-            float lg = 0.f;
-            if (t < a.T) {
-                if (a.decay_kind == LA_DECAY_PER_HEAD) lg = a.log_g[h];
-                if (a.decay_kind == LA_DECAY_PER_STEP) lg = a.log_g[bh * a.T + t];
-            }
-            x[i] = lg < kLogFloor ? kLogFloor : lg;
-        }
-        double s = x[0] + x[1];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
-        }
-        L[2 * lane + 1] = s;
-        L[2 * lane] = s - x[1];
-    }
+    if (warp == 0) decay_prefix(L, lane, a.log_g, a.decay_kind, h, bh, t0, a.T);
 
     float M[4][4] = {}, N[4][4] = {};
     float dQ[kJ][4] = {}, Kr[kJ][4] = {}, Z[kJ][4] = {};
@@ -463,7 +443,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(GradArgs a) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int s = 32 * wc + 8 * j + tq + x;
-                const float d = s <= t ? expf(static_cast<float>(L[t] - L[s])) : 0.f;
+                const float d = s <= t ? decay_between(L[t], L[s]) : 0.f;
                 const float m = a.scale * d * M[j][2 * r + x], w = s < t ? -d * N[j][2 * r + x] : 0.f;
                 cs[x] += (s <= t ? m * qk[j][2 * r + x] : 0.f) + (s < t ? w * kk[j][2 * r + x] : 0.f);
                 p2[x] = s <= t ? m * beta[s] : 0.f;

@@ -5,7 +5,7 @@
 // Bound by HBM: the whole fp32 state is read and written once (8 Dk Dv bytes
 // per (b, h)) for 6 Dk Dv flops.  The update needs S^T k over all rows before
 // it can change any of them, so a block holds its columns of S in registers
-// between the read and the write (16 float4 a thread at Dk = Dv = 128): the
+// between the read and the write (8 float4 a thread at Dk = 128): the
 // state crosses HBM once each way, and y comes from the same sums (the last
 // line above substitutes the updated state), not from a second pass.
 #include <cuda_bf16.h>
@@ -17,26 +17,27 @@ namespace la {
 namespace delta {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRegs = 64;  // state values a thread holds
+constexpr int kThreads = 128;
+constexpr int kRegs = 32;   // state values a thread holds
+constexpr int kSlice = 32;  // value columns of a block: 128 rows of them fill its registers
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_f(float* p, float x) { *p = x; }
 __device__ __forceinline__ void from_f(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// One block per (b, h) and slice of W value columns; a thread owns VEC
+// One block per (b, h) and slice of value columns; a thread owns VEC
 // neighbouring columns and every R-th row.
 template <typename TIn, int VEC>
-__global__ void __launch_bounds__(kThreads) decode_kernel(DecodeArgs a, int W, int slices) {
+__global__ void __launch_bounds__(kThreads, 5) decode_kernel(DecodeArgs a, int slices) {
     constexpr int kRows = kRegs / VEC;
     __shared__ float ks[128], qs[128];
     __shared__ float sk[kThreads * VEC], sq[kThreads * VEC];
-    __shared__ float us[128];
+    __shared__ float us[kSlice];
     __shared__ float kq_s;
     const int tid = threadIdx.x;
     const long long bh = blockIdx.x / slices;
-    const int c0 = blockIdx.x % slices * W, Wc = min(W, a.Dv - c0);
+    const int c0 = blockIdx.x % slices * kSlice, Wc = min(kSlice, a.Dv - c0);
     const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
     const long long hk = static_cast<long long>(b) * a.Hk + h / (a.H / a.Hk);
     const int nc = Wc / VEC, R = kThreads / nc;
@@ -132,14 +133,12 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeArgs a, int W, i
 template <typename TIn>
 cudaError_t launch_typed(const DecodeArgs& a) {
     const long long BH = static_cast<long long>(a.B) * a.H;
-    // Few (b, h): slices of 32 columns spread the state's read over more SMs.
-    const int W = BH * 2 <= 148 && a.Dv > 32 ? 32 : a.Dv;
-    const int slices = (a.Dv + W - 1) / W;
+    const int slices = (a.Dv + kSlice - 1) / kSlice;
     const unsigned grid = static_cast<unsigned>(BH * slices);
     if (a.Dv % 4 == 0)
-        decode_kernel<TIn, 4><<<grid, kThreads, 0, a.stream>>>(a, W, slices);
+        decode_kernel<TIn, 4><<<grid, kThreads, 0, a.stream>>>(a, slices);
     else
-        decode_kernel<TIn, 1><<<grid, kThreads, 0, a.stream>>>(a, W, slices);
+        decode_kernel<TIn, 1><<<grid, kThreads, 0, a.stream>>>(a, slices);
     return cudaGetLastError();
 }
 

@@ -39,20 +39,25 @@ __global__ void split_kernel(const float* __restrict__ x, __nv_bfloat16* __restr
 // the whole 64 x 64 matrix by one thread a column was bound by fetching its
 // 2700 unrolled instructions for two warps.
 constexpr int kPrepThreads = 128;
+constexpr int kBS = 24;                // row stride of a 16 x 16 bf16 block: ldmatrix without bank conflicts
+constexpr int kBlock = 16 * kBS;       // elements of such a block
+
+// The blocks of N below the diagonal: (1,0), (2,0), (2,1), (3,0), ...
+__host__ __device__ constexpr int low_block(int i, int k) { return i * (i - 1) / 2 + k; }
 
 template <int DKP, int NI, int NM, int NP>
 struct PrepTiles {
     static constexpr int kRow = DKP + kPad;
-    static constexpr int rec = 0;                                 // the record, as it leaves
-    static constexpr int L = (NM + NP) * kSq + 4 * kTok;          // doubles
+    static constexpr int L = 0;                                   // float2: log2 of the decays' prefix, high and low part
     static constexpr int bt = L + 8 * C;                          // beta
-    static constexpr int diag = bt + 4 * C;                       // fp32 [4][16][20]: diagonal blocks of N
-    static constexpr int tiles = diag + 4 * 4 * 16 * 20;
-    static constexpr int kt = tiles;                              // K, Q tiles; then ...
+    static constexpr int tiles = bt + 4 * C;
+    static constexpr int kt = tiles;                              // K, Q tiles; then, over them,
     static constexpr int qt = kt + 2 * NI * C * kRow;
-    static constexpr int np = tiles;                              // ... planes of N below the diagonal blocks
-    static constexpr int tp = np + 2 * 3 * C * kCS;               // and of the E_ii: [3][C][24]
-    static constexpr int end_a = qt + 2 * NI * C * kRow, end_b = tp + 2 * 3 * C * 24;
+    static constexpr int rec = tiles;                             // the record, as it leaves,
+    static constexpr int diag = rec + (NM + NP) * kSq + 4 * kTok; // fp32 [4][16][20]: diagonal blocks of N,
+    static constexpr int np = diag + 4 * 4 * 16 * 20;             // [3 planes][6 blocks] of N below the diagonal,
+    static constexpr int tp = np + 2 * 3 * 6 * kBlock;            // [3 planes][4 blocks] E_ii
+    static constexpr int end_a = qt + 2 * NI * C * kRow, end_b = tp + 2 * 3 * 4 * kBlock;
     static constexpr int bytes = end_a > end_b ? end_a : end_b;
 };
 
@@ -62,8 +67,9 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
                                                             int H, int Hk, int T, int n, unsigned char* __restrict__ records) {
     using Tl = PrepTiles<DKP, NI, NM, NP>;
     extern __shared__ __align__(128) unsigned char smem[];
-    double* L = reinterpret_cast<double*>(smem + Tl::L);
+    float2* L = reinterpret_cast<float2*>(smem + Tl::L);
     float* bt = reinterpret_cast<float*>(smem + Tl::bt);
+    unsigned char* rec = smem + Tl::rec;
     float* diag = reinterpret_cast<float*>(smem + Tl::diag);
     __nv_bfloat16* kt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::kt);
     __nv_bfloat16* qt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::qt);
@@ -80,27 +86,10 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
     load_tile<DKP, NI>(qt, q, hk, t0, tid, kPrepThreads);
     cp_commit();
 
-    if (warp == 0) {  // inclusive prefix of log g in 64 bits: differences of L are taken later
-        double a[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = t0 + 2 * lane + i;
-            float g = 0.f;
-            if (t < T) {
-                if (decay_kind == LA_DECAY_PER_HEAD) g = log_g[h];
-                if (decay_kind == LA_DECAY_PER_STEP) g = log_g[bh * T + t];
-            }
-            a[i] = g < kLogFloor ? kLogFloor : g;
-            bt[2 * lane + i] = t < T ? beta[bh * T + t] : 0.f;
-        }
-        double s = a[0] + a[1];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double x = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += x;
-        }
-        L[2 * lane + 1] = s;
-        L[2 * lane] = s - a[1];
+    if (warp == 0) decay_prefix(L, lane, log_g, decay_kind, h, bh, t0, T);
+    if (tid >= C) {
+        const int t = t0 + tid - C;
+        bt[tid - C] = t < T ? beta[bh * T + t] : 0.f;
     }
     cp_wait<0>();
     __syncthreads();
@@ -130,49 +119,54 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
     __syncthreads();  // the tiles' space becomes N's
 
     if (tid < C) {
-        float* tk = reinterpret_cast<float*>(smem + (NM + NP) * kSq);
-        tk[tid] = expf(static_cast<float>(L[tid]));
-        tk[C + tid] = expf(static_cast<float>(L[C - 1] - L[tid]));
+        float* tk = reinterpret_cast<float*>(rec + (NM + NP) * kSq);
+        tk[tid] = decay_between(L[tid], make_float2(0.f, 0.f));
+        tk[C + tid] = decay_between(L[C - 1], L[tid]);
         tk[2 * C + tid] = bt[tid];
     }
     const int g = lane >> 2, tq = (lane & 3) * 2;
+    const float2 lt[2] = {L[16 * warp + g], L[16 * warp + g + 8]};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         if (j / 2 <= warp) {
+            const int s = 8 * j + tq;
+            const float4 ls = *reinterpret_cast<const float4*>(L + s);
+            const float2 bs = *reinterpret_cast<const float2*>(bt + s);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int t = 16 * warp + g + 8 * r, s = 8 * j + tq;
-                float d0 = 0.f, d1 = 0.f;
-                if (s <= t) d0 = expf(static_cast<float>(L[t] - L[s]));
-                if (s + 1 <= t) d1 = expf(static_cast<float>(L[t] - L[s + 1]));
-                uint32_t p[NP];
-                // masked entries stay zero whatever the scores are there
-                split2<NP>(s <= t ? scale * d0 * qk[j][2 * r] : 0.f, s + 1 <= t ? scale * d1 * qk[j][2 * r + 1] : 0.f, p);
-#pragma unroll
-                for (int i = 0; i < NP; ++i) *reinterpret_cast<uint32_t*>(smem + (NM + i) * kSq + swz64(t, s)) = p[i];
-                const float x = s < t ? d0 * kk[j][2 * r] * bt[s] : 0.f;
-                const float y = s + 1 < t ? d1 * kk[j][2 * r + 1] * bt[s + 1] : 0.f;
-                if (j / 2 == warp) {
-                    *reinterpret_cast<float2*>(diag + (16 * warp + g + 8 * r) * 20 + (s & 15)) = make_float2(x, y);
+                const int t = 16 * warp + g + 8 * r;
+                float d0 = decay_between(lt[r], make_float2(ls.x, ls.y)), d1 = decay_between(lt[r], make_float2(ls.z, ls.w));
+                float p0 = scale * d0 * qk[j][2 * r], p1 = scale * d1 * qk[j][2 * r + 1];
+                float x = d0 * kk[j][2 * r] * bs.x, y = d1 * kk[j][2 * r + 1] * bs.y;
+                if (j / 2 == warp) {  // masked entries are zero whatever the scores are there
+                    p0 = s <= t ? p0 : 0.f;
+                    p1 = s + 1 <= t ? p1 : 0.f;
+                    x = s < t ? x : 0.f;
+                    y = s + 1 < t ? y : 0.f;
+                    *reinterpret_cast<float2*>(diag + t * 20 + (s & 15)) = make_float2(x, y);
                 } else {
                     uint32_t m[3];
                     split2<3>(x, y, m);
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(np + (i * C + t) * kCS + s) = m[i];
+                    for (int i = 0; i < 3; ++i)
+                        *reinterpret_cast<uint32_t*>(np + (i * 6 + low_block(warp, j / 2)) * kBlock + (t & 15) * kBS + (s & 15)) = m[i];
                 }
+                uint32_t p[NP];
+                split2<NP>(p0, p1, p);
+#pragma unroll
+                for (int i = 0; i < NP; ++i) *reinterpret_cast<uint32_t*>(rec + (NM + i) * kSq + swz64(t, s)) = p[i];
             }
         }
-    __syncthreads();
+    __syncwarp();
 
-    if (tid < C) {  // the diagonal blocks: thread = column tid % 16 of block tid / 16
-        const int i0 = tid & ~15, c = tid & 15;
+    if (lane < 16) {  // the diagonal block of this warp's rows: lane = column
         float x[16];
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
-            float a0 = t == c ? 1.f : 0.f, a1 = 0.f;
+            float a0 = t == lane ? 1.f : 0.f, a1 = 0.f;
 #pragma unroll
             for (int s = 0; s < t; s += 2) {
-                const float2 m = *reinterpret_cast<const float2*>(diag + (i0 + t) * 20 + s);
+                const float2 m = *reinterpret_cast<const float2*>(diag + (16 * warp + t) * 20 + s);
                 a0 = fmaf(-m.x, x[s], a0);
                 if (s + 1 < t) a1 = fmaf(-m.y, x[s + 1], a1);
             }
@@ -185,8 +179,8 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 const unsigned short u = static_cast<unsigned short>(p[i]);
-                *reinterpret_cast<unsigned short*>(tp + (i * C + i0 + t) * 24 + c) = u;
-                if (i < NM) *reinterpret_cast<unsigned short*>(smem + i * kSq + swz64(i0 + t, i0 + c)) = u;
+                *reinterpret_cast<unsigned short*>(tp + (i * 4 + warp) * kBlock + t * kBS + lane) = u;
+                if (i < NM) *reinterpret_cast<unsigned short*>(rec + i * kSq + swz64(16 * warp + t, 16 * warp + lane)) = u;
             }
         }
     }
@@ -199,7 +193,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
         for (int i = 0; i < 4; ++i)
             if (i == warp) {
 #pragma unroll
-                for (int p = 0; p < 3; ++p) ldsm4t(col[i][p], smem_addr(tp + (p * C + 16 * i) * 24 + off_cols(lane, 24)));
+                for (int p = 0; p < 3; ++p) ldsm4t(col[i][p], smem_addr(tp + (p * 4 + i) * kBlock + off_cols(lane, kBS)));
             }
 #pragma unroll
         for (int i = 1; i < 4; ++i)
@@ -211,7 +205,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
 #pragma unroll
                         for (int p = 0; p < 3; ++p) {
                             uint32_t r[4];
-                            ldsm4(r, smem_addr(np + (p * C + 16 * i) * kCS + 16 * m + off_cols(lane, kCS)));
+                            ldsm4(r, smem_addr(np + (p * 6 + low_block(i, m)) * kBlock + off_cols(lane, kBS)));
                             mma_planes<3, 3>(acc[0], acc[1], col[m], p, r);
                         }
                     }
@@ -221,7 +215,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
 #pragma unroll
                 for (int p = 0; p < 3; ++p) {
                     uint32_t r[4];
-                    ldsm4(r, smem_addr(tp + (p * C + 16 * i) * 24 + off_cols(lane, 24)));
+                    ldsm4(r, smem_addr(tp + (p * 4 + i) * kBlock + off_cols(lane, kBS)));
                     mma_planes<3, 3>(e[0], e[1], a, p, r);
                 }
 #pragma unroll
@@ -235,7 +229,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
                     for (int y = 0; y < 4; ++y) {
                         // registers: rows (columns of E) 8 (y & 1) .., tokens 8 (y >> 1) ..
                         const uint32_t u = mov_trans(col[i][p][y]);
-                        *reinterpret_cast<uint32_t*>(smem + p * kSq + swz64(16 * i + 8 * (y >> 1) + g, 16 * warp + 8 * (y & 1) + tq)) = u;
+                        *reinterpret_cast<uint32_t*>(rec + p * kSq + swz64(16 * i + 8 * (y >> 1) + g, 16 * warp + 8 * (y & 1) + tq)) = u;
                     }
             }
     }
@@ -243,7 +237,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
     fence_async_smem();
     __syncthreads();
     constexpr long long kRec = record_bytes(NM + NP);
-    if (tid == 0) bulk_store(records + (bh * n + chunk) * kRec, smem_addr(smem), static_cast<uint32_t>(kRec));
+    if (tid == 0) bulk_store(records + (bh * n + chunk) * kRec, smem_addr(rec), static_cast<uint32_t>(kRec));
 }
 
 // ---------------------------------------------------------------- scan

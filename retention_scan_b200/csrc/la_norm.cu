@@ -121,7 +121,7 @@ __device__ __forceinline__ float team_sum(float x, float* red) {
 
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
-__device__ __forceinline__ long long at(const View& v, int i0, int i1, int i2) {
+__device__ __forceinline__ long long at(const View& v, unsigned i0, unsigned i1, unsigned i2) {
     return i0 * v.stride[0] + i1 * v.stride[1] + i2 * v.stride[2];
 }
 
@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(Args a) {
     const bool live = row < a.rows;
     // a warp's shuffles need all its lanes: a team behind the last row repeats it and stores nothing
     const long long rc = live ? row : a.rows - 1;
-    const int i2 = static_cast<int>(rc % a.n[2]), i1 = static_cast<int>(rc / a.n[2] % a.n[1]),
-              i0 = static_cast<int>(rc / a.n[2] / a.n[1]);
+    unsigned i1, i2;
+    const unsigned i0 = a.n1.divmod(a.n2.divmod(static_cast<unsigned>(rc), i2), i1);
     const T* xp = static_cast<const T*>(a.x.data) + at(a.x, i0, i1, i2);
     float x[NV][V], z[NV][V], rs[NV][V];
 #pragma unroll
@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(Args a) {
          first += static_cast<long long>(gridDim.x) * kTeams) {
         const bool live = first + team < a.rows;
         const long long row = live ? first + team : a.rows - 1;
-        const int i2 = static_cast<int>(row % a.n[2]), i1 = static_cast<int>(row / a.n[2] % a.n[1]),
-                  i0 = static_cast<int>(row / a.n[2] / a.n[1]);
+        unsigned i1, i2;
+        const unsigned i0 = a.n1.divmod(a.n2.divmod(static_cast<unsigned>(row), i2), i1);
         const T* xp = static_cast<const T*>(a.x.data) + at(a.x, i0, i1, i2);
         const T* dp = static_cast<const T*>(a.dout.data) + at(a.dout, i0, i1, i2);
         const T* zp = a.gate.data ? static_cast<const T*>(a.gate.data) + at(a.gate, i0, i1, i2) : nullptr;
@@ -416,7 +416,10 @@ size_t backward_workspace_bytes(long long rows, int D) {
     return check::round256(sizeof(float) * static_cast<size_t>(b) * D);
 }
 
-cudaError_t launch(const Args& a, la_dtype dtype, bool backward) {
+cudaError_t launch(const Args& args, la_dtype dtype, bool backward) {
+    Args a = args;
+    a.n1 = FastDiv(static_cast<unsigned>(a.n[1]));
+    a.n2 = FastDiv(static_cast<unsigned>(a.n[2]));
     return dtype == LA_BF16 ? typed<__nv_bfloat16>(a, backward) : typed<float>(a, backward);
 }
 

@@ -62,7 +62,8 @@ __device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
 // One block: tokens t0 .. t0 + tokens - 1 of sequence b, heads h0 .. h0 + per - 1
 // of the two tensors' heads counted through.
 template <typename T, int V, int A, int kLayout>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(Args a, int tokens, int per, int tblocks, int hblocks) {
+__global__ void __launch_bounds__(kThreads) rotary_kernel(Args a, int tokens, int per, int tblocks, int hblocks, FastDiv by_items,
+                                                          FastDiv by_tokens) {
     extern __shared__ float2 cs[];  // [tokens][R / 2]: cos, sin, times mscale
     const int hb = blockIdx.x % hblocks, tb = blockIdx.x / hblocks % tblocks, b = blockIdx.x / hblocks / tblocks;
     const int t0 = tb * tokens, nt = min(tokens, a.T - t0), pairs = a.R / 2;
@@ -82,8 +83,11 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(Args a, int tokens, in
     // Work items of a row: vectors of pairs, then vectors of the copied rest.
     const int turned = kLayout == LA_ROTARY_HALF ? pairs / V : a.R / V, items = turned + (a.D - a.R) / A;
     const int h0 = hb * per, nh = min(per, a.heads[0] + a.heads[1] - h0);
-    for (int i = threadIdx.x; i < nh * nt * items; i += kThreads) {
-        const int item = i % items, t = i / items % nt, hh = h0 + i / items / nt;
+    for (int i = threadIdx.x; i < nh * tokens * items; i += kThreads) {
+        unsigned item_u, t_u;
+        const int hh = h0 + static_cast<int>(by_tokens.divmod(by_items.divmod(i, item_u), t_u));
+        const int item = static_cast<int>(item_u), t = static_cast<int>(t_u);
+        if (t >= nt) continue;  // the last block of a sequence has fewer tokens
         const int w = hh >= a.heads[0], h = w ? hh - a.heads[0] : hh;
         const View& xv = a.x[w];
         const View& ov = a.out[w];
@@ -136,8 +140,10 @@ cudaError_t run(const Args& a) {
     const long long grid = a.B * tblocks * hblocks;
     if (grid > 2147483647LL || tblocks > 2147483647LL) return cudaErrorNotSupported;
     const size_t smem = sizeof(float2) * tokens * pairs;
+    const int items = (kLayout == LA_ROTARY_HALF ? pairs / V : a.R / V) + (a.D - a.R) / A;
     rotary_kernel<T, V, A, kLayout><<<static_cast<unsigned>(grid), kThreads, smem, a.stream>>>(a, tokens, per,
-                                                                                           static_cast<int>(tblocks), hblocks);
+                                                                                           static_cast<int>(tblocks), hblocks,
+                                                                                           FastDiv(items), FastDiv(tokens));
     return cudaGetLastError();
 }
 

@@ -8,7 +8,11 @@ import ctypes
 
 import torch
 
-from . import (DECAY_NONE, DECAY_PER_HEAD, DECAY_PER_STEP, _check, _decay, _dtype_code, _need, _ptr, _stream, lib)
+from . import (DECAY_NONE, DECAY_PER_HEAD, DECAY_PER_STEP, _check, _decay, _device, _dtype_code, _need, _raw_stream, lib)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _heads(q, k, v, beta, decay_kind, log_g, token):
@@ -79,12 +83,12 @@ def delta_forward(q, k, v, beta, decay_kind=DECAY_NONE, log_g=None, init_state=N
         final_state = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
     _need(final_state, "final_state", (B, H, Dk, Dv), torch.float32, dev)
     d = _decay(decay_kind, log_g)
-    with torch.cuda.device(dev):
+    with _device(dev):
         workspace = _scratch(workspace, delta_workspace_size(B, H, T, Dk, Dv, q.dtype, Hk), dev, stream)
         _check(lib().la_delta_forward_ws(
             _ptr(q), _ptr(k), _ptr(v), _ptr(beta), ctypes.byref(d) if d is not None else None, float(q_scale),
             _ptr(init_state), _ptr(out), _ptr(final_state), B, H, Hk, T, Dk, Dv, _dtype_code(q.dtype),
-            _ptr(workspace), workspace.numel(), _stream(stream, dev)))
+            _ptr(workspace), workspace.numel(), _raw_stream(stream, dev)))
     return out, final_state
 
 
@@ -131,13 +135,13 @@ def delta_backward(q, k, v, beta, dy, decay_kind=DECAY_NONE, log_g=None, init_st
             _need(d_log_g, "d_log_g", tuple(log_g.shape), torch.float32, dev)
         _need(d_init, "d_init_state", (B, H, Dk, Dv), torch.float32, dev)
     d = _decay(decay_kind, log_g)
-    with torch.cuda.device(dev):
+    with _device(dev):
         workspace = _scratch(workspace, delta_backward_workspace_size(B, H, T, Dk, Dv, q.dtype, Hk), dev, stream)
         _check(lib().la_delta_backward_ws(
             _ptr(q), _ptr(k), _ptr(v), _ptr(beta), ctypes.byref(d) if d is not None else None, float(q_scale),
             _ptr(init_state), _ptr(dy), _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbeta), _ptr(d_log_g),
             _ptr(d_init), B, H, Hk, T, Dk, Dv, _dtype_code(q.dtype), _ptr(workspace), workspace.numel(),
-            _stream(stream, dev)))
+            _raw_stream(stream, dev)))
     return dq, dk, dv, dbeta, d_log_g, d_init
 
 
@@ -154,8 +158,8 @@ def delta_decode_step(q, k, v, beta, state, decay_kind=DECAY_NONE, log_g=None, q
         out = torch.empty((B, H, Dv), dtype=q.dtype, device=dev)
     _need(out, "out", (B, H, Dv), q.dtype, dev)
     d = _decay(decay_kind, log_g)
-    with torch.cuda.device(dev):
+    with _device(dev):
         _check(lib().la_delta_decode_step(
             _ptr(q), _ptr(k), _ptr(v), _ptr(beta), ctypes.byref(d) if d is not None else None, float(q_scale),
-            _ptr(state), _ptr(out), B, H, Hk, Dk, Dv, _dtype_code(q.dtype), _stream(stream, dev)))
+            _ptr(state), _ptr(out), B, H, Hk, Dk, Dv, _dtype_code(q.dtype), _raw_stream(stream, dev)))
     return out

@@ -727,7 +727,8 @@ LA_API la_status la_delta_decode_step(const void* q, const void* k, const void* 
                                       int H, int Hk, int Dk, int Dv, la_dtype dtype, la_stream_t stream);
 
 /* A view of n0 x n1 x n2 rows of D dense elements: row (i0, i1, i2) starts at
- * data + i0 stride[0] + i1 stride[1] + i2 stride[2] (in elements, >= 0).  So
+ * data + i0 stride[0] + i1 stride[1] + i2 stride[2] (in elements, >= 0; the last two
+ * below 2^32).  So
  * [B,H,T,D] and [B,T,H,D] tensors, slices of a fused projection and broadcast
  * (stride 0) inputs are read where they lie. */
 typedef struct {
@@ -763,7 +764,7 @@ typedef enum {
  *
  * D up to 8192.  n0 n1 n2 == 0 is a no-op.  Errors (synchronous):
  * LA_ERR_INVALID_ARG for a NULL view or data, an address that is not a multiple
- * of the element, negative strides, an output with stride 0 along a
+ * of the element, strides outside their range, an output with stride 0 along a
  * size above 1, bad sizes, kinds or numbers; LA_ERR_UNSUPPORTED for D > 8192 or
  * more than 2^31 - 1 rows; LA_ERR_CUDA if a launch fails.
  */

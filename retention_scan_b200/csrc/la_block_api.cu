@@ -18,6 +18,7 @@ bool read_view(const la_view* v, const int (&n)[3], size_t es, bool output, la::
     to->data = v->data;
     for (int i = 0; i < 3; ++i) {
         if (v->stride[i] < 0 || (output && n[i] > 1 && v->stride[i] == 0)) return false;
+        if (i > 0 && n[i] > 1 && v->stride[i] > UINT_MAX) return false;
         to->stride[i] = v->stride[i];
     }
     return true;

@@ -19,71 +19,15 @@
 
 #include "la_check.h"
 #include "la_norm.h"
+#include "la_rows.cuh"
+#include "la_sm100.cuh"
 
 namespace la {
 namespace norm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxBlocks = 148 * 8;  // of the backward: each keeps one partial sum of dw
-
-template <typename T, int V>
-struct Vec;
-template <>
-struct Vec<__nv_bfloat16, 8> {
-    using raw = uint4;
-};
-template <>
-struct Vec<__nv_bfloat16, 2> {
-    using raw = uint32_t;
-};
-template <>
-struct Vec<__nv_bfloat16, 1> {
-    using raw = unsigned short;
-};
-template <>
-struct Vec<float, 4> {
-    using raw = uint4;
-};
-template <>
-struct Vec<float, 2> {
-    using raw = uint2;
-};
-template <>
-struct Vec<float, 1> {
-    using raw = uint32_t;
-};
-
-template <int V>
-__device__ __forceinline__ void load(const __nv_bfloat16* p, float (&x)[V]) {
-    typename Vec<__nv_bfloat16, V>::raw r = *reinterpret_cast<const typename Vec<__nv_bfloat16, V>::raw*>(p);
-    const __nv_bfloat16* h = reinterpret_cast<const __nv_bfloat16*>(&r);
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = __bfloat162float(h[i]);
-}
-template <int V>
-__device__ __forceinline__ void load(const float* p, float (&x)[V]) {
-    typename Vec<float, V>::raw r = *reinterpret_cast<const typename Vec<float, V>::raw*>(p);
-    const float* h = reinterpret_cast<const float*>(&r);
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = h[i];
-}
-template <int V>
-__device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[V]) {
-    typename Vec<__nv_bfloat16, V>::raw r;
-    __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(&r);
-#pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = __float2bfloat16_rn(x[i]);
-    *reinterpret_cast<typename Vec<__nv_bfloat16, V>::raw*>(p) = r;
-}
-template <int V>
-__device__ __forceinline__ void store(float* p, const float (&x)[V]) {
-    typename Vec<float, V>::raw r;
-    float* h = reinterpret_cast<float*>(&r);
-#pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = x[i];
-    *reinterpret_cast<typename Vec<float, V>::raw*>(p) = r;
-}
+constexpr int kMaxBlocks = 148 * 2;  // of the backward, resident at once: each keeps one partial sum of dw
 
 // V weights; the address is 16-byte aligned wherever V > 1.
 template <int V>
@@ -119,36 +63,48 @@ __device__ __forceinline__ float team_sum(float x, float* red) {
     return x;
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
-
-__device__ __forceinline__ long long at(const View& v, unsigned i0, unsigned i1, unsigned i2) {
-    return i0 * v.stride[0] + i1 * v.stride[1] + i2 * v.stride[2];
+// 1 / (1 + e^-z) with the fast exponential and reciprocal; e^-z beyond the range
+// is infinite and gives 0.
+__device__ __forceinline__ float sigmoid(float z) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-1.4426950408889634f * z)));
+    return r;
 }
 
-// The row's statistics from its values; leaves x - mu in x.
+// The inner strides fit 32 bits (the entry points refuse others): one wide multiply each.
+__device__ __forceinline__ long long at(const View& v, unsigned i0, unsigned i1, unsigned i2) {
+    return i0 * v.stride[0] + static_cast<long long>(static_cast<unsigned long long>(i1) * static_cast<unsigned>(v.stride[1]) +
+                                                     static_cast<unsigned long long>(i2) * static_cast<unsigned>(v.stride[2]));
+}
+
+template <int V>
+__device__ __forceinline__ float lane_sum(const float (&acc)[V]) {
+    float s = acc[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) s += acc[i];
+    return s;
+}
+
+// The row's statistics from its values; leaves x - mu in x.  inv = 1 / D.
 template <int V, int G, int NV>
-__device__ __forceinline__ float normalise(float (&x)[NV][V], int D, int lane, int kind, float eps, float* red) {
+__device__ __forceinline__ float normalise(float (&x)[NV][V], int D, float inv, int lane, int kind, float eps, float* red) {
+    float acc[V];
     if (kind == LA_NORM_LAYER) {
-        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) vfmas(acc, x[u], 1.f, acc);
+        const float mu = team_sum<G>(lane_sum(acc), red) * inv;
 #pragma unroll
         for (int u = 0; u < NV; ++u)
-#pragma unroll
-            for (int i = 0; i < V; ++i) s += x[u][i];
-        const float mu = team_sum<G>(s, red) / D;
-#pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            const bool in = (u * G + lane) * V < D;
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[u][i] = in ? x[u][i] - mu : 0.f;
-        }
+            if ((u * G + lane) * V < D) vshift(x[u], x[u], -mu);  // what lies behind the row stays zero
     }
-    float s = 0.f;
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) s = fmaf(x[u][i], x[u][i], s);
-    s = team_sum<G>(s, red + 8);
-    return rsqrtf((kind == LA_NORM_L2 ? s : s / D) + eps);
+    for (int u = 0; u < NV; ++u) vfma(acc, x[u], x[u], acc);
+    const float s = team_sum<G>(lane_sum(acc), red + 8);
+    return rsqrtf((kind == LA_NORM_L2 ? s : s * inv) + eps);
 }
 
 template <typename T, int V, int G, int NV>
@@ -162,23 +118,18 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(Args a) {
     unsigned i1, i2;
     const unsigned i0 = a.n1.divmod(a.n2.divmod(static_cast<unsigned>(rc), i2), i1);
     const T* xp = static_cast<const T*>(a.x.data) + at(a.x, i0, i1, i2);
-    float x[NV][V], z[NV][V], rs[NV][V];
+    Raw<T, V> xr[NV], zr[NV], rr[NV];
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
         const int c = (u * G + lane) * V;
-        if (c < a.D) {
-            load<V>(xp + c, x[u]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[u][i] = 0.f;
-        }
+        if (c < a.D) xr[u].load(xp + c);
     }
     if (a.gate.data) {
         const T* p = static_cast<const T*>(a.gate.data) + at(a.gate, i0, i1, i2);
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             const int c = (u * G + lane) * V;
-            if (c < a.D) load<V>(p + c, z[u]);
+            if (c < a.D) zr[u].load(p + c);
         }
     }
     if (a.residual.data) {
@@ -186,110 +137,178 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(Args a) {
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             const int c = (u * G + lane) * V;
-            if (c < a.D) load<V>(p + c, rs[u]);
+            if (c < a.D) rr[u].load(p + c);
         }
     }
-    const float r = normalise<V, G, NV>(x, a.D, lane, a.kind, a.eps, red);
+    float x[NV][V];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        if ((u * G + lane) * V < a.D) {
+            xr[u].unpack(x[u]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[u][i] = 0.f;
+        }
+    }
+    const float r = a.scale * normalise<V, G, NV>(x, a.D, a.inv, lane, a.kind, a.eps, red);
     T* op = static_cast<T*>(a.out.data) + at(a.out, i0, i1, i2);
+    const bool silu = a.activation == LA_GATE_SILU;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
         const int c = (u * G + lane) * V;
         if (c < a.D) {
-            float w[V];
-            if (a.weight) load_weight<V>(a.weight + c, w);
-            float o[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float y = a.scale * x[u][i] * r;
-                if (a.weight) y *= w[i];
-                if (a.gate.data) {
-                    const float s = sigmoid(z[u][i]);
-                    y *= a.activation == LA_GATE_SILU ? z[u][i] * s : s;
-                }
-                o[i] = a.residual.data ? rs[u][i] + y : y;
+            vscale(x[u], x[u], r);
+            if (a.weight) {
+                float w[V];
+                load_weight<V>(a.weight + c, w);
+                vmul(x[u], x[u], w);
             }
-            if (live) store<V>(op + c, o);
+            if (a.gate.data) {
+                float z[V], f[V];
+                zr[u].unpack(z);
+#pragma unroll
+                for (int i = 0; i < V; ++i) f[i] = sigmoid(z[i]);
+                if (silu) vmul(f, f, z);
+                vmul(x[u], x[u], f);
+            }
+            if (a.residual.data) {
+                float rs[V];
+                rr[u].unpack(rs);
+                vfmas(x[u], x[u], 1.f, rs);
+            }
+            if (live) store_row<T, V>(op + c, x[u]);
         }
     }
 }
 
 template <typename T, int V, int G, int NV>
-__global__ void __launch_bounds__(kThreads) backward_kernel(Args a) {
-    extern __shared__ float shared[];  // 32 floats, then a partial dw row per team
+__global__ void __launch_bounds__(kThreads, NV * V > 16 ? 1 : 2) backward_kernel(Args a) {
+    extern __shared__ __align__(16) float shared[];  // 32 floats, scale * weight, a partial dw row per team
     float* red = shared;
+    float* ws = shared + 32;
     const int lane = threadIdx.x % G, team = threadIdx.x / G;
     constexpr int kTeams = kThreads / G;
+    for (int c = threadIdx.x; c < a.D; c += kThreads) ws[c] = a.weight ? a.scale * a.weight[c] : a.scale;
+    __syncthreads();
     float dw[NV][V];
 #pragma unroll
     for (int u = 0; u < NV; ++u)
 #pragma unroll
         for (int i = 0; i < V; ++i) dw[u][i] = 0.f;
-    // every team of a block makes the same number of rounds
-    for (long long first = static_cast<long long>(blockIdx.x) * kTeams; first < a.rows;
-         first += static_cast<long long>(gridDim.x) * kTeams) {
-        const bool live = first + team < a.rows;
-        const long long row = live ? first + team : a.rows - 1;
-        unsigned i1, i2;
-        const unsigned i0 = a.n1.divmod(a.n2.divmod(static_cast<unsigned>(row), i2), i1);
-        const T* xp = static_cast<const T*>(a.x.data) + at(a.x, i0, i1, i2);
-        const T* dp = static_cast<const T*>(a.dout.data) + at(a.dout, i0, i1, i2);
-        const T* zp = a.gate.data ? static_cast<const T*>(a.gate.data) + at(a.gate, i0, i1, i2) : nullptr;
-        float x[NV][V], m[NV][V], z[NV][V];
+    const bool silu = a.activation == LA_GATE_SILU;
+    const bool gated = a.gate.data != nullptr;
+    // A team takes a run of neighbouring rows: its addresses move by a stride and
+    // are computed anew only where the innermost index wraps.  Every team makes
+    // the same number of rounds.
+    const unsigned teams = gridDim.x * kTeams, run = static_cast<unsigned>((a.rows + teams - 1) / teams);
+    const long long row0 = static_cast<long long>(blockIdx.x * kTeams + team) * run;
+    unsigned i0, i1, i2;
+    const T *xp, *mp, *zp;
+    T *op, *gp;  // of the row before, whose results are still to come
+    auto place = [&](long long row) {
+        i0 = a.n1.divmod(a.n2.divmod(static_cast<unsigned>(row < a.rows ? row : a.rows - 1), i2), i1);
+        xp = static_cast<const T*>(a.x.data) + at(a.x, i0, i1, i2);
+        mp = static_cast<const T*>(a.dout.data) + at(a.dout, i0, i1, i2);
+        op = static_cast<T*>(a.dx.data) + at(a.dx, i0, i1, i2);
+        if (gated) {
+            zp = static_cast<const T*>(a.gate.data) + at(a.gate, i0, i1, i2);
+            gp = static_cast<T*>(a.dgate.data) + at(a.dgate, i0, i1, i2);
+        }
+    };
+    // The next row is on its way while this one is worked on.
+    Raw<T, V> xr[NV], mr[NV], zr[NV];
+    auto fetch = [&] {
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             const int c = (u * G + lane) * V;
             if (c < a.D) {
-                load<V>(xp + c, x[u]);
-                load<V>(dp + c, m[u]);
-                if (zp) load<V>(zp + c, z[u]);
+                xr[u].load(xp + c);
+                mr[u].load(mp + c);
+                if (gated) zr[u].load(zp + c);
+            }
+        }
+    };
+    place(row0);
+    fetch();
+    for (unsigned k = 0; k < run; ++k) {
+        const bool live = row0 + k < a.rows;
+        float x[NV][V], m[NV][V];
+        Raw<T, V> z_raw[NV];
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            if ((u * G + lane) * V < a.D) {
+                xr[u].unpack(x[u]);
+                mr[u].unpack(m[u]);
+                z_raw[u] = zr[u];
             } else {
 #pragma unroll
                 for (int i = 0; i < V; ++i) x[u][i] = m[u][i] = 0.f;
             }
         }
-        const float r = normalise<V, G, NV>(x, a.D, lane, a.kind, a.eps, red);
-        T* gp = zp && live ? static_cast<T*>(a.dgate.data) + at(a.dgate, i0, i1, i2) : nullptr;
+        T *dxp = op, *dgp = gp;
+        if (row0 + k + 1 < a.rows && k + 1 < run) {
+            if (i2 + 1 < static_cast<unsigned>(a.n[2])) {
+                ++i2;
+                xp += a.x.stride[2];
+                mp += a.dout.stride[2];
+                op += a.dx.stride[2];
+                zp += a.gate.stride[2];
+                gp += a.dgate.stride[2];
+            } else {
+                place(row0 + k + 1);
+            }
+            fetch();
+        }
+        const float r = normalise<V, G, NV>(x, a.D, a.inv, lane, a.kind, a.eps, red);
         float inner = 0.f, sum = 0.f;
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             const int c = (u * G + lane) * V;
             if (c < a.D) {
                 float w[V], dg[V];
-                if (a.weight) load_weight<V>(a.weight + c, w);
+                load_weight<V>(ws + c, w);
+                // m is dout, then dn; dw takes its scale at the end
+                if (gated) {
+                    float z[V];
+                    z_raw[u].unpack(z);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float n = x[u][i] * r, wi = a.weight ? w[i] : 1.f;
-                    float dn = a.scale * m[u][i];
-                    if (zp) {
-                        const float s = sigmoid(z[u][i]);
-                        const bool silu = a.activation == LA_GATE_SILU;
-                        const float da = silu ? s * fmaf(z[u][i], 1.f - s, 1.f) : s * (1.f - s);
-                        dg[i] = dn * n * wi * da;
-                        dn *= silu ? z[u][i] * s : s;
+                    for (int i = 0; i < V; ++i) {
+                        const float s = sigmoid(z[i]), act = silu ? z[i] * s : s, n = x[u][i] * r;
+                        const float t = m[u][i] * w[i];
+                        // silu' = s + z s (1 - s), sigmoid' = s (1 - s)
+                        dg[i] = t * n * fmaf(act, 1.f - s, silu ? s : 0.f);
+                        x[u][i] = n;
+                        dw[u][i] = fmaf(m[u][i] * act, live ? n : 0.f, dw[u][i]);
+                        m[u][i] = t * act;
                     }
-                    if (live) dw[u][i] = fmaf(dn, n, dw[u][i]);
-                    dn *= wi;
-                    x[u][i] = n;
-                    m[u][i] = dn;
-                    inner = fmaf(dn, n, inner);
-                    sum += dn;
+                    if (live) store_row<T, V>(dgp + c, dg);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        x[u][i] *= r;
+                        dw[u][i] = fmaf(m[u][i], live ? x[u][i] : 0.f, dw[u][i]);
+                        m[u][i] *= w[i];
+                    }
                 }
-                if (gp) store<V>(gp + c, dg);
+#pragma unroll
+                for (int i = 0; i < V; ++i) inner = fmaf(m[u][i], x[u][i], inner);
+                if (a.kind == LA_NORM_LAYER) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum += m[u][i];
+                }
             }
         }
         inner = team_sum<G>(inner, red + 16);
-        if (a.kind != LA_NORM_L2) inner /= a.D;
-        sum = a.kind == LA_NORM_LAYER ? team_sum<G>(sum, red + 24) / a.D : 0.f;
+        if (a.kind != LA_NORM_L2) inner *= a.inv;
+        sum = a.kind == LA_NORM_LAYER ? team_sum<G>(sum, red + 24) * a.inv : 0.f;
         if (live) {
-            T* op = static_cast<T*>(a.dx.data) + at(a.dx, i0, i1, i2);
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
                 const int c = (u * G + lane) * V;
                 if (c < a.D) {
-                    float o[V];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) o[i] = r * (m[u][i] - fmaf(x[u][i], inner, sum));
-                    store<V>(op + c, o);
+                    for (int i = 0; i < V; ++i) m[u][i] = r * (m[u][i] - fmaf(x[u][i], inner, sum));
+                    store_row<T, V>(dxp + c, m[u]);
                 }
             }
         }
@@ -303,10 +322,10 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(Args a) {
             const int c = (u * G + lane) * V;
             if (c < a.D)
 #pragma unroll
-                for (int i = 0; i < V; ++i) part[c + i] = dw[u][i];
+                for (int i = 0; i < V; ++i) part[c + i] = a.scale * dw[u][i];
         }
     } else {
-        float* mine = shared + 32 + team * a.D;
+        float* mine = ws + (1 + team) * a.D;
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             const int c = (u * G + lane) * V;
@@ -317,26 +336,26 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(Args a) {
         __syncthreads();
         for (int c = threadIdx.x; c < a.D; c += kThreads) {
             float s = 0.f;
-            for (int t = 0; t < kTeams; ++t) s += shared[32 + t * a.D + c];
-            part[c] = s;
+            for (int t = 0; t < kTeams; ++t) s += ws[(1 + t) * a.D + c];
+            part[c] = a.scale * s;
         }
     }
 }
 
-// dw: the blocks' partial rows, in their order (8 threads a column).
+// dw: the blocks' partial rows, in a fixed order (32 threads a column).
 __global__ void weight_kernel(const float* __restrict__ part, float* __restrict__ dw, int blocks, int D) {
-    __shared__ float red[8][33];
+    __shared__ float red[32][33];
     const int c = blockIdx.x * 32 + threadIdx.x;
     float s = 0.f;
     if (c < D)
-        for (int b = threadIdx.y; b < blocks; b += 8) s += part[static_cast<long long>(b) * D + c];
+        for (int b = threadIdx.y; b < blocks; b += 32) s += part[static_cast<long long>(b) * D + c];
     red[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    if (threadIdx.y == 0 && c < D) {
+    s = red[threadIdx.x][threadIdx.y];  // this warp's column
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += red[i][threadIdx.x];
-        dw[c] = s;
-    }
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int out = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && out < D) dw[out] = s;
 }
 
 int team_blocks(long long rows, int teams) {
@@ -352,25 +371,28 @@ cudaError_t run(const Args& a, bool backward) {
         return cudaGetLastError();
     }
     const int blocks = team_blocks(a.rows, kTeams);
-    const size_t smem = sizeof(float) * (32 + (kTeams > 1 && a.partial ? static_cast<size_t>(kTeams) * a.D : 0));
+    const size_t smem = sizeof(float) * (32 + static_cast<size_t>(kTeams > 1 && a.partial ? 1 + kTeams : 1) * a.D);
     backward_kernel<T, V, G, NV><<<blocks, kThreads, smem, a.stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && a.partial) {
-        weight_kernel<<<(a.D + 31) / 32, dim3(32, 8), 0, a.stream>>>(a.partial, a.dweight, blocks, a.D);
+        weight_kernel<<<(a.D + 31) / 32, dim3(32, 32), 0, a.stream>>>(a.partial, a.dweight, blocks, a.D);
         e = cudaGetLastError();
     }
     return e;
 }
 
-// Threads a row: as few lanes as hold it in one vector each, up to a warp with
-// four (D <= 32 * 4 * V); wider rows take the block, 2 to 64 values a thread.
+// Threads a row: two vectors each, so that a row's index arithmetic and
+// reductions are shared by 16 bf16 elements (forward, B8 H16 T4096 D128: one
+// vector a lane took 38 instructions an element and 122 us, two, with two fp32
+// values an instruction, 19 and 65 us), up to a warp with four; wider rows take
+// the block, 1 to 32 vectors a thread.
 template <typename T, int V>
 cudaError_t teams(const Args& a, bool backward) {
     const int vecs = (a.D + V - 1) / V;
     if (vecs <= 4) return run<T, V, 4, 1>(a, backward);
-    if (vecs <= 8) return run<T, V, 8, 1>(a, backward);
-    if (vecs <= 16) return run<T, V, 16, 1>(a, backward);
-    if (vecs <= 32) return run<T, V, 32, 1>(a, backward);
+    if (vecs <= 8) return run<T, V, 4, 2>(a, backward);
+    if (vecs <= 16) return run<T, V, 8, 2>(a, backward);
+    if (vecs <= 32) return run<T, V, 16, 2>(a, backward);
     if (vecs <= 64) return run<T, V, 32, 2>(a, backward);
     if (vecs <= 128) return run<T, V, 32, 4>(a, backward);
     if (vecs <= 256) return run<T, V, kThreads, 1>(a, backward);
@@ -420,6 +442,7 @@ cudaError_t launch(const Args& args, la_dtype dtype, bool backward) {
     Args a = args;
     a.n1 = FastDiv(static_cast<unsigned>(a.n[1]));
     a.n2 = FastDiv(static_cast<unsigned>(a.n[2]));
+    a.inv = 1.f / static_cast<float>(a.D);
     return dtype == LA_BF16 ? typed<__nv_bfloat16>(a, backward) : typed<float>(a, backward);
 }
 

@@ -46,7 +46,7 @@ struct Args {
     FastDiv n1, n2;               // division by n[1], n[2]
     long long rows;
     int D, kind, activation;
-    float eps, scale;
+    float eps, scale, inv;        // inv: 1 / D
     cudaStream_t stream;
 };
 cudaError_t launch(const Args& a, la_dtype dtype, bool backward);

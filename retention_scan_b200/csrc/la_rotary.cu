@@ -17,40 +17,13 @@
 #include <cstdint>
 
 #include "la_norm.h"
+#include "la_rows.cuh"
 
 namespace la {
 namespace rotary {
 namespace {
 
 constexpr int kThreads = 256;
-
-template <int N>
-struct alignas(N) Bytes {
-    unsigned char b[N];
-};
-
-// V elements in accesses of A.
-template <typename T, int V, int A>
-__device__ __forceinline__ void load(const T* p, float (&x)[V]) {
-#pragma unroll
-    for (int k = 0; k < V; k += A) {
-        const Bytes<A * sizeof(T)> r = *reinterpret_cast<const Bytes<A * sizeof(T)>*>(p + k);
-        const T* h = reinterpret_cast<const T*>(&r);
-#pragma unroll
-        for (int i = 0; i < A; ++i) x[k + i] = static_cast<float>(h[i]);
-    }
-}
-template <typename T, int V, int A>
-__device__ __forceinline__ void store(T* p, const float (&x)[V]) {
-#pragma unroll
-    for (int k = 0; k < V; k += A) {
-        Bytes<A * sizeof(T)> r;
-        T* h = reinterpret_cast<T*>(&r);
-#pragma unroll
-        for (int i = 0; i < A; ++i) h[i] = static_cast<T>(x[k + i]);
-        *reinterpret_cast<Bytes<A * sizeof(T)>*>(p + k) = r;
-    }
-}
 
 // The roundings are spelt out, so that every vector width gives the same bits.
 __device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
@@ -59,66 +32,91 @@ __device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
     a = u;
 }
 
+// Rows (heads) a thread loads before it stores the first: the output may be the
+// input, so the compiler cannot move a load over a store, and one row in flight a
+// thread does not fill HBM's latency.
+constexpr int kBatch = 4;
+
 // One block: tokens t0 .. t0 + tokens - 1 of sequence b, heads h0 .. h0 + per - 1
-// of the two tensors' heads counted through.
+// of the two tensors' heads counted through.  A thread keeps one token's item
+// (V pairs or elements of a row) and its sines and cosines in registers, and
+// walks the heads.
 template <typename T, int V, int A, int kLayout>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(Args a, int tokens, int per, int tblocks, int hblocks, FastDiv by_items,
-                                                          FastDiv by_tokens) {
-    extern __shared__ float2 cs[];  // [tokens][R / 2]: cos, sin, times mscale
+__global__ void __launch_bounds__(kThreads, 2) rotary_kernel(Args a, int tokens, int per, int tblocks, int hblocks, int turned,
+                                                          FastDiv by_items) {
+    constexpr int PV = kLayout == LA_ROTARY_HALF ? V : V / 2;  // pairs of an item
+    extern __shared__ float2 cs[];  // [tokens][PV][turned]: cos, sin, times mscale; a warp's reads are neighbours
     const int hb = blockIdx.x % hblocks, tb = blockIdx.x / hblocks % tblocks, b = blockIdx.x / hblocks / tblocks;
     const int t0 = tb * tokens, nt = min(tokens, a.T - t0), pairs = a.R / 2;
     for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
-        const int t = t0 + i / pairs;
-        const long long pos = a.pos ? a.pos[b * a.pos_stride + t] : a.start + t;
-        const double x = static_cast<double>(pos) * static_cast<double>(a.freq[i % pairs]);
+        const int t = i / pairs, pair = i % pairs;
+        const long long pos = a.pos ? a.pos[b * a.pos_stride + t0 + t] : a.start + t0 + t;
+        const double x = static_cast<double>(pos) * static_cast<double>(a.freq[pair]);
         constexpr double k2Pi = 6.283185307179586477, k2PiLow = 2.449293598294706414e-16;  // 2 pi = their sum
         const double k = rint(x * 0.15915494309189533577);
         const float r = static_cast<float>(fma(-k, k2PiLow, fma(-k, k2Pi, x)));
         float s, c;
         sincosf(r, &s, &c);
-        cs[i] = make_float2(a.mscale * c, a.direction * a.mscale * s);
+        cs[t * pairs + pair % PV * turned + pair / PV] = make_float2(a.mscale * c, a.direction * a.mscale * s);
     }
     __syncthreads();
 
-    // Work items of a row: vectors of pairs, then vectors of the copied rest.
-    const int turned = kLayout == LA_ROTARY_HALF ? pairs / V : a.R / V, items = turned + (a.D - a.R) / A;
-    const int h0 = hb * per, nh = min(per, a.heads[0] + a.heads[1] - h0);
-    for (int i = threadIdx.x; i < nh * tokens * items; i += kThreads) {
-        unsigned item_u, t_u;
-        const int hh = h0 + static_cast<int>(by_tokens.divmod(by_items.divmod(i, item_u), t_u));
-        const int item = static_cast<int>(item_u), t = static_cast<int>(t_u);
-        if (t >= nt) continue;  // the last block of a sequence has fewer tokens
-        const int w = hh >= a.heads[0], h = w ? hh - a.heads[0] : hh;
-        const View& xv = a.x[w];
-        const View& ov = a.out[w];
-        const T* x = static_cast<const T*>(xv.data) + b * xv.stride[0] + h * xv.stride[1] + (t0 + t) * xv.stride[2];
-        T* o = static_cast<T*>(ov.data) + b * ov.stride[0] + h * ov.stride[1] + (t0 + t) * ov.stride[2];
-        const float2* c = cs + t * pairs;
-        if (item >= turned) {
-            const int at = a.R + (item - turned) * A;
-            float y[A];
-            load<T, A, A>(x + at, y);
-            store<T, A, A>(o + at, y);
-        } else if constexpr (kLayout == LA_ROTARY_HALF) {
-            const int at = item * V;
-            float p[V], q[V];
-            load<T, V, A>(x + at, p);
-            load<T, V, A>(x + at + pairs, q);
+    const int combos = nt * static_cast<int>(by_items.d), lanes = min(combos, kThreads);
+    const int step = kThreads / lanes, first = threadIdx.x / lanes;
+    if (first >= step) return;
+    const int h0 = hb * per, h1 = min(h0 + per, a.heads[0] + a.heads[1]);
+    constexpr bool kHalf = kLayout == LA_ROTARY_HALF;
+    for (int i = threadIdx.x % lanes; i < combos; i += lanes) {
+        unsigned item;
+        const int t = static_cast<int>(by_items.divmod(i, item));
+        const bool turns = static_cast<int>(item) < turned;
+        float2 k[PV];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                turn(p[j], q[j], c[at + j]);
-            }
-            store<T, V, A>(o + at, p);
-            store<T, V, A>(o + at + pairs, q);
-        } else {
-            const int at = item * V;
-            float p[V];
-            load<T, V, A>(x + at, p);
+        for (int j = 0; j < PV; ++j) k[j] = turns ? cs[t * pairs + j * turned + item] : make_float2(1.f, 0.f);
+        const int at = turns ? static_cast<int>(item) * V : a.R + (static_cast<int>(item) - turned) * V;
+        // an odd rest: the last item copies one element (single accesses only)
+        const bool whole = A == V || at + V <= a.D;
+        auto row = [&](const View (&v)[2], int h) {
+            const int w = h >= a.heads[0];
+            return static_cast<T*>(v[w].data) + b * v[w].stride[0] + (h - (w ? a.heads[0] : 0)) * v[w].stride[1] +
+                   (t0 + t) * v[w].stride[2] + at;
+        };
+        for (int h = h0 + first; h < h1; h += kBatch * step) {
+            Raw<T, V, A> p[kBatch], q[kHalf ? kBatch : 1];
 #pragma unroll
-            for (int j = 0; j < V; j += 2) {
-                turn(p[j], p[j + 1], c[(at + j) / 2]);
-            }
-            store<T, V, A>(o + at, p);
+            for (int u = 0; u < kBatch; ++u)
+                if (h + u * step < h1) {
+                    const T* r = row(a.x, h + u * step);
+                    if (whole)
+                        p[u].load(r);
+                    else
+                        *reinterpret_cast<T*>(&p[u].r[0]) = *r;
+                    if (kHalf && turns) q[kHalf ? u : 0].load(r + pairs);
+                }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (h + u * step < h1) {
+                    T* r = row(a.out, h + u * step);
+                    if (turns) {
+                        float y[V];
+                        p[u].unpack(y);
+                        if constexpr (kHalf) {
+                            float z[V];
+                            q[u].unpack(z);
+#pragma unroll
+                            for (int j = 0; j < V; ++j) turn(y[j], z[j], k[j]);
+                            store_row<T, V, A>(r + pairs, z);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < V; j += 2) turn(y[j], y[j + 1], k[j / 2]);
+                        }
+                        store_row<T, V, A>(r, y);
+                    } else if (whole) {
+                        p[u].store(r);
+                    } else {
+                        *r = *reinterpret_cast<const T*>(&p[u].r[0]);
+                    }
+                }
         }
     }
 }
@@ -140,10 +138,9 @@ cudaError_t run(const Args& a) {
     const long long grid = a.B * tblocks * hblocks;
     if (grid > 2147483647LL || tblocks > 2147483647LL) return cudaErrorNotSupported;
     const size_t smem = sizeof(float2) * tokens * pairs;
-    const int items = (kLayout == LA_ROTARY_HALF ? pairs / V : a.R / V) + (a.D - a.R) / A;
-    rotary_kernel<T, V, A, kLayout><<<static_cast<unsigned>(grid), kThreads, smem, a.stream>>>(a, tokens, per,
-                                                                                           static_cast<int>(tblocks), hblocks,
-                                                                                           FastDiv(items), FastDiv(tokens));
+    const int turned = kLayout == LA_ROTARY_HALF ? pairs / V : a.R / V;
+    rotary_kernel<T, V, A, kLayout><<<static_cast<unsigned>(grid), kThreads, smem, a.stream>>>(
+        a, tokens, per, static_cast<int>(tblocks), hblocks, turned, FastDiv(turned + (a.D - a.R + V - 1) / V));
     return cudaGetLastError();
 }
 

@@ -59,8 +59,8 @@ class _Prologue(ctypes.Structure):
     _fields_ = [("feature_map", ctypes.c_int), ("q_scale", ctypes.c_float)]
 
 
-class _View(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_longlong * 3)]
+class _View(ctypes.Structure):  # la_view: its three strides one by one
+    _fields_ = [("data", ctypes.c_void_p)] + [(f"stride{i}", ctypes.c_longlong) for i in range(3)]
 
 
 _lib = None

@@ -15,9 +15,6 @@ import torch
 from . import (GATE_SIGMOID, GATE_SILU, NORM_L2, NORM_LAYER, NORM_RMS, ROTARY_HALF, ROTARY_INTERLEAVED, _check, _device,
                _dtype_code, _need, _raw_stream, _View, lib)
 
-_Strides = ctypes.c_longlong * 3
-
-
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -32,12 +29,14 @@ def _view(t, name, shape, dtype, device, output=False):
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    lead, n = t.stride(), len(shape)
+    if lead[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be dense")
-    lead = [s if n > 1 else 0 for n, s in zip(t.shape[:-1], t.stride())]
-    if output and 0 in lead and any(n > 1 and s == 0 for n, s in zip(t.shape[:-1], lead)):
+    if output and 0 in lead and any(k > 1 and s == 0 for k, s in zip(shape[:-1], lead)):
         raise ValueError(f"{name}: an output's rows must not share memory")
-    return _View(t.data_ptr(), _Strides(*([0] * (3 - len(lead)) + lead)))
+    if n == 4:
+        return _View(t.data_ptr(), lead[0], lead[1], lead[2])
+    return _View(t.data_ptr(), *([0] * (4 - n)), *lead[:-1])
 
 
 def _ref(v):
@@ -51,8 +50,7 @@ def _rows(x, name="x"):
         raise ValueError(f"{name}: expected a CUDA tensor, got {x.device}")
     if x.shape[-1] < 1:
         raise ValueError(f"{name}: the last dimension is empty")
-    lead = list(x.shape[:-1])
-    return [1] * (3 - len(lead)) + lead
+    return (1,) * (4 - x.dim()) + tuple(x.shape[:-1])
 
 
 def gated_norm(x, gate=None, weight=None, residual=None, kind=NORM_RMS, activation=GATE_SILU, eps=1e-5, scale=1.0,
@@ -67,13 +65,14 @@ def gated_norm(x, gate=None, weight=None, residual=None, kind=NORM_RMS, activati
     contiguous tensor of x's shape unless given; it may be x, gate or residual
     itself)."""
     n = _rows(x)
-    dev, D = x.device, x.shape[-1]
-    code = _dtype_code(x.dtype)
+    dev, shape, dtype = x.device, x.shape, x.dtype
+    D, code = shape[-1], _dtype_code(dtype)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    xv = _view(x, "x", x.shape, x.dtype, dev)
-    gv, rv = (_view(t, name, x.shape, x.dtype, dev) for t, name in ((gate, "gate"), (residual, "residual")))
-    ov = _view(out, "out", x.shape, x.dtype, dev, output=True)
+        out = x.new_empty(shape)
+    xv = _view(x, "x", shape, dtype, dev)
+    gv = _view(gate, "gate", shape, dtype, dev)
+    rv = _view(residual, "residual", shape, dtype, dev)
+    ov = _view(out, "out", shape, dtype, dev, output=True)
     _need(weight, "weight", (D,), torch.float32, dev)
     with _device(dev):
         _check(lib().la_gated_norm(_ref(xv), _ref(gv), _ptr(weight), _ref(rv), _ref(ov), *n, D, int(kind), int(activation),
@@ -156,7 +155,7 @@ def rotary(x, freq, positions=None, x2=None, start=0, layout=ROTARY_HALF, mscale
         raise ValueError("out2 without x2")
     pstride = 0
     if positions is not None:
-        if tuple(positions.shape) not in ((T,), (B, T)):
+        if positions.shape != (B, T) and positions.shape != (T,):
             raise ValueError(f"positions: expected shape {(T,)} or {(B, T)}, got {tuple(positions.shape)}")
         if positions.dtype != torch.int64:
             raise TypeError(f"positions: expected int64, got {positions.dtype}")
@@ -167,13 +166,13 @@ def rotary(x, freq, positions=None, x2=None, start=0, layout=ROTARY_HALF, mscale
         if start != 0:
             raise ValueError("start applies only without positions")
         pstride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    shape, shape2, dtype = (B, H, T, D), (B, H2, T, D), x.dtype
     if out is None:
-        out = torch.empty((B, H, T, D), dtype=x.dtype, device=dev)
+        out = x.new_empty(shape)
     if out2 is None and x2 is not None:
-        out2 = torch.empty((B, H2, T, D), dtype=x.dtype, device=dev)
-    xv, ov = _view(x, "x", (B, H, T, D), x.dtype, dev), _view(out, "out", (B, H, T, D), x.dtype, dev, output=True)
-    xv2 = _view(x2, "x2", (B, H2, T, D), x.dtype, dev)
-    ov2 = _view(out2, "out2", (B, H2, T, D), x.dtype, dev, output=True)
+        out2 = x.new_empty(shape2)
+    xv, ov = _view(x, "x", shape, dtype, dev), _view(out, "out", shape, dtype, dev, output=True)
+    xv2, ov2 = _view(x2, "x2", shape2, dtype, dev), _view(out2, "out2", shape2, dtype, dev, output=True)
     with _device(dev):
         _check(lib().la_rotary(_ref(xv), H, _ref(xv2), H2, _ref(ov), _ref(ov2), _ptr(freq), _ptr(positions), pstride,
                                int(start), B, T, D, R, int(layout), float(mscale), int(bool(backward)), code,

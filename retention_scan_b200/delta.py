@@ -19,32 +19,33 @@ def _heads(q, k, v, beta, decay_kind, log_g, token):
     """Sizes (B, H, Hk, T, Dk, Dv) after the shape, dtype and device checks;
     token: one-token tensors, without the T dimension."""
     want = 3 if token else 4
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        if t.dim() != want:
-            raise ValueError(f"{name}: expected {want} dimensions, got shape {tuple(t.shape)}")
+    if q.dim() != want or k.dim() != want or v.dim() != want:
+        raise ValueError(f"q, k, v: expected {want} dimensions, got {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
     if not q.is_cuda:
         raise ValueError(f"q: expected a CUDA tensor, got {q.device}")
-    B, Hk, Dk = q.shape[0], q.shape[1], q.shape[-1]
-    H, Dv = v.shape[1], v.shape[-1]
-    T = () if token else (q.shape[2],)
-    if H and (Hk == 0 or H % Hk):
-        raise ValueError(f"v has {H} heads, which is not a multiple of q's {Hk}")
-    _dtype_code(q.dtype)
     if beta is None:
         raise ValueError("beta is required")
-    if decay_kind != DECAY_NONE and log_g is None:
-        raise ValueError("log_g is required for a per-head or per-step decay")
-    _need(q, "q", (B, Hk, *T, Dk), q.dtype, q.device)
-    _need(k, "k", (B, Hk, *T, Dk), q.dtype, q.device)
-    _need(v, "v", (B, H, *T, Dv), q.dtype, q.device)
-    _need(beta, "beta", (B, H, *T), torch.float32, q.device)
-    if decay_kind == DECAY_PER_HEAD:
-        _need(log_g, "log_g", (H,), torch.float32, q.device)
-    elif decay_kind == DECAY_PER_STEP:
-        _need(log_g, "log_g", (B, H, *T), torch.float32, q.device)
-    elif decay_kind != DECAY_NONE:
-        raise ValueError(f"unknown decay kind {decay_kind}")
-    return B, H, Hk, (1 if token else T[0]), Dk, Dv
+    shape, vshape, dev, dtype = q.shape, v.shape, q.device, q.dtype
+    B, Hk, Dk = shape[0], shape[1], shape[-1]
+    H, Dv = vshape[1], vshape[-1]
+    if H and (Hk == 0 or H % Hk):
+        raise ValueError(f"v has {H} heads, which is not a multiple of q's {Hk}")
+    _dtype_code(dtype)
+    per_token = vshape[:-1]
+    _need(q, "q", shape, dtype, dev)
+    _need(k, "k", shape, dtype, dev)
+    _need(v, "v", (B, H, Dv) if token else (B, H, shape[2], Dv), dtype, dev)
+    _need(beta, "beta", per_token, torch.float32, dev)
+    if decay_kind != DECAY_NONE:
+        if log_g is None:
+            raise ValueError("log_g is required for a per-head or per-step decay")
+        if decay_kind == DECAY_PER_STEP:
+            _need(log_g, "log_g", per_token, torch.float32, dev)
+        elif decay_kind == DECAY_PER_HEAD:
+            _need(log_g, "log_g", (H,), torch.float32, dev)
+        else:
+            raise ValueError(f"unknown decay kind {decay_kind}")
+    return B, H, Hk, (1 if token else shape[2]), Dk, Dv
 
 
 def _scratch(workspace, nbytes, dev, stream):
@@ -77,8 +78,9 @@ def delta_forward(q, k, v, beta, decay_kind=DECAY_NONE, log_g=None, init_state=N
     dev = q.device
     _need(init_state, "init_state", (B, H, Dk, Dv), torch.float32, dev)
     if out is None:
-        out = torch.empty((B, H, T, Dv), dtype=q.dtype, device=dev)
-    _need(out, "out", (B, H, T, Dv), q.dtype, dev)
+        out = torch.empty_like(v)
+    else:
+        _need(out, "out", v.shape, q.dtype, dev)
     if final_state is None and return_final:
         final_state = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
     _need(final_state, "final_state", (B, H, Dk, Dv), torch.float32, dev)
@@ -155,8 +157,9 @@ def delta_decode_step(q, k, v, beta, state, decay_kind=DECAY_NONE, log_g=None, q
         raise ValueError("state is required")
     _need(state, "state", (B, H, Dk, Dv), torch.float32, dev)
     if out is None:
-        out = torch.empty((B, H, Dv), dtype=q.dtype, device=dev)
-    _need(out, "out", (B, H, Dv), q.dtype, dev)
+        out = torch.empty_like(v)
+    else:
+        _need(out, "out", v.shape, q.dtype, dev)
     d = _decay(decay_kind, log_g)
     with _device(dev):
         _check(lib().la_delta_decode_step(

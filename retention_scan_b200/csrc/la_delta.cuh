@@ -288,24 +288,24 @@ __device__ __forceinline__ void values_to_global(const float (&x)[8][4], float* 
 // S^T in accumulator tiles (s[j]: columns 8 j .. 8 j + 7 of Dk) from and to a
 // [Dk][Dv] fp32 state.
 template <int DKP>
-__device__ __forceinline__ void state_load(float (&s)[DKP / 8][4], const float* S, int Dk, int Dv, int v0, int lane) {
+__device__ __forceinline__ void state_load(float (&s)[DKP / 8][4], const float* S, int Dk, int Dv, int v0, int lane, int d0 = 0) {
     const int g = lane >> 2, tq = (lane & 3) * 2;
 #pragma unroll
     for (int j = 0; j < DKP / 8; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int d = 8 * j + tq + (i & 1), v = v0 + g + (i >> 1) * 8;
+            const int d = d0 + 8 * j + tq + (i & 1), v = v0 + g + (i >> 1) * 8;
             s[j][i] = S && d < Dk && v < Dv ? S[d * Dv + v] : 0.f;
         }
 }
 template <int DKP>
-__device__ __forceinline__ void state_store(const float (&s)[DKP / 8][4], float* S, int Dk, int Dv, int v0, int lane) {
+__device__ __forceinline__ void state_store(const float (&s)[DKP / 8][4], float* S, int Dk, int Dv, int v0, int lane, int d0 = 0) {
     const int g = lane >> 2, tq = (lane & 3) * 2;
 #pragma unroll
     for (int j = 0; j < DKP / 8; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int d = 8 * j + tq + (i & 1), v = v0 + g + (i >> 1) * 8;
+            const int d = d0 + 8 * j + tq + (i & 1), v = v0 + g + (i >> 1) * 8;
             if (d < Dk && v < Dv) S[d * Dv + v] = s[j][i];
         }
 }
@@ -360,7 +360,7 @@ __device__ __forceinline__ float decay_between(float2 t, float2 s) { return ex2_
 // ---------------------------------------------------------------- the scans' pipeline
 // Shared memory of one stage: the chunk's K (and Q) tiles as 64-column panels,
 // the record's matrices and factors, the warps' value tiles.
-template <int DKP, int NI, int kPlanes, int NW, bool kQ, bool kV>
+template <int DKP, int NI, int kPlanes, int NW, bool kQ, bool kV, int kExtra = 0>
 struct ScanTiles {
     static constexpr int kPanels = (DKP + 63) / 64;
     static constexpr int kTile = kPanels * 8192;  // one plane of K or Q
@@ -370,9 +370,10 @@ struct ScanTiles {
     static constexpr int tok = rec + kPlanes * kSq;
     static constexpr int v = tok + 1024;
     static constexpr int bytes = (v + (kV ? 2048 * NW : 0) + 1023) / 1024 * 1024;
-    static constexpr int kMost = (227 * 1024 - 1024 - 256) / bytes;
+    static constexpr int kMost = (227 * 1024 - 1024 - 256 - kExtra) / bytes;
     static constexpr int stages = kMost > 3 ? 3 : kMost;
-    static constexpr int smem = 1024 + stages * bytes + 256;  // alignment, stages, barriers
+    static constexpr int extra = stages * bytes + 256;                 // behind the stages and their barriers
+    static constexpr int smem = 1024 + extra + kExtra;                 // and the base's alignment
     static_assert(stages >= 1, "a chunk's tiles have to fit an SM");
 };
 
@@ -393,7 +394,7 @@ struct Feed {
     const CUtensorMap *mk, *mq, *mv;
     const unsigned char* records;  // of this (b, h)
     long long rec_bytes;
-    int rec_used, hk, planes_apart, bh, v0, nv;
+    int rec_used, hk, planes_apart, bh, v0, nv, warps;  // nv: value tiles, warps: those that read a stage
 
     __device__ __forceinline__ void issue(uint32_t base, Ring<Tl::stages>* ring, int s, int c) const {
         uint64_t* bar = &ring->full[s];
@@ -450,7 +451,7 @@ __device__ __forceinline__ void release_stage(const F& feed, uint32_t base, Ring
         __threadfence_block();  // this warp's reads come before the count
         if (atomicSub(&ring->left[s], 1) == 1) {
             __threadfence_block();  // and every other's before the copies
-            ring->left[s] = feed.nv;
+            ring->left[s] = feed.warps;
             if (next >= 0 && *static_cast<volatile int*>(&ring->abort) == 0) {
                 fence_async_smem();
                 feed.issue(base, ring, s, next);
@@ -464,7 +465,7 @@ __device__ __forceinline__ void start_ring(const F& feed, uint32_t base, Ring<Tl
     if (threadIdx.x == 0) {
         for (int s = 0; s < Tl::stages; ++s) {
             mbar_init(&ring->full[s], 1);
-            ring->left[s] = feed.nv;
+            ring->left[s] = feed.warps;
             ring->issued[s] = 0;
         }
         ring->abort = 0;
@@ -473,6 +474,115 @@ __device__ __forceinline__ void start_ring(const F& feed, uint32_t base, Ring<Tl
         for (int s = 0; s < Tl::stages && s < n; ++s) feed.issue(base, ring, s, first + s * step);
     }
     __syncthreads();
+}
+
+// ---------------------------------------------------------------- two warps a slice
+// Where a warp per slice leaves tensor cores idle, two share one.  Warp `half`
+// has half of the key width of S^T in its accumulators and two of the chunk's
+// four 16-token blocks, {0, 3} or {1, 2}, which have the same share of the
+// triangular products.  What one needs of the other (split operands) passes
+// through shared memory in register order, a 16-byte access a lane.
+__device__ __forceinline__ int pair_block(int half, int j) { return half ? 1 + j : 3 * j; }
+
+// Planes [N][32 lanes] of an A operand.
+template <int N>
+__device__ __forceinline__ void put_planes(uint4* at, int lane, const uint32_t (&a)[N][4]) {
+#pragma unroll
+    for (int p = 0; p < N; ++p) at[p * 32 + lane] = make_uint4(a[p][0], a[p][1], a[p][2], a[p][3]);
+}
+template <int N>
+__device__ __forceinline__ void get_planes(const uint4* at, int lane, uint32_t (&a)[N][4]) {
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        const uint4 x = at[p * 32 + lane];
+        a[p][0] = x.x;
+        a[p][1] = x.y;
+        a[p][2] = x.z;
+        a[p][3] = x.w;
+    }
+}
+
+// The pair's barrier (64 threads).  It is reached by both warps or, once a wait
+// gave up, by neither: pair_agree() ends both.
+__device__ __forceinline__ void pair_sync(int slice) { asm volatile("bar.sync %0, 64;" ::"r"(1 + slice) : "memory"); }
+__device__ __forceinline__ bool pair_agree(int slice, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "bar.red.and.pred q, %1, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(all)
+        : "r"(1 + slice), "r"(ok ? 1u : 0u)
+        : "memory");
+    return all != 0;
+}
+
+// Byte offset, within a K or Q tile's row band, of k-step d of the `half`th half
+// of the key width, from the lane's offset of k-step d of the first half.
+template <int DKP>
+__device__ __forceinline__ uint32_t half_step(uint32_t o, int half) {
+    return DKP == 128 ? o + 8192 * half : o ^ (half * DKP);  // DKP / 2 columns of 2 bytes, within the swizzle
+}
+
+// One 16-token block in accumulator layout, from the warp's tile or (fp32) from global memory ...
+__device__ __forceinline__ void block_from_tile(float (&x)[2][4], uint32_t tile, int block, int lane) {
+    uint32_t r[4];
+    ldsm4t(r, tile + 512 * block + (lane & 15) * 32 + (lane >> 4) * 16);
+    x[0][0] = low_of(r[0]);
+    x[0][1] = high_of(r[0]);
+    x[1][0] = low_of(r[1]);
+    x[1][1] = high_of(r[1]);
+    x[0][2] = low_of(r[2]);
+    x[0][3] = high_of(r[2]);
+    x[1][2] = low_of(r[3]);
+    x[1][3] = high_of(r[3]);
+}
+__device__ __forceinline__ void block_from_global(float (&x)[2][4], const float* base, int t0, int T, int Dv, int v0, int lane) {
+    const int g = lane >> 2, tq = (lane & 3) * 2;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = t0 + 8 * j + tq + (i & 1), v = v0 + g + (i >> 1) * 8;
+            x[j][i] = t < T && v < Dv ? base[static_cast<long long>(t) * Dv + v] : 0.f;
+        }
+}
+// ... and back.
+__device__ __forceinline__ void block_to_global(const float (&x)[2][4], __nv_bfloat16* base, int t0, int T, int Dv, int v0,
+                                                int lane) {
+    const int g = lane >> 2, tq = (lane & 3) * 2;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t lo = mov_trans(pack(x[j][0], x[j][1])), hi = mov_trans(pack(x[j][2], x[j][3]));
+        const int t = t0 + 8 * j + g;
+        if (t < T) {
+            __nv_bfloat16* p = base + static_cast<long long>(t) * Dv + v0 + tq;
+            *reinterpret_cast<uint32_t*>(p) = lo;
+            *reinterpret_cast<uint32_t*>(p + 8) = hi;
+        }
+    }
+}
+__device__ __forceinline__ void block_to_global(const float (&x)[2][4], float* base, int t0, int T, int Dv, int v0, int lane) {
+    const int g = lane >> 2, tq = (lane & 3) * 2;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = t0 + 8 * j + tq + (i & 1), v = v0 + g + (i >> 1) * 8;
+            if (t < T && v < Dv) base[static_cast<long long>(t) * Dv + v] = x[j][i];
+        }
+}
+// x[j] *= f of the block's tokens (f: the chunk's factors)
+__device__ __forceinline__ void block_scale(float (&x)[2][4], const float* f, int block, int tq, float s = 1.f) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const float2 m = *reinterpret_cast<const float2*>(f + 16 * block + 8 * j + tq);
+        x[j][0] *= s * m.x;
+        x[j][1] *= s * m.y;
+        x[j][2] *= s * m.x;
+        x[j][3] *= s * m.y;
+    }
 }
 
 }  // namespace delta

@@ -14,23 +14,27 @@ bool supports(int Dk, int Dv, la_dtype dtype) {
     return dtype == LA_F32 || (Dk % 16 == 0 && Dv % 16 == 0);
 }
 
-// Value slices (16 columns, one warp each) per block of the scans.  A block
-// fills an SM's shared memory, so blocks beyond the SMs run in another round;
-// up to four warps have a tensor core each, eight share them and take about
-// 1.7 times as long.  The fewest rounds win, then the wider block.
-static int scan_warps(long long BH, int slices) {
-    int best = 1;
+// Blocks of the scans.  A block fills an SM's shared memory, so blocks beyond the
+// SMs run in another round.  Few slices (16 value columns of a (b, h)): two warps
+// each, one or two slices a block, one round.  Else a warp each: up to four have a
+// tensor core of their own, eight share them and take about 1.7 times as long;
+// the fewest rounds win, then the wider block.
+static void plan_scan(Plan* p) {
+    const int slices = p->DVP / 16;
+    p->pair = true;
+    for (p->warps = 1; p->warps <= 2; ++p->warps)
+        if (p->BH * ((slices + p->warps - 1) / p->warps) <= 148) return;
+    p->pair = false;
     double least = 0;
     for (int w = 1; w <= 8; w *= 2) {
         if (w > 1 && w / 2 >= slices) break;
-        const long long blocks = BH * ((slices + w - 1) / w);
+        const long long blocks = p->BH * ((slices + w - 1) / w);
         const double t = static_cast<double>((blocks + 147) / 148) * (w == 8 ? 1.7 : 1.0);
         if (w == 1 || t <= least) {
-            best = w;
+            p->warps = w;
             least = t;
         }
     }
-    return best;
 }
 
 static bool make_map(CUtensorMap* map, const void* base, int width, long long rows, long long outer, long long row_elems,
@@ -60,7 +64,7 @@ Plan make_plan(const Args& a, bool backward, void* workspace) {
     p.n = static_cast<int>((static_cast<long long>(a.T) + C - 1) / C);
     p.DKP = a.Dk <= 32 ? 32 : a.Dk <= 64 ? 64 : 128;
     p.DVP = (a.Dv + 15) / 16 * 16;
-    p.warps = scan_warps(p.BH, p.DVP / 16);
+    plan_scan(&p);
     const bool f32 = a.dtype == LA_F32;
     const size_t nm = f32 ? 3 : 2, np = f32 ? 3 : backward ? 2 : 1, bf = sizeof(__nv_bfloat16);
     const size_t chunks = static_cast<size_t>(p.BH) * p.n, keys = static_cast<size_t>(a.B) * a.Hk;

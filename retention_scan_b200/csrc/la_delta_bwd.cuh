@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(32 * NW) reverse_kernel(const __grid_constant_
     feed.bh = bh;
     feed.v0 = vb;
     feed.nv = nv;
+    feed.warps = nv;
     start_ring<Tl>(feed, base, ring, a.n, a.n - 1, -1);
     if (warp >= nv) return;
 
@@ -221,6 +222,218 @@ __global__ void __launch_bounds__(32 * NW) reverse_kernel(const __grid_constant_
         release_stage<Tl>(feed, base, ring, stage, c - kS);
     }
     if (a.d_init) state_store<DKP>(S, a.d_init + static_cast<long long>(bh) * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane);
+}
+
+// The same with two warps a slice (la_delta.cuh).  dY is read by both; the
+// halves of dS, diag(beta) dU and diag(e^L) dR are exchanged.
+template <int DKP, int NM>
+struct RevSpace {  // a slice's exchange, in 16-byte words
+    static constexpr int kHalf = DKP / 32;
+    static constexpr int s = 0;                        // [2][kHalf][NM][32]
+    static constexpr int u = s + 2 * kHalf * NM * 32;  // [2][2][NM][32]
+    static constexpr int w = u + 2 * 2 * NM * 32;
+    static constexpr int words = w + 2 * 2 * NM * 32;
+};
+
+template <int DKP, int NI, int NM, int NS, typename TIn>
+__global__ void __launch_bounds__(64 * NS) pair_reverse_kernel(const __grid_constant__ CUtensorMap mk,
+                                                               const __grid_constant__ CUtensorMap mq,
+                                                               const __grid_constant__ CUtensorMap my, RevArgs a) {
+    constexpr bool kF32 = sizeof(TIn) == 4;
+    using Ex = RevSpace<DKP, NM>;
+    using Tl = ScanTiles<DKP, NI, 2 * NM, NS, true, !kF32, 16 * Ex::words * NS>;
+    constexpr int kS = Tl::stages, kHalf = Ex::kHalf;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+    unsigned char* smem = smem_raw + (base - smem_addr(smem_raw));
+    Ring<kS>* ring = reinterpret_cast<Ring<kS>*>(smem + kS * Tl::bytes);
+    const int tid = threadIdx.x, lane = tid & 31, slice = tid >> 6, half = (tid >> 5) & 1;
+    uint4* ex = reinterpret_cast<uint4*>(smem + Tl::extra) + slice * Ex::words;
+    const int bh = blockIdx.x / a.vblocks;
+    const int vb = blockIdx.x % a.vblocks * 16 * NS, v0 = vb + 16 * slice;
+    const int nv = min(NS, (a.Dv - vb + 15) / 16);
+    const int b = bh / a.H, h = bh % a.H;
+    Feed<Tl, NI, true, !kF32> feed;
+    feed.mk = &mk;
+    feed.mq = &mq;
+    feed.mv = &my;
+    feed.rec_bytes = record_bytes(2 * NM);
+    feed.records = a.records + static_cast<long long>(bh) * a.n * feed.rec_bytes;
+    feed.rec_used = 2 * NM * kSq;
+    feed.hk = b * a.Hk + h / (a.H / a.Hk);
+    feed.planes_apart = a.planes_apart;
+    feed.bh = bh;
+    feed.v0 = vb;
+    feed.nv = nv;
+    feed.warps = 2 * nv;
+    start_ring<Tl>(feed, base, ring, a.n, a.n - 1, -1);
+    if (slice >= nv) return;
+
+    const TIn* ysrc = static_cast<const TIn*>(a.dy) + static_cast<long long>(bh) * a.T * a.Dv;
+    const int tq = (lane & 3) * 2;
+    const LaneOffsets oc = swz_cols(lane), orow = swz_rows(lane);
+    const int d0 = half * (DKP / 2);
+    float S[DKP / 16][4];
+    state_load<DKP / 2>(S, a.d_final ? a.d_final + static_cast<long long>(bh) * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, v0, lane, d0);
+
+    for (int i = 0; i < a.n; ++i) {
+        const int stage = i % kS, c = a.n - 1 - i;
+        const long long cid = static_cast<long long>(bh) * a.n + c;
+        uint32_t so[kHalf][NM][4];
+#pragma unroll
+        for (int d = 0; d < kHalf; ++d) {
+            split_frag<NM>(S[2 * d], S[2 * d + 1], so[d]);
+            put_planes<NM>(ex + Ex::s + (half * kHalf + d) * NM * 32, lane, so[d]);
+            frag_to_planes<NM>(so[d], a.dSst + cid * NM * a.DVP * DKP, static_cast<long long>(a.DVP) * DKP, DKP, v0, d0 + 16 * d,
+                               lane);
+        }
+        if (!pair_agree(slice, wait_stage(ring, stage, i / kS, a.err))) return;
+        const uint32_t st = base + stage * Tl::bytes;
+        const uint32_t kt = st + Tl::k, qt = st + Tl::q, et = st + Tl::rec, pt = et + NM * kSq;
+        const float* gam = reinterpret_cast<const float*>(smem + stage * Tl::bytes + Tl::tok);
+        const float* rest = gam + C;
+        const float* beta = gam + 2 * C;
+
+        // X = (K dS)^T for this warp's tokens, then dU = e^(L_C - L) X + (P^T dY)
+        float X[2][2][4] = {};
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            const int hh = o ? 1 - half : half;
+#pragma unroll
+            for (int d = 0; d < kHalf; ++d) {
+                uint32_t s[NM][4];
+                if (o) {
+                    get_planes<NM>(ex + Ex::s + (hh * kHalf + d) * NM * 32, lane, s);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < NM; ++p)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) s[p][x] = so[d][p][x];
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int p = 0; p < NI; ++p) {
+                        uint32_t r[4];
+                        ldsm4(r, kt + p * Tl::kTile + 2048 * pair_block(half, j) + half_step<DKP>(oc.o[d], hh));
+                        mma_planes<NM, NM>(X[j][0], X[j][1], s, p, r);
+                    }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) block_scale(X[j], rest, pair_block(half, j), tq);
+        // dY block by block: into dU of the tokens up to it, and with its factors into dS's update
+        const float total = gam[C - 1];
+#pragma unroll
+        for (int d = 0; d < 2 * kHalf; ++d)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) S[d][x] *= total;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            float Y[2][4];
+            if constexpr (kF32)
+                block_from_global(Y, ysrc, c * C + 16 * m, a.T, a.Dv, v0, lane);
+            else
+                block_from_tile(Y, st + Tl::v + 2048 * slice, m, lane);
+            uint32_t x[NI][4], y[NM][4];
+            split_frag<NI>(Y[0], Y[1], x);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int blk = pair_block(half, j);
+                if (blk <= m) {
+#pragma unroll
+                    for (int p = 0; p < NM; ++p) {
+                        uint32_t r[4];
+                        ldsm4t(r, pt + p * kSq + 2048 * m + (orow.o[0] ^ (blk << 5)));
+                        mma_planes<NI, NM>(X[j][0], X[j][1], x, p, r);
+                    }
+                }
+            }
+            block_scale(Y, gam, m, tq, a.scale);
+            split_frag<NM>(Y[0], Y[1], y);
+#pragma unroll
+            for (int d = 0; d < kHalf; ++d)
+#pragma unroll
+                for (int p = 0; p < NI; ++p) {
+                    uint32_t r[4];
+                    ldsm4t(r, qt + p * Tl::kTile + half_step<DKP>(orow.o[d], half) + 2048 * m);
+                    mma_planes<NM, NM>(S[2 * d], S[2 * d + 1], y, p, r);
+                }
+        }
+        uint32_t uo[2][NM][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            block_scale(X[j], beta, pair_block(half, j), tq);
+            split_frag<NM>(X[j][0], X[j][1], uo[j]);
+            put_planes<NM>(ex + Ex::u + (half * 2 + j) * NM * 32, lane, uo[j]);
+        }
+        pair_sync(slice);
+        // dR = T^T diag(beta) dU for this warp's tokens
+        float R[2][2][4] = {};
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+#pragma unroll
+            for (int jm = 0; jm < 2; ++jm) {
+                const int hh = o ? 1 - half : half, m = pair_block(hh, jm);
+                uint32_t u[NM][4];
+                if (o) {
+                    get_planes<NM>(ex + Ex::u + (hh * 2 + jm) * NM * 32, lane, u);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < NM; ++p)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) u[p][x] = uo[jm][p][x];
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int blk = pair_block(half, j);
+                    if (blk <= m) {
+#pragma unroll
+                        for (int p = 0; p < NM; ++p) {
+                            uint32_t r[4];
+                            ldsm4t(r, et + p * kSq + 2048 * m + (orow.o[0] ^ (blk << 5)));
+                            mma_planes<NM, NM>(R[j][0], R[j][1], u, p, r);
+                        }
+                    }
+                }
+            }
+        uint32_t wo[2][NM][4], wp[2][NM][4];
+        TIn* out = static_cast<TIn*>(a.dv) + static_cast<long long>(bh) * a.T * a.Dv;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int blk = pair_block(half, j);
+            block_to_global(R[j], out, c * C + 16 * blk, a.T, a.Dv, v0, lane);
+            split_frag<NM>(R[j][0], R[j][1], wo[j]);
+            frag_to_planes<NM>(wo[j], a.dRst + cid * NM * a.DVP * C, static_cast<long long>(a.DVP) * C, C, v0, 16 * blk, lane);
+            block_scale(R[j], gam, blk, tq, -1.f);
+            split_frag<NM>(R[j][0], R[j][1], wo[j]);
+            put_planes<NM>(ex + Ex::w + (half * 2 + j) * NM * 32, lane, wo[j]);
+        }
+        pair_sync(slice);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) get_planes<NM>(ex + Ex::w + ((1 - half) * 2 + j) * NM * 32, lane, wp[j]);
+#pragma unroll
+        for (int d = 0; d < kHalf; ++d) {
+            float acc[2][4] = {};
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int p = 0; p < NI; ++p) {
+                    const uint32_t at = kt + p * Tl::kTile + half_step<DKP>(orow.o[d], half);
+                    uint32_t r[4];
+                    ldsm4t(r, at + 2048 * pair_block(half, j));
+                    mma_planes<NM, NM>(acc[0], acc[1], wo[j], p, r);
+                    ldsm4t(r, at + 2048 * pair_block(1 - half, j));
+                    mma_planes<NM, NM>(acc[0], acc[1], wp[j], p, r);
+                }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) S[2 * d + j][x] += acc[j][x];
+        }
+        release_stage<Tl>(feed, base, ring, stage, c - kS);
+    }
+    if (a.d_init) state_store<DKP / 2>(S, a.d_init + static_cast<long long>(bh) * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane, d0);
 }
 
 // ---------------------------------------------------------------- gradients of a chunk
@@ -644,6 +857,19 @@ cudaError_t reverse_run(const Plan& p, const Args& a, RevArgs r) {
     return cudaGetLastError();
 }
 
+template <int DKP, int NI, int NM, int NS, typename TIn>
+cudaError_t pair_reverse_run(const Plan& p, const Args& a, RevArgs r) {
+    auto kern = pair_reverse_kernel<DKP, NI, NM, NS, TIn>;
+    using Tl = ScanTiles<DKP, NI, 2 * NM, NS, true, sizeof(TIn) == 2, 16 * RevSpace<DKP, NM>::words * NS>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tl::smem);
+    if (e != cudaSuccess) return e;
+    ScanMaps m;
+    if (!scan_maps(p, a, a.dy, &m)) return cudaErrorUnknown;
+    r.vblocks = (a.Dv + 16 * NS - 1) / (16 * NS);
+    kern<<<static_cast<unsigned>(p.BH * r.vblocks), 64 * NS, Tl::smem, a.stream>>>(m.k, m.q, m.v, r);
+    return cudaGetLastError();
+}
+
 template <int DKP, int NI, int NM, typename TIn>
 cudaError_t backward_typed(const Plan& p, const Args& a) {
     RevArgs r{};
@@ -664,7 +890,8 @@ cudaError_t backward_typed(const Plan& p, const Args& a) {
     r.Dv = a.Dv;
     r.DVP = p.DVP;
     r.n = p.n;
-    cudaError_t e = p.warps == 1   ? reverse_run<DKP, NI, NM, 1, TIn>(p, a, r)
+    cudaError_t e = p.pair ? (p.warps == 1 ? pair_reverse_run<DKP, NI, NM, 1, TIn>(p, a, r) : pair_reverse_run<DKP, NI, NM, 2, TIn>(p, a, r))
+                    : p.warps == 1 ? reverse_run<DKP, NI, NM, 1, TIn>(p, a, r)
                     : p.warps == 2 ? reverse_run<DKP, NI, NM, 2, TIn>(p, a, r)
                     : p.warps == 4 ? reverse_run<DKP, NI, NM, 4, TIn>(p, a, r)
                                    : reverse_run<DKP, NI, NM, 8, TIn>(p, a, r);

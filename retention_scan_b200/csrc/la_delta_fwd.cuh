@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(32 * NW) scan_kernel(const __grid_constant__ C
     feed.bh = bh;
     feed.v0 = vb;
     feed.nv = nv;
+    feed.warps = nv;
     start_ring<Tl>(feed, base, ring, a.n, 0, 1);
     if (warp >= nv) return;
 
@@ -423,6 +424,244 @@ __global__ void __launch_bounds__(32 * NW) scan_kernel(const __grid_constant__ C
         state_store<DKP>(S, a.final_state + static_cast<long long>(bh) * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane);
 }
 
+// The same scan with two warps a slice (la_delta.cuh), for few (b, h): NS slices
+// a block.  Per chunk and pair three barriers: the state's halves, the
+// right-hand sides R, and U are exchanged.
+template <int DKP, int NM>
+struct PairSpace {  // a slice's exchange, in 16-byte words
+    static constexpr int kHalf = DKP / 32;           // k-steps of half the key width
+    static constexpr int s = 0;                      // [2][kHalf][NM][32]
+    static constexpr int r = s + 2 * kHalf * NM * 32;  // [2][2][NM][32]
+    static constexpr int u = r + 2 * 2 * NM * 32;
+    static constexpr int w = u + 2 * 2 * NM * 32;
+    static constexpr int words = w + 2 * 2 * NM * 32;
+};
+
+template <int DKP, int NI, int NM, int NP, int NS, bool kOut, typename TIn>
+__global__ void __launch_bounds__(64 * NS) pair_scan_kernel(const __grid_constant__ CUtensorMap mk,
+                                                            const __grid_constant__ CUtensorMap mq,
+                                                            const __grid_constant__ CUtensorMap mv, ScanArgs a) {
+    constexpr bool kF32 = sizeof(TIn) == 4;
+    using Ex = PairSpace<DKP, NM>;
+    using Tl = ScanTiles<DKP, NI, kOut ? NM + NP : NM, NS, kOut, !kF32, 16 * Ex::words * NS>;
+    constexpr int kS = Tl::stages, kHalf = Ex::kHalf;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+    unsigned char* smem = smem_raw + (base - smem_addr(smem_raw));
+    Ring<kS>* ring = reinterpret_cast<Ring<kS>*>(smem + kS * Tl::bytes);
+    const int tid = threadIdx.x, lane = tid & 31, slice = tid >> 6, half = (tid >> 5) & 1;
+    uint4* ex = reinterpret_cast<uint4*>(smem + Tl::extra) + slice * Ex::words;
+    const int bh = blockIdx.x / a.vblocks;
+    const int vb = blockIdx.x % a.vblocks * 16 * NS, v0 = vb + 16 * slice;
+    const int nv = min(NS, (a.Dv - vb + 15) / 16);
+    const int b = bh / a.H, h = bh % a.H;
+    Feed<Tl, NI, kOut, !kF32> feed;
+    feed.mk = &mk;
+    feed.mq = &mq;
+    feed.mv = &mv;
+    feed.rec_bytes = record_bytes(NM + NP);
+    feed.records = a.records + static_cast<long long>(bh) * a.n * feed.rec_bytes;
+    feed.rec_used = (kOut ? NM + NP : NM) * kSq;
+    feed.hk = b * a.Hk + h / (a.H / a.Hk);
+    feed.planes_apart = a.planes_apart;
+    feed.bh = bh;
+    feed.v0 = vb;
+    feed.nv = nv;
+    feed.warps = 2 * nv;
+    start_ring<Tl>(feed, base, ring, a.n, 0, 1);
+    if (slice >= nv) return;
+
+    const TIn* vsrc = static_cast<const TIn*>(a.v) + static_cast<long long>(bh) * a.T * a.Dv;
+    const int tq = (lane & 3) * 2;
+    const LaneOffsets oc = swz_cols(lane), orow = swz_rows(lane);
+    const int d0 = half * (DKP / 2);
+    float S[DKP / 16][4];
+    state_load<DKP / 2>(S, a.init_state ? a.init_state + static_cast<long long>(bh) * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, v0,
+                        lane, d0);
+
+    for (int c = 0; c < a.n; ++c) {
+        const int stage = c % kS;
+        const long long cid = static_cast<long long>(bh) * a.n + c;
+        uint32_t so[kHalf][NM][4];
+#pragma unroll
+        for (int d = 0; d < kHalf; ++d) {
+            split_frag<NM>(S[2 * d], S[2 * d + 1], so[d]);
+            put_planes<NM>(ex + Ex::s + (half * kHalf + d) * NM * 32, lane, so[d]);
+            if constexpr (!kOut)
+                frag_to_planes<NM>(so[d], a.Sst + cid * NM * a.DVP * DKP, static_cast<long long>(a.DVP) * DKP, DKP, v0,
+                                   d0 + 16 * d, lane);
+        }
+        if (!pair_agree(slice, wait_stage(ring, stage, c / kS, a.err))) return;
+        const uint32_t st = base + stage * Tl::bytes;
+        const uint32_t kt = st + Tl::k, qt = st + Tl::q, et = st + Tl::rec, pt = et + NM * kSq;
+        const float* gam = reinterpret_cast<const float*>(smem + stage * Tl::bytes + Tl::tok);
+        const float* rest = gam + C;
+        const float* beta = gam + 2 * C;
+
+        // X = (K S)^T, Y = (Q S)^T for this warp's tokens: its own half of S, then the other's
+        float X[2][2][4] = {}, Y[2][2][4] = {};
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            const int hh = o ? 1 - half : half;
+#pragma unroll
+            for (int d = 0; d < kHalf; ++d) {
+                uint32_t s[NM][4];
+                if (o) {
+                    get_planes<NM>(ex + Ex::s + (hh * kHalf + d) * NM * 32, lane, s);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < NM; ++p)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[p][i] = so[d][p][i];
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int p = 0; p < NI; ++p) {
+                        const uint32_t at = p * Tl::kTile + 2048 * pair_block(half, j) + half_step<DKP>(oc.o[d], hh);
+                        uint32_t r[4];
+                        ldsm4(r, kt + at);
+                        mma_planes<NM, NM>(X[j][0], X[j][1], s, p, r);
+                        if constexpr (kOut) {
+                            ldsm4(r, qt + at);
+                            mma_planes<NM, NM>(Y[j][0], Y[j][1], s, p, r);
+                        }
+                    }
+            }
+        }
+        // R = V - e^L (K S), exchanged
+        uint32_t ro[2][NM][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int blk = pair_block(half, j);
+            float R[2][4];
+            if constexpr (kF32)
+                block_from_global(R, vsrc, c * C + 16 * blk, a.T, a.Dv, v0, lane);
+            else
+                block_from_tile(R, st + Tl::v + 2048 * slice, blk, lane);
+            block_scale(X[j], gam, blk, tq);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    R[x][i] -= X[j][x][i];
+                    X[j][x][i] = 0.f;
+                }
+            split_frag<NM>(R[0], R[1], ro[j]);
+            put_planes<NM>(ex + Ex::r + (half * 2 + j) * NM * 32, lane, ro[j]);
+        }
+        pair_sync(slice);
+        // E for this warp's tokens: the blocks of (I + A diag(beta))^-1 R at and before each
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+#pragma unroll
+            for (int jm = 0; jm < 2; ++jm) {
+                const int hh = o ? 1 - half : half, m = pair_block(hh, jm);
+                uint32_t r[NM][4];
+                if (o) {
+                    get_planes<NM>(ex + Ex::r + (hh * 2 + jm) * NM * 32, lane, r);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < NM; ++p)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) r[p][i] = ro[jm][p][i];
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int blk = pair_block(half, j);
+                    if (m <= blk) {
+#pragma unroll
+                        for (int p = 0; p < NM; ++p) {
+                            uint32_t e[4];
+                            ldsm4(e, et + p * kSq + 2048 * blk + (oc.o[0] ^ (m << 5)));
+                            mma_planes<NM, NM>(X[j][0], X[j][1], r, p, e);
+                        }
+                    }
+                }
+            }
+        // U = diag(beta) E, and diag(e^(L_C - L)) U for the state, exchanged
+        uint32_t uo[2][NM][4], wo[2][NM][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int blk = pair_block(half, j);
+            if constexpr (!kOut) {
+                split_frag<NM>(X[j][0], X[j][1], uo[j]);
+                frag_to_planes<NM>(uo[j], a.Est + cid * NM * a.DVP * C, static_cast<long long>(a.DVP) * C, C, v0, 16 * blk, lane);
+            }
+            block_scale(X[j], beta, blk, tq);
+            if constexpr (kOut) {
+                split_frag<NM>(X[j][0], X[j][1], uo[j]);
+                put_planes<NM>(ex + Ex::u + (half * 2 + j) * NM * 32, lane, uo[j]);
+            }
+            block_scale(X[j], rest, blk, tq);
+            split_frag<NM>(X[j][0], X[j][1], wo[j]);
+            put_planes<NM>(ex + Ex::w + (half * 2 + j) * NM * 32, lane, wo[j]);
+        }
+        pair_sync(slice);
+        if constexpr (kOut) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) block_scale(Y[j], gam, pair_block(half, j), tq, a.scale);
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int jm = 0; jm < 2; ++jm) {
+                    const int hh = o ? 1 - half : half, m = pair_block(hh, jm);
+                    uint32_t u[NM][4];
+                    if (o) {
+                        get_planes<NM>(ex + Ex::u + (hh * 2 + jm) * NM * 32, lane, u);
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < NM; ++p)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) u[p][i] = uo[jm][p][i];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int blk = pair_block(half, j);
+                        if (m <= blk) {
+#pragma unroll
+                            for (int p = 0; p < NP; ++p) {
+                                uint32_t r[4];
+                                ldsm4(r, pt + p * kSq + 2048 * blk + (oc.o[0] ^ (m << 5)));
+                                mma_planes<NM, NM>(Y[j][0], Y[j][1], u, p, r);
+                            }
+                        }
+                    }
+                }
+            TIn* out = static_cast<TIn*>(a.out) + static_cast<long long>(bh) * a.T * a.Dv;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) block_to_global(Y[j], out, c * C + 16 * pair_block(half, j), a.T, a.Dv, v0, lane);
+        }
+        // This warp's half of S <- e^(L_C) S + K^T diag(e^(L_C - L)) U
+        uint32_t wp[2][NM][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) get_planes<NM>(ex + Ex::w + ((1 - half) * 2 + j) * NM * 32, lane, wp[j]);
+        const float total = gam[C - 1];
+#pragma unroll
+        for (int d = 0; d < kHalf; ++d) {
+            float acc[2][4] = {};
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int p = 0; p < NI; ++p) {
+                    const uint32_t at = kt + p * Tl::kTile + half_step<DKP>(orow.o[d], half);
+                    uint32_t r[4];
+                    ldsm4t(r, at + 2048 * pair_block(half, j));
+                    mma_planes<NM, NM>(acc[0], acc[1], wo[j], p, r);
+                    ldsm4t(r, at + 2048 * pair_block(1 - half, j));
+                    mma_planes<NM, NM>(acc[0], acc[1], wp[j], p, r);
+                }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[2 * d + j][i] = fmaf(total, S[2 * d + j][i], acc[j][i]);
+        }
+        release_stage<Tl>(feed, base, ring, stage, c + kS < a.n ? c + kS : -1);
+    }
+    if (a.final_state)
+        state_store<DKP / 2>(S, a.final_state + static_cast<long long>(bh) * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane, d0);
+}
+
 template <typename K>
 cudaError_t allow_smem(K kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
@@ -453,8 +692,24 @@ cudaError_t scan_run(const Plan& p, const Args& a) {
     return cudaGetLastError();
 }
 
+template <int DKP, int NI, int NM, int NP, int NS, bool kOut, typename TIn>
+cudaError_t pair_scan_run(const Plan& p, const Args& a) {
+    auto kern = pair_scan_kernel<DKP, NI, NM, NP, NS, kOut, TIn>;
+    using Tl = ScanTiles<DKP, NI, kOut ? NM + NP : NM, NS, kOut, sizeof(TIn) == 2, 16 * PairSpace<DKP, NM>::words * NS>;
+    cudaError_t e = allow_smem(kern, Tl::smem);
+    if (e != cudaSuccess) return e;
+    ScanMaps m;
+    if (!scan_maps(p, a, a.v, &m)) return cudaErrorUnknown;
+    ScanArgs s = scan_args(p, a);
+    s.vblocks = (a.Dv + 16 * NS - 1) / (16 * NS);
+    kern<<<static_cast<unsigned>(p.BH * s.vblocks), 64 * NS, Tl::smem, a.stream>>>(m.k, m.q, m.v, s);
+    return cudaGetLastError();
+}
+
 template <int DKP, int NI, int NM, int NP, bool kOut, typename TIn>
 cudaError_t scan_widths(const Plan& p, const Args& a) {
+    if (p.pair)
+        return p.warps == 1 ? pair_scan_run<DKP, NI, NM, NP, 1, kOut, TIn>(p, a) : pair_scan_run<DKP, NI, NM, NP, 2, kOut, TIn>(p, a);
     switch (p.warps) {
         case 1: return scan_run<DKP, NI, NM, NP, 1, kOut, TIn>(p, a);
         case 2: return scan_run<DKP, NI, NM, NP, 2, kOut, TIn>(p, a);

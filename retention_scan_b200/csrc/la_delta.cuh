@@ -120,12 +120,11 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
 }
 __device__ __forceinline__ uint32_t mov_trans(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -310,19 +309,19 @@ __device__ __forceinline__ void state_store(const float (&s)[DKP / 8][4], float*
         }
 }
 
-// Planes of an A operand to a [v][col] array of bf16 planes (`plane` apart),
-// rows v0.., columns col0..col0+15.
+// What the scans leave for the gradients (states, errors, ...): the operand
+// planes of each 16 value columns x 16 columns block as four 8 x 8 tiles of 128
+// contiguous bytes, [slice][plane][block][4][8][8].  A warp stores a register as
+// one whole line, and ldmatrix on base + 16 lane finds a tile's rows side by
+// side, without bank conflicts and in the order of the registers.
+constexpr int kBlk = 256;  // elements of a block
 template <int N>
-__device__ __forceinline__ void frag_to_planes(const uint32_t (&a)[N][4], __nv_bfloat16* base, long long plane, int width,
-                                               int v0, int col0, int lane) {
-    const int g = lane >> 2, tq = (lane & 3) * 2;
+__device__ __forceinline__ void put_tiles(const uint32_t (&a)[N][4], __nv_bfloat16* base, int slice, int blocks, int blk, int lane) {
 #pragma unroll
     for (int p = 0; p < N; ++p) {
-        __nv_bfloat16* r = base + p * plane + (v0 + g) * width + col0 + tq;
-        *reinterpret_cast<uint32_t*>(r) = a[p][0];
-        *reinterpret_cast<uint32_t*>(r + 8 * width) = a[p][1];
-        *reinterpret_cast<uint32_t*>(r + 8) = a[p][2];
-        *reinterpret_cast<uint32_t*>(r + 8 * width + 8) = a[p][3];
+        __nv_bfloat16* r = base + (static_cast<long long>(slice * N + p) * blocks + blk) * kBlk + lane * 2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(r + 64 * i) = a[p][i];
     }
 }
 

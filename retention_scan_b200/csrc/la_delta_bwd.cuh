@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(32 * NW) reverse_kernel(const __grid_constant_
         for (int d = 0; d < DKP / 16; ++d) {
             uint32_t s[NM][4];
             split_frag<NM>(S[2 * d], S[2 * d + 1], s);
-            frag_to_planes<NM>(s, a.dSst + cid * NM * a.DVP * DKP, static_cast<long long>(a.DVP) * DKP, DKP, v0, 16 * d, lane);
+            put_tiles<NM>(s, a.dSst + cid * NM * a.DVP * DKP, v0 / 16, DKP / 16, d, lane);
 #pragma unroll
             for (int nn = 0; nn < 4; ++nn)
 #pragma unroll
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(32 * NW) reverse_kernel(const __grid_constant_
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             split_frag<NM>(R[2 * m], R[2 * m + 1], w[m]);
-            frag_to_planes<NM>(w[m], a.dRst + cid * NM * a.DVP * C, static_cast<long long>(a.DVP) * C, C, v0, 16 * m, lane);
+            put_tiles<NM>(w[m], a.dRst + cid * NM * a.DVP * C, v0 / 16, C / 16, m, lane);
 #pragma unroll
             for (int j = 2 * m; j < 2 * m + 2; ++j) {
                 const float2 gm = *reinterpret_cast<const float2*>(gam + 8 * j + tq);
@@ -284,8 +284,7 @@ __global__ void __launch_bounds__(64 * NS) pair_reverse_kernel(const __grid_cons
         for (int d = 0; d < kHalf; ++d) {
             split_frag<NM>(S[2 * d], S[2 * d + 1], so[d]);
             put_planes<NM>(ex + Ex::s + (half * kHalf + d) * NM * 32, lane, so[d]);
-            frag_to_planes<NM>(so[d], a.dSst + cid * NM * a.DVP * DKP, static_cast<long long>(a.DVP) * DKP, DKP, v0, d0 + 16 * d,
-                               lane);
+            put_tiles<NM>(so[d], a.dSst + cid * NM * a.DVP * DKP, v0 / 16, DKP / 16, half * kHalf + d, lane);
         }
         if (!pair_agree(slice, wait_stage(ring, stage, i / kS, a.err))) return;
         const uint32_t st = base + stage * Tl::bytes;
@@ -404,7 +403,7 @@ __global__ void __launch_bounds__(64 * NS) pair_reverse_kernel(const __grid_cons
             const int blk = pair_block(half, j);
             block_to_global(R[j], out, c * C + 16 * blk, a.T, a.Dv, v0, lane);
             split_frag<NM>(R[j][0], R[j][1], wo[j]);
-            frag_to_planes<NM>(wo[j], a.dRst + cid * NM * a.DVP * C, static_cast<long long>(a.DVP) * C, C, v0, 16 * blk, lane);
+            put_tiles<NM>(wo[j], a.dRst + cid * NM * a.DVP * C, v0 / 16, C / 16, blk, lane);
             block_scale(R[j], gam, blk, tq, -1.f);
             split_frag<NM>(R[j][0], R[j][1], wo[j]);
             put_planes<NM>(ex + Ex::w + (half * 2 + j) * NM * 32, lane, wo[j]);
@@ -439,31 +438,55 @@ __global__ void __launch_bounds__(64 * NS) pair_reverse_kernel(const __grid_cons
 // ---------------------------------------------------------------- gradients of a chunk
 // One block of 8 warps per (b, h, chunk): warp (r, c) = (w % 4, w / 4) holds rows
 // 16 r .. of every product and column half c.  The contraction over the value
-// columns streams 16 of them at a time (S, dS, E, dR, dY slices); then the
-// C x C gradients go through shared memory as A operands of the products with
-// K and Q.
+// columns streams 16 of them at a time (S, dS, E, dR, dY) through a ring of bulk
+// copies; then the C x C gradients go through shared memory as A operands of the
+// products with K and Q.  Measured at B2 H16 T4096 D128: 310 us with cp.async
+// into padded rows (6000 instructions a warp and chunk, two in three of them
+// addresses), see DESIGN for this form.
 constexpr int kGradThreads = 256;
-constexpr int kVS = 16;  // value columns per streamed slice
 
-template <int DKP, int NI, int NM>
+template <int DKP, int NI, int NM, bool kF32>
 struct GradTiles {
-    static constexpr int kRow = DKP + kPad, kY = kVS + kPad;
-    static constexpr int k = 0;
-    static constexpr int q = k + 2 * NI * C * kRow;
-    static constexpr int s = q + 2 * NI * C * kRow;         // [NM][kVS][kRow]
-    static constexpr int ds = s + 2 * NM * kVS * kRow;
-    static constexpr int e = ds + 2 * NM * kVS * kRow;      // [NM][kVS][kCS]
-    static constexpr int r = e + 2 * NM * kVS * kCS;
-    static constexpr int y = r + 2 * NM * kVS * kCS;        // [NI][C][kY]
-    static constexpr int slice = y + 2 * NI * C * kY - s;   // one streamed slice
-    static constexpr int stages = 2;
-    static constexpr int dp = s;                            // [NM][C][kCS], over the slices once they are done
+    static constexpr int kRow = DKP + kPad;
+    static constexpr int s = 0;                               // one stage: the slice's blocks ...
+    static constexpr int ds = s + 2 * NM * (DKP / 16) * kBlk;
+    static constexpr int e = ds + 2 * NM * (DKP / 16) * kBlk;
+    static constexpr int r = e + 2 * NM * (C / 16) * kBlk;
+    static constexpr int y = r + 2 * NM * (C / 16) * kBlk;    // ... and dY's 64 x 16 tile (bf16)
+    static constexpr int copied = y + (kF32 ? 0 : 2048);
+    static constexpr int bytes = copied;
+    static constexpr int stages = 3;
+    static constexpr int dp = 0;                              // [NM][C][kCS], over the stages once they are done
     static constexpr int da = dp + 2 * NM * C * kCS;
-    static constexpr int after = (2 * slice > 4 * NM * C * kCS ? 2 * slice : 4 * NM * C * kCS) + s;
-    static constexpr int tok = after;                       // kTok floats, L, sums
+    static constexpr int over = stages * bytes > 4 * NM * C * kCS ? stages * bytes : 4 * NM * C * kCS;
+    static constexpr int ring = over;
+    static constexpr int k = ring + 256;
+    static constexpr int q = k + 2 * NI * C * kRow;
+    static constexpr int tok = q + 2 * NI * C * kRow;         // kTok floats, L, sums
     static constexpr int L = tok + 4 * kTok;
-    static constexpr int sums = L + 8 * C;                  // floats: [4][2][C] row sums, [4][C] column sums
-    static constexpr int bytes = sums + 4 * (8 * C + 4 * C + 64);
+    static constexpr int sums = L + 8 * C;                    // floats: [4][C] row sums, [4][C] column sums, per warp
+    static constexpr int smem = sums + 4 * (4 * C + 4 * C + 64) + 128;
+};
+
+// Brings one slice into a stage.
+template <typename Tl, int DKP, int NM, bool kF32>
+struct GradFeed {
+    const __nv_bfloat16 *S, *dS, *E, *dR;  // of this chunk
+    const CUtensorMap* my;
+    int t0, bh, warps;
+
+    __device__ __forceinline__ void issue(uint32_t base, Ring<Tl::stages>* ring, int st, int sl) const {
+        uint64_t* bar = &ring->full[st];
+        const uint32_t at = base + st * Tl::bytes;
+        constexpr int kState = NM * (DKP / 16) * kBlk, kTokens = NM * (C / 16) * kBlk;
+        ring->issued[st] = ring->issued[st] + 1;
+        mbar_arrive_expect_tx(bar, Tl::copied);
+        bulk_load(at + Tl::s, S + static_cast<long long>(sl) * kState, 2 * kState, bar);
+        bulk_load(at + Tl::ds, dS + static_cast<long long>(sl) * kState, 2 * kState, bar);
+        bulk_load(at + Tl::e, E + static_cast<long long>(sl) * kTokens, 2 * kTokens, bar);
+        bulk_load(at + Tl::r, dR + static_cast<long long>(sl) * kTokens, 2 * kTokens, bar);
+        if (!kF32) tma_load(at + Tl::y, my, bar, 16 * sl, t0, bh);
+    }
 };
 
 struct GradArgs {
@@ -479,112 +502,112 @@ struct GradArgs {
     float* dbeta;
     float* d_log_g;        // per step, or null
     double* dlog;          // per chunk (per-head decay), or null
+    int* err;
     int H, Hk, T, Dk, Dv, DVP, n;
 };
 
+// Two neighbouring elements of a K or Q tile, its planes summed.
+template <int NI, int kRow>
+__device__ __forceinline__ float2 tile_pair(const __nv_bfloat16* tile, int t, int col) {
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int p = NI - 1; p >= 0; --p) {
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(tile + (p * C + t) * kRow + col);
+        s.x += low_of(u);
+        s.y += high_of(u);
+    }
+    return s;
+}
+
 template <int DKP, int NI, int NM, typename TIn>
-__global__ void __launch_bounds__(kGradThreads) grad_kernel(GradArgs a) {
-    using Tl = GradTiles<DKP, NI, NM>;
-    constexpr int kRow = Tl::kRow, kY = Tl::kY, kHalf = DKP / 2, kJ = kHalf / 8;
-    extern __shared__ __align__(16) unsigned char smem[];
+__global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constant__ CUtensorMap my, GradArgs a) {
+    constexpr bool kF32 = sizeof(TIn) == 4;
+    using Tl = GradTiles<DKP, NI, NM, kF32>;
+    constexpr int kRow = Tl::kRow, kHalf = DKP / 2, kJ = kHalf / 8, kS = Tl::stages;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 127) & ~127u;
+    unsigned char* smem = smem_raw + (base - smem_addr(smem_raw));
+    Ring<kS>* ring = reinterpret_cast<Ring<kS>*>(smem + Tl::ring);
     __nv_bfloat16* kt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::k);
     __nv_bfloat16* qt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::q);
     float* tok = reinterpret_cast<float*>(smem + Tl::tok);
     float2* L = reinterpret_cast<float2*>(smem + Tl::L);
-    float* rowsum = reinterpret_cast<float*>(smem + Tl::sums);  // [4 kinds][2 halves][C]
-    float* colsum = rowsum + 8 * C;                             // [4 row groups][C]
+    float* rowsum = reinterpret_cast<float*>(smem + Tl::sums);  // [dL, k.Z][2 halves][C]
+    float* colsum = rowsum + 4 * C;                             // [4 row groups][C]
     float* wsum = colsum + 4 * C;                               // per warp
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int wr = warp & 3, wc = warp >> 2;
     const int g = lane >> 2, tq = (lane & 3) * 2;
-    const long long bh = blockIdx.x / a.n;
+    const int bh = blockIdx.x / a.n;
     const int chunk = blockIdx.x % a.n, t0 = chunk * C;
-    const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
+    const int b = bh / a.H, h = bh % a.H;
     const long long hk = static_cast<long long>(b) * a.Hk + h / (a.H / a.Hk);
-    const long long cid = bh * a.n + chunk;
-    const TIn* ysrc = static_cast<const TIn*>(a.dy) + bh * a.T * a.Dv;
-    const __nv_bfloat16* Sg = a.S + cid * NM * a.DVP * DKP;
-    const __nv_bfloat16* dSg = a.dS + cid * NM * a.DVP * DKP;
-    const __nv_bfloat16* Eg = a.E + cid * NM * a.DVP * C;
-    const __nv_bfloat16* Rg = a.dR + cid * NM * a.DVP * C;
+    const long long cid = static_cast<long long>(bh) * a.n + chunk;
+    const TIn* ysrc = static_cast<const TIn*>(a.dy) + static_cast<long long>(bh) * a.T * a.Dv;
+    const int slices = a.DVP / 16;
 
-    auto load = [&](int sl) {
-        if (sl * kVS < a.DVP) {
-            unsigned char* st = smem + (sl & 1) * Tl::slice;
-            const int v0 = sl * kVS;
-#pragma unroll
-            for (int p = 0; p < NM; ++p) {
-                for (int i = tid; i < kVS * (DKP / 8); i += kGradThreads) {
-                    const int r = i / (DKP / 8), col = i % (DKP / 8) * 8;
-                    const long long o = (static_cast<long long>(p) * a.DVP + v0 + r) * DKP + col;
-                    cp16(reinterpret_cast<__nv_bfloat16*>(st + Tl::s) + (p * kVS + r) * kRow + col, Sg + o, true);
-                    cp16(reinterpret_cast<__nv_bfloat16*>(st + Tl::ds) + (p * kVS + r) * kRow + col, dSg + o, true);
-                }
-                for (int i = tid; i < kVS * (C / 8); i += kGradThreads) {
-                    const int r = i / (C / 8), col = i % (C / 8) * 8;
-                    const long long o = (static_cast<long long>(p) * a.DVP + v0 + r) * C + col;
-                    cp16(reinterpret_cast<__nv_bfloat16*>(st + Tl::e) + (p * kVS + r) * kCS + col, Eg + o, true);
-                    cp16(reinterpret_cast<__nv_bfloat16*>(st + Tl::r) + (p * kVS + r) * kCS + col, Rg + o, true);
-                }
-            }
-            __nv_bfloat16* yt = reinterpret_cast<__nv_bfloat16*>(st + Tl::y);
-            if constexpr (sizeof(TIn) == 2) {
-                for (int i = tid; i < C * (kVS / 8); i += kGradThreads) {
-                    const int r = i / (kVS / 8), col = i % (kVS / 8) * 8, t = t0 + r;
-                    const bool ok = t < a.T && v0 + col < a.Dv;
-                    cp16(yt + r * kY + col, ok ? ysrc + static_cast<long long>(t) * a.Dv + v0 + col : ysrc, ok);
-                }
-            } else {
-                for (int i = tid; i < C * (kVS / 2); i += kGradThreads) {
-                    const int r = i / (kVS / 2), col = i % (kVS / 2) * 2, t = t0 + r;
-                    float x = 0.f, y = 0.f;
-                    if (t < a.T && v0 + col < a.Dv) x = ysrc[static_cast<long long>(t) * a.Dv + v0 + col];
-                    if (t < a.T && v0 + col + 1 < a.Dv) y = ysrc[static_cast<long long>(t) * a.Dv + v0 + col + 1];
-                    uint32_t p[NI];
-                    split2<NI>(x, y, p);
-#pragma unroll
-                    for (int j = 0; j < NI; ++j) *reinterpret_cast<uint32_t*>(yt + (j * C + r) * kY + col) = p[j];
-                }
-            }
-        }
-        cp_commit();
-    };
-
+    GradFeed<Tl, DKP, NM, kF32> feed;
+    feed.S = a.S + cid * NM * a.DVP * DKP;
+    feed.dS = a.dS + cid * NM * a.DVP * DKP;
+    feed.E = a.E + cid * NM * a.DVP * C;
+    feed.dR = a.dR + cid * NM * a.DVP * C;
+    feed.my = &my;
+    feed.t0 = t0;
+    feed.bh = bh;
+    feed.warps = kGradThreads / 32;
+    start_ring<Tl>(feed, base, ring, slices, 0, 1);
     load_tile<DKP, NI>(kt, a.kp, hk, t0, tid, kGradThreads);
     load_tile<DKP, NI>(qt, a.qp, hk, t0, tid, kGradThreads);
     for (int i = tid; i < kTok / 4; i += kGradThreads) cp16(tok + 4 * i, a.records + (cid + 1) * record_bytes(2 * NM) - 4 * kTok + 16 * i, true);
-    load(0);
+    cp_commit();
     if (warp == 0) decay_prefix(L, lane, a.log_g, a.decay_kind, h, bh, t0, a.T);
 
     float M[4][4] = {}, N[4][4] = {};
     float dQ[kJ][4] = {}, Kr[kJ][4] = {}, Z[kJ][4] = {};
-    float inner = 0.f;  // <S, dS>
-    const int slices = a.DVP / kVS;
+    float in[2][4] = {};  // S dS^T over 16 columns of the key width: its diagonal is summed
+    bool ok = true;
     for (int sl = 0; sl < slices; ++sl) {
-        load(sl + 1);
-        cp_wait<1>();
-        __syncthreads();
-        unsigned char* st = smem + (sl & 1) * Tl::slice;
-        const __nv_bfloat16* s_t = reinterpret_cast<const __nv_bfloat16*>(st + Tl::s);
-        const __nv_bfloat16* ds_t = reinterpret_cast<const __nv_bfloat16*>(st + Tl::ds);
-        const __nv_bfloat16* e_t = reinterpret_cast<const __nv_bfloat16*>(st + Tl::e);
-        const __nv_bfloat16* r_t = reinterpret_cast<const __nv_bfloat16*>(st + Tl::r);
-        const __nv_bfloat16* y_t = reinterpret_cast<const __nv_bfloat16*>(st + Tl::y);
+        const int stage = sl % kS;
+        ok = wait_stage(ring, stage, sl / kS, a.err);
+        if (!ok) break;
+        const uint32_t st = base + stage * Tl::bytes;
+        const uint32_t lo = lane * 16;
         uint32_t ay[NI][4], ae[NM][4], ar[NM][4];
+        if constexpr (kF32) {
+            // rows t, columns v of dY straight from global memory
+            float x[2][4];
 #pragma unroll
-        for (int p = 0; p < NI; ++p) ldsm4(ay[p], smem_addr(y_t + (p * C + 16 * wr) * kY + off_rows(lane, kY)));
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int p = 0; p < NM; ++p) {
-            ldsm4t(ae[p], smem_addr(e_t + p * kVS * kCS + 16 * wr + off_cols(lane, kCS)));
-            ldsm4t(ar[p], smem_addr(r_t + p * kVS * kCS + 16 * wr + off_cols(lane, kCS)));
+                for (int i = 0; i < 4; ++i) {
+                    const int t = t0 + 16 * wr + g + (i >> 1) * 8, v = 16 * sl + 8 * j + tq + (i & 1);
+                    x[j][i] = t < a.T && v < a.Dv ? ysrc[static_cast<long long>(t) * a.Dv + v] : 0.f;
+                }
+            split_frag<NI>(x[0], x[1], ay);
+        } else {
+            ldsm4(ay[0], st + Tl::y + 512 * wr + (lane & 15) * 32 + (lane >> 4) * 16);
+        }
+#pragma unroll
+        for (int p = 0; p < NM; ++p) {  // A operands: tokens are the blocks' columns
+            uint32_t r[4];
+            ldsm4t(r, st + Tl::e + (p * (C / 16) + wr) * 512 + lo);
+            ae[p][0] = r[0];
+            ae[p][1] = r[2];
+            ae[p][2] = r[1];
+            ae[p][3] = r[3];
+            ldsm4t(r, st + Tl::r + (p * (C / 16) + wr) * 512 + lo);
+            ar[p][0] = r[0];
+            ar[p][1] = r[2];
+            ar[p][2] = r[1];
+            ar[p][3] = r[3];
         }
 #pragma unroll
         for (int nn = 0; nn < 2; ++nn)
-            if (32 * wc + 16 * nn <= 16 * wr) {
+            if (2 * wc + nn <= wr) {
 #pragma unroll
                 for (int p = 0; p < NM; ++p) {
                     uint32_t r[4];
-                    ldsm4t(r, smem_addr(e_t + p * kVS * kCS + 32 * wc + 16 * nn + off_rows(lane, kCS)));
+                    ldsm4t(r, st + Tl::e + (p * (C / 16) + 2 * wc + nn) * 512 + lo);
                     mma_planes<NI, NM>(M[2 * nn], M[2 * nn + 1], ay, p, r);
                     mma_planes<NM, NM>(N[2 * nn], N[2 * nn + 1], ar, p, r);
                 }
@@ -593,30 +616,38 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(GradArgs a) {
         for (int d = 0; d < kHalf / 16; ++d)
 #pragma unroll
             for (int p = 0; p < NM; ++p) {
+                const uint32_t at = st + (p * (DKP / 16) + wc * (kHalf / 16) + d) * 512 + lo;
                 uint32_t r[4];
-                ldsm4t(r, smem_addr(s_t + p * kVS * kRow + kHalf * wc + 16 * d + off_rows(lane, kRow)));
+                ldsm4t(r, at + Tl::s);
                 mma_planes<NI, NM>(dQ[2 * d], dQ[2 * d + 1], ay, p, r);
                 mma_planes<NM, NM>(Kr[2 * d], Kr[2 * d + 1], ar, p, r);
-                ldsm4t(r, smem_addr(ds_t + p * kVS * kRow + kHalf * wc + 16 * d + off_rows(lane, kRow)));
+                ldsm4t(r, at + Tl::ds);
                 mma_planes<NM, NM>(Z[2 * d], Z[2 * d + 1], ae, p, r);
             }
-        for (int i = tid; i < kVS * (DKP / 2); i += kGradThreads) {
-            const int r = i / (DKP / 2), col = i % (DKP / 2) * 2;
-            float x0 = 0.f, x1 = 0.f, y0 = 0.f, y1 = 0.f;
+        if (warp < DKP / 16) {
+            uint32_t as[NM][4];
 #pragma unroll
-            for (int p = NM - 1; p >= 0; --p) {
-                const uint32_t u = *reinterpret_cast<const uint32_t*>(s_t + (p * kVS + r) * kRow + col);
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(ds_t + (p * kVS + r) * kRow + col);
-                x0 += low_of(u);
-                x1 += high_of(u);
-                y0 += low_of(w);
-                y1 += high_of(w);
+            for (int p = 0; p < NM; ++p) ldsm4(as[p], st + Tl::s + (p * (DKP / 16) + warp) * 512 + lo);
+#pragma unroll
+            for (int p = 0; p < NM; ++p) {
+                uint32_t r[4], x[4];
+                ldsm4(r, st + Tl::ds + (p * (DKP / 16) + warp) * 512 + lo);
+                x[0] = r[0];
+                x[1] = r[2];
+                x[2] = r[1];
+                x[3] = r[3];
+                mma_planes<NM, NM>(in[0], in[1], as, p, x);
             }
-            inner = fmaf(x0, y0, fmaf(x1, y1, inner));
         }
-        __syncthreads();
+        release_stage<Tl>(feed, base, ring, stage, sl + kS < slices ? sl + kS : -1);
     }
+    // all warps of a block give up together: no copy is in flight, the outputs are incomplete, the error word says so
     cp_wait<0>();
+    if (!__syncthreads_and(ok)) return;
+    // diagonal of the 16 x 16 accumulator: rows g, g + 8; columns 8 j + tq, + 1
+    float inner = 0.f;
+    if (g == tq) inner = in[0][0] + in[1][2];
+    if (g == tq + 1) inner = in[0][1] + in[1][3];
 
     // The chunk's scores again (exact operands), in the layout of M and N.
     const float* gam = tok;
@@ -687,19 +718,17 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(GradArgs a) {
         const int t = 16 * wr + g + 8 * r;
         const float gm = gam[t], rs = rest[t], bt = beta[t];
 #pragma unroll
-        for (int j = 0; j < kJ; ++j)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int col = kHalf * wc + 8 * j + tq + x;
-                float kv = 0.f;
-#pragma unroll
-                for (int p = NI - 1; p >= 0; --p) kv += __bfloat162float(kt[(p * C + t) * kRow + col]);
-                dQ[j][2 * r + x] *= a.scale * gm;
-                Kr[j][2 * r + x] *= -gm;
-                const float z = rs * Z[j][2 * r + x];
-                zk[r] = fmaf(kv, z, zk[r]);
-                Kc[j][2 * r + x] = bt * z;
-            }
+        for (int j = 0; j < kJ; ++j) {
+            const float2 kv = tile_pair<NI, kRow>(kt, t, kHalf * wc + 8 * j + tq);
+            const float z0 = rs * Z[j][2 * r], z1 = rs * Z[j][2 * r + 1];
+            dQ[j][2 * r] *= a.scale * gm;
+            dQ[j][2 * r + 1] *= a.scale * gm;
+            Kr[j][2 * r] *= -gm;
+            Kr[j][2 * r + 1] *= -gm;
+            zk[r] = fmaf(kv.x, z0, fmaf(kv.y, z1, zk[r]));
+            Kc[j][2 * r] = bt * z0;
+            Kc[j][2 * r + 1] = bt * z1;
+        }
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -735,7 +764,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(GradArgs a) {
     }
 
     // Outputs and the row sums of dL.
-    const long long base = a.dqh ? bh : hk;
+    const long long head = a.dqh ? bh : hk;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const int t = 16 * wr + g + 8 * r;
@@ -743,19 +772,13 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(GradArgs a) {
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
             const int col = kHalf * wc + 8 * j + tq;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float kv = 0.f, qv = 0.f;
-#pragma unroll
-                for (int p = NI - 1; p >= 0; --p) {
-                    kv += __bfloat162float(kt[(p * C + t) * kRow + col + x]);
-                    qv += __bfloat162float(qt[(p * C + t) * kRow + col + x]);
-                }
-                dl = fmaf(qv, dQ[j][2 * r + x], dl);
-                dl = fmaf(kv, Kr[j][2 * r + x] - Kc[j][2 * r + x], dl);
-            }
+            const float2 kv = tile_pair<NI, kRow>(kt, t, col), qv = tile_pair<NI, kRow>(qt, t, col);
+            dl = fmaf(qv.x, dQ[j][2 * r], dl);
+            dl = fmaf(qv.y, dQ[j][2 * r + 1], dl);
+            dl = fmaf(kv.x, Kr[j][2 * r] - Kc[j][2 * r], dl);
+            dl = fmaf(kv.y, Kr[j][2 * r + 1] - Kc[j][2 * r + 1], dl);
             if (t0 + t < a.T) {
-                const long long o = (base * a.T + t0 + t) * a.Dk + col;
+                const long long o = (head * a.T + t0 + t) * a.Dk + col;
                 const float q0 = dQ[j][2 * r], q1 = dQ[j][2 * r + 1];
                 const float k0 = Kr[j][2 * r] + Kc[j][2 * r], k1 = Kr[j][2 * r + 1] + Kc[j][2 * r + 1];
                 if (a.dqh || sizeof(TIn) == 4) {
@@ -923,11 +946,14 @@ cudaError_t backward_typed(const Plan& p, const Args& a) {
     g.Dv = a.Dv;
     g.DVP = p.DVP;
     g.n = p.n;
+    g.err = r.err;
     auto kern = grad_kernel<DKP, NI, NM, TIn>;
-    using Tl = GradTiles<DKP, NI, NM>;
-    static_assert(Tl::bytes <= 227 * 1024, "the gradient kernel's tiles have to fit an SM");
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tl::bytes)) != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(p.BH * p.n), kGradThreads, Tl::bytes, a.stream>>>(g);
+    using Tl = GradTiles<DKP, NI, NM, sizeof(TIn) == 4>;
+    static_assert(Tl::smem <= 227 * 1024, "the gradient kernel's tiles have to fit an SM");
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tl::smem)) != cudaSuccess) return e;
+    ScanMaps m;
+    if (!scan_maps(p, a, a.dy, &m)) return cudaErrorUnknown;
+    kern<<<static_cast<unsigned>(p.BH * p.n), kGradThreads, Tl::smem, a.stream>>>(m.v, g);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.dqh) {
         const long long inner = static_cast<long long>(a.T) * a.Dk, total = static_cast<long long>(a.B) * a.Hk * inner;

@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(32 * NW) scan_kernel(const __grid_constant__ C
             uint32_t s[NM][4];
             split_frag<NM>(S[2 * d], S[2 * d + 1], s);
             if constexpr (!kOut)
-                frag_to_planes<NM>(s, a.Sst + cid * NM * a.DVP * DKP, static_cast<long long>(a.DVP) * DKP, DKP, v0, 16 * d, lane);
+                put_tiles<NM>(s, a.Sst + cid * NM * a.DVP * DKP, v0 / 16, DKP / 16, d, lane);
 #pragma unroll
             for (int nn = 0; nn < 4; ++nn)
 #pragma unroll
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(32 * NW) scan_kernel(const __grid_constant__ C
             for (int m = 0; m < 4; ++m) {
                 uint32_t e[NM][4];
                 split_frag<NM>(X[2 * m], X[2 * m + 1], e);
-                frag_to_planes<NM>(e, a.Est + cid * NM * a.DVP * C, static_cast<long long>(a.DVP) * C, C, v0, 16 * m, lane);
+                put_tiles<NM>(e, a.Est + cid * NM * a.DVP * C, v0 / 16, C / 16, m, lane);
             }
         }
         // U = diag(beta) E; Y = scale e^L (Q S) + P U
@@ -488,8 +488,7 @@ __global__ void __launch_bounds__(64 * NS) pair_scan_kernel(const __grid_constan
             split_frag<NM>(S[2 * d], S[2 * d + 1], so[d]);
             put_planes<NM>(ex + Ex::s + (half * kHalf + d) * NM * 32, lane, so[d]);
             if constexpr (!kOut)
-                frag_to_planes<NM>(so[d], a.Sst + cid * NM * a.DVP * DKP, static_cast<long long>(a.DVP) * DKP, DKP, v0,
-                                   d0 + 16 * d, lane);
+                put_tiles<NM>(so[d], a.Sst + cid * NM * a.DVP * DKP, v0 / 16, DKP / 16, half * kHalf + d, lane);
         }
         if (!pair_agree(slice, wait_stage(ring, stage, c / kS, a.err))) return;
         const uint32_t st = base + stage * Tl::bytes;
@@ -586,7 +585,7 @@ __global__ void __launch_bounds__(64 * NS) pair_scan_kernel(const __grid_constan
             const int blk = pair_block(half, j);
             if constexpr (!kOut) {
                 split_frag<NM>(X[j][0], X[j][1], uo[j]);
-                frag_to_planes<NM>(uo[j], a.Est + cid * NM * a.DVP * C, static_cast<long long>(a.DVP) * C, C, v0, 16 * blk, lane);
+                put_tiles<NM>(uo[j], a.Est + cid * NM * a.DVP * C, v0 / 16, C / 16, blk, lane);
             }
             block_scale(X[j], beta, blk, tq);
             if constexpr (kOut) {

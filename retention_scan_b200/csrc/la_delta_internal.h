@@ -46,8 +46,8 @@ struct Plan {
     unsigned char* records;     // [BH][n][record_bytes(planes of both matrices)]
     __nv_bfloat16 *qs, *ks;     // fp32 inputs' planes
     // backward only
-    __nv_bfloat16 *S, *dS;      // [BH][n][planes][DVP][DKP]: states before, gradients after each chunk
-    __nv_bfloat16 *Er, *dR;     // [BH][n][planes][DVP][C]
+    __nv_bfloat16 *S, *dS;      // [BH][n] x planes of DVP x DKP (put_tiles): states before, gradients after each chunk
+    __nv_bfloat16 *Er, *dR;     // [BH][n] x planes of DVP x C
     float *dqh, *dkh;           // [BH][T][Dk] per value head, where key heads are shared
     double* dlog;               // [BH][n]: a chunk's sum of d log g (per-head decay)
     size_t bytes;

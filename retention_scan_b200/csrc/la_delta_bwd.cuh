@@ -436,17 +436,16 @@ __global__ void __launch_bounds__(64 * NS) pair_reverse_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------- gradients of a chunk
-// One block of 8 warps per (b, h, chunk): warp (r, c) = (w % 4, w / 4) holds rows
-// 16 r .. of every product and column half c.  The contraction over the value
-// columns streams 16 of them at a time (S, dS, E, dR, dY) through a ring of bulk
-// copies; then the C x C gradients go through shared memory as A operands of the
-// products with K and Q.  Measured at B2 H16 T4096 D128: 310 us with cp.async
-// into padded rows (6000 instructions a warp and chunk, two in three of them
-// addresses), see DESIGN for this form.
-constexpr int kGradThreads = 256;
+// One block per (b, h, chunk), 16 warps (8 at key width 32): warp (r, c) =
+// (w % 4, w / 4) holds rows 16 r .. of every product and column group c.  The
+// contraction over the value columns streams 16 of them at a time (S, dS, E, dR,
+// dY) through a ring of bulk copies; then the C x C gradients go through shared
+// memory as A operands of the products with K and Q.
 
 template <int DKP, int NI, int NM, bool kF32>
 struct GradTiles {
+    static constexpr int kGroups = DKP >= 64 ? 4 : 2;         // column groups
+    static constexpr int kThreads = 128 * kGroups;
     static constexpr int kRow = DKP + kPad;
     static constexpr int s = 0;                               // one stage: the slice's blocks ...
     static constexpr int ds = s + 2 * NM * (DKP / 16) * kBlk;
@@ -464,8 +463,8 @@ struct GradTiles {
     static constexpr int q = k + 2 * NI * C * kRow;
     static constexpr int tok = q + 2 * NI * C * kRow;         // kTok floats, L, sums
     static constexpr int L = tok + 4 * kTok;
-    static constexpr int sums = L + 8 * C;                    // floats: [4][C] row sums, [4][C] column sums, per warp
-    static constexpr int smem = sums + 4 * (4 * C + 4 * C + 64) + 128;
+    static constexpr int sums = L + 8 * C;                    // floats: [2][kGroups][C] row sums, [4][C] column sums, per warp
+    static constexpr int smem = sums + 4 * (2 * kGroups * C + 4 * C + 64) + 128;
 };
 
 // Brings one slice into a stage.
@@ -520,10 +519,12 @@ __device__ __forceinline__ float2 tile_pair(const __nv_bfloat16* tile, int t, in
 }
 
 template <int DKP, int NI, int NM, typename TIn>
-__global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constant__ CUtensorMap my, GradArgs a) {
+__global__ void __launch_bounds__(DKP >= 64 ? 512 : 256) grad_kernel(const __grid_constant__ CUtensorMap my, GradArgs a) {
     constexpr bool kF32 = sizeof(TIn) == 4;
     using Tl = GradTiles<DKP, NI, NM, kF32>;
-    constexpr int kRow = Tl::kRow, kHalf = DKP / 2, kJ = kHalf / 8, kS = Tl::stages;
+    constexpr int kRow = Tl::kRow, kGroups = Tl::kGroups, kCols = DKP / kGroups, kJ = kCols / 8, kS = Tl::stages;
+    constexpr int kNB = C / 16 / kGroups;  // 16-column blocks of M and N a warp holds
+    constexpr int kGradThreads = Tl::kThreads;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 127) & ~127u;
     unsigned char* smem = smem_raw + (base - smem_addr(smem_raw));
@@ -532,8 +533,8 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
     __nv_bfloat16* qt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::q);
     float* tok = reinterpret_cast<float*>(smem + Tl::tok);
     float2* L = reinterpret_cast<float2*>(smem + Tl::L);
-    float* rowsum = reinterpret_cast<float*>(smem + Tl::sums);  // [dL, k.Z][2 halves][C]
-    float* colsum = rowsum + 4 * C;                             // [4 row groups][C]
+    float* rowsum = reinterpret_cast<float*>(smem + Tl::sums);  // [dL, k.Z][kGroups][C]
+    float* colsum = rowsum + 2 * kGroups * C;                             // [4 row groups][C]
     float* wsum = colsum + 4 * C;                               // per warp
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int wr = warp & 3, wc = warp >> 2;
@@ -562,7 +563,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
     cp_commit();
     if (warp == 0) decay_prefix(L, lane, a.log_g, a.decay_kind, h, bh, t0, a.T);
 
-    float M[4][4] = {}, N[4][4] = {};
+    float M[2 * kNB][4] = {}, N[2 * kNB][4] = {};
     float dQ[kJ][4] = {}, Kr[kJ][4] = {}, Z[kJ][4] = {};
     float in[2][4] = {};  // S dS^T over 16 columns of the key width: its diagonal is summed
     bool ok = true;
@@ -602,21 +603,21 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
             ar[p][3] = r[3];
         }
 #pragma unroll
-        for (int nn = 0; nn < 2; ++nn)
-            if (2 * wc + nn <= wr) {
+        for (int nn = 0; nn < kNB; ++nn)
+            if (kNB * wc + nn <= wr) {
 #pragma unroll
                 for (int p = 0; p < NM; ++p) {
                     uint32_t r[4];
-                    ldsm4t(r, st + Tl::e + (p * (C / 16) + 2 * wc + nn) * 512 + lo);
+                    ldsm4t(r, st + Tl::e + (p * (C / 16) + kNB * wc + nn) * 512 + lo);
                     mma_planes<NI, NM>(M[2 * nn], M[2 * nn + 1], ay, p, r);
                     mma_planes<NM, NM>(N[2 * nn], N[2 * nn + 1], ar, p, r);
                 }
             }
 #pragma unroll
-        for (int d = 0; d < kHalf / 16; ++d)
+        for (int d = 0; d < kCols / 16; ++d)
 #pragma unroll
             for (int p = 0; p < NM; ++p) {
-                const uint32_t at = st + (p * (DKP / 16) + wc * (kHalf / 16) + d) * 512 + lo;
+                const uint32_t at = st + (p * (DKP / 16) + wc * (kCols / 16) + d) * 512 + lo;
                 uint32_t r[4];
                 ldsm4t(r, at + Tl::s);
                 mma_planes<NI, NM>(dQ[2 * d], dQ[2 * d + 1], ay, p, r);
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
     const float* gam = tok;
     const float* rest = tok + C;
     const float* beta = tok + 2 * C;
-    float qk[4][4] = {}, kk[4][4] = {};
+    float qk[2 * kNB][4] = {}, kk[2 * kNB][4] = {};
 #pragma unroll
     for (int d = 0; d < DKP / 16; ++d) {
         uint32_t aq[NI][4], ak[NI][4];
@@ -663,12 +664,12 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
             ldsm4(ak[p], smem_addr(kt + (p * C + 16 * wr) * kRow + 16 * d + off_rows(lane, kRow)));
         }
 #pragma unroll
-        for (int nn = 0; nn < 2; ++nn)
-            if (32 * wc + 16 * nn <= 16 * wr) {
+        for (int nn = 0; nn < kNB; ++nn)
+            if (kNB * wc + nn <= wr) {
 #pragma unroll
                 for (int p = 0; p < NI; ++p) {
                     uint32_t r[4];
-                    ldsm4(r, smem_addr(kt + (p * C + 32 * wc + 16 * nn) * kRow + 16 * d + off_cols(lane, kRow)));
+                    ldsm4(r, smem_addr(kt + (p * C + 16 * (kNB * wc + nn)) * kRow + 16 * d + off_cols(lane, kRow)));
                     mma_planes<NI, NM>(qk[2 * nn], qk[2 * nn + 1], aq, p, r);
                     mma_planes<NI, NM>(kk[2 * nn], kk[2 * nn + 1], ak, p, r);
                 }
@@ -678,7 +679,8 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
     __nv_bfloat16* dpt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::dp);
     __nv_bfloat16* dat = reinterpret_cast<__nv_bfloat16*>(smem + Tl::da);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2 * kNB; ++j) {
+        const int s0 = 16 * kNB * wc + 8 * j + tq;
         float cs[2] = {0.f, 0.f};
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
             float p2[2], a2[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const int s = 32 * wc + 8 * j + tq + x;
+                const int s = s0 + x;
                 const float d = s <= t ? decay_between(L[t], L[s]) : 0.f;
                 const float m = a.scale * d * M[j][2 * r + x], w = s < t ? -d * N[j][2 * r + x] : 0.f;
                 cs[x] += (s <= t ? m * qk[j][2 * r + x] : 0.f) + (s < t ? w * kk[j][2 * r + x] : 0.f);
@@ -696,16 +698,16 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
             uint32_t pl[NM];
             split2<NM>(p2[0], p2[1], pl);
 #pragma unroll
-            for (int p = 0; p < NM; ++p) *reinterpret_cast<uint32_t*>(dpt + (p * C + t) * kCS + 32 * wc + 8 * j + tq) = pl[p];
+            for (int p = 0; p < NM; ++p) *reinterpret_cast<uint32_t*>(dpt + (p * C + t) * kCS + s0) = pl[p];
             split2<NM>(a2[0], a2[1], pl);
 #pragma unroll
-            for (int p = 0; p < NM; ++p) *reinterpret_cast<uint32_t*>(dat + (p * C + t) * kCS + 32 * wc + 8 * j + tq) = pl[p];
+            for (int p = 0; p < NM; ++p) *reinterpret_cast<uint32_t*>(dat + (p * C + t) * kCS + s0) = pl[p];
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) cs[x] += __shfl_xor_sync(0xffffffffu, cs[x], o);
-            if (g == 0) colsum[wr * C + 32 * wc + 8 * j + tq + x] = cs[x];
+            if (g == 0) colsum[wr * C + s0 + x] = cs[x];
         }
     }
     __syncthreads();
@@ -719,7 +721,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
         const float gm = gam[t], rs = rest[t], bt = beta[t];
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
-            const float2 kv = tile_pair<NI, kRow>(kt, t, kHalf * wc + 8 * j + tq);
+            const float2 kv = tile_pair<NI, kRow>(kt, t, kCols * wc + 8 * j + tq);
             const float z0 = rs * Z[j][2 * r], z1 = rs * Z[j][2 * r + 1];
             dQ[j][2 * r] *= a.scale * gm;
             dQ[j][2 * r + 1] *= a.scale * gm;
@@ -746,18 +748,18 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
             }
         }
 #pragma unroll
-        for (int d = 0; d < kHalf / 16; ++d)
+        for (int d = 0; d < kCols / 16; ++d)
 #pragma unroll
             for (int p = 0; p < NI; ++p) {
                 uint32_t r[4];
-                ldsm4t(r, smem_addr(kt + (p * C + 16 * m) * kRow + kHalf * wc + 16 * d + off_rows(lane, kRow)));
+                ldsm4t(r, smem_addr(kt + (p * C + 16 * m) * kRow + kCols * wc + 16 * d + off_rows(lane, kRow)));
                 if (below) {
                     mma_planes<NM, NM>(dQ[2 * d], dQ[2 * d + 1], x, p, r);
                     mma_planes<NM, NM>(Kr[2 * d], Kr[2 * d + 1], y, p, r);
                 }
                 if (above) {
                     mma_planes<NM, NM>(Kc[2 * d], Kc[2 * d + 1], yt, p, r);
-                    ldsm4t(r, smem_addr(qt + (p * C + 16 * m) * kRow + kHalf * wc + 16 * d + off_rows(lane, kRow)));
+                    ldsm4t(r, smem_addr(qt + (p * C + 16 * m) * kRow + kCols * wc + 16 * d + off_rows(lane, kRow)));
                     mma_planes<NM, NM>(Kc[2 * d], Kc[2 * d + 1], xt, p, r);
                 }
             }
@@ -771,7 +773,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
         float dl = 0.f;
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
-            const int col = kHalf * wc + 8 * j + tq;
+            const int col = kCols * wc + 8 * j + tq;
             const float2 kv = tile_pair<NI, kRow>(kt, t, col), qv = tile_pair<NI, kRow>(qt, t, col);
             dl = fmaf(qv.x, dQ[j][2 * r], dl);
             dl = fmaf(qv.y, dQ[j][2 * r + 1], dl);
@@ -804,8 +806,8 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
             zk[r] += __shfl_xor_sync(0xffffffffu, zk[r], o);
         }
         if ((lane & 3) == 0) {
-            rowsum[(0 + wc) * C + t] = dl;
-            rowsum[(2 + wc) * C + t] = zk[r];
+            rowsum[wc * C + t] = dl;
+            rowsum[(kGroups + wc) * C + t] = zk[r];
         }
     }
 #pragma unroll
@@ -821,13 +823,18 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int t = 2 * lane + i;
-            const float z = rowsum[2 * C + t] + rowsum[3 * C + t];
+            float z = 0.f;
+            dl[i] = 0.0;
+#pragma unroll
+            for (int x = 0; x < kGroups; ++x) {
+                z += rowsum[(kGroups + x) * C + t];
+                dl[i] += rowsum[x * C + t];
+            }
             float db = z;
 #pragma unroll
             for (int r = 0; r < 4; ++r) db += colsum[r * C + t];
             if (t0 + t < a.T) a.dbeta[bh * a.T + t0 + t] = db;
             cz = fmaf(beta[t], z, cz);
-            dl[i] = static_cast<double>(rowsum[t]) + rowsum[C + t];
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) cz += __shfl_xor_sync(0xffffffffu, cz, o);
@@ -953,7 +960,7 @@ cudaError_t backward_typed(const Plan& p, const Args& a) {
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tl::smem)) != cudaSuccess) return e;
     ScanMaps m;
     if (!scan_maps(p, a, a.dy, &m)) return cudaErrorUnknown;
-    kern<<<static_cast<unsigned>(p.BH * p.n), kGradThreads, Tl::smem, a.stream>>>(m.v, g);
+    kern<<<static_cast<unsigned>(p.BH * p.n), Tl::kThreads, Tl::smem, a.stream>>>(m.v, g);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.dqh) {
         const long long inner = static_cast<long long>(a.T) * a.Dk, total = static_cast<long long>(a.B) * a.Hk * inner;

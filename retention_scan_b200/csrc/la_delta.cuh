@@ -44,14 +44,15 @@ constexpr int C = 64;            // tokens per chunk
 constexpr int kPad = 8;          // bf16 padding of a shared-memory row: ldmatrix without bank conflicts
 constexpr int kCS = C + kPad;    // row stride of a C-wide tile
 constexpr int kTok = 3 * C;      // floats per chunk of per-token factors: e^L, e^(L_C - L), beta
+constexpr int kTail = 5 * C;     // and, behind them, the prefix L itself as pairs (decay_prefix)
 constexpr int kSq = 2 * C * C;   // bytes of a C x C bf16 plane
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // every barrier wait gives up after this long
 constexpr float kLogFloor = -128.f;  // a decay below e^-128 is zero in fp32 next to anything it is added to
 
 // What prep leaves for each chunk: [planes of (I + A diag(beta))^-1][planes of P]
-// [kTok floats], the matrices as the 128-byte-row swizzled tiles the scans
+// [kTail floats], the matrices as the 128-byte-row swizzled tiles the scans
 // read, so that one bulk copy brings them into shared memory.
-constexpr long long record_bytes(int planes) { return static_cast<long long>(planes) * kSq + sizeof(float) * kTok; }
+constexpr long long record_bytes(int planes) { return static_cast<long long>(planes) * kSq + sizeof(float) * kTail; }
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -407,7 +408,7 @@ struct Feed {
             }
         const unsigned char* rec = records + c * rec_bytes;
         bulk_load(st + Tl::rec, rec, rec_used, bar);
-        bulk_load(st + Tl::tok, rec + rec_bytes - 4 * kTok, 4 * kTok, bar);
+        bulk_load(st + Tl::tok, rec + rec_bytes - 4 * kTail, 4 * kTok, bar);
         if (kV)
             for (int w = 0; w < nv; ++w) tma_load(st + Tl::v + 2048 * w, mv, bar, v0 + 16 * w, c * C, bh);
     }

@@ -461,9 +461,8 @@ struct GradTiles {
     static constexpr int ring = over;
     static constexpr int k = ring + 256;
     static constexpr int q = k + 2 * NI * C * kRow;
-    static constexpr int tok = q + 2 * NI * C * kRow;         // kTok floats, L, sums
-    static constexpr int L = tok + 4 * kTok;
-    static constexpr int sums = L + 8 * C;                    // floats: [2][kGroups][C] row sums, [4][C] column sums, per warp
+    static constexpr int tok = q + 2 * NI * C * kRow;         // kTail floats, sums
+    static constexpr int sums = tok + 4 * kTail;                    // floats: [2][kGroups][C] row sums, [4][C] column sums, per warp
     static constexpr int smem = sums + 4 * (2 * kGroups * C + 4 * C + 64) + 128;
 };
 
@@ -493,8 +492,6 @@ struct GradArgs {
     const void* dy;
     const __nv_bfloat16 *S, *dS, *E, *dR;
     const unsigned char* records;
-    const float* log_g;
-    int decay_kind;
     float scale;
     void *dq, *dk;         // final, where key heads are not shared
     float *dqh, *dkh;      // else per value head
@@ -532,7 +529,7 @@ __global__ void __launch_bounds__(DKP >= 64 ? 512 : 256) grad_kernel(const __gri
     __nv_bfloat16* kt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::k);
     __nv_bfloat16* qt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::q);
     float* tok = reinterpret_cast<float*>(smem + Tl::tok);
-    float2* L = reinterpret_cast<float2*>(smem + Tl::L);
+    const float2* L = reinterpret_cast<const float2*>(tok + kTok);
     float* rowsum = reinterpret_cast<float*>(smem + Tl::sums);  // [dL, k.Z][kGroups][C]
     float* colsum = rowsum + 2 * kGroups * C;                             // [4 row groups][C]
     float* wsum = colsum + 4 * C;                               // per warp
@@ -559,9 +556,9 @@ __global__ void __launch_bounds__(DKP >= 64 ? 512 : 256) grad_kernel(const __gri
     start_ring<Tl>(feed, base, ring, slices, 0, 1);
     load_tile<DKP, NI>(kt, a.kp, hk, t0, tid, kGradThreads);
     load_tile<DKP, NI>(qt, a.qp, hk, t0, tid, kGradThreads);
-    for (int i = tid; i < kTok / 4; i += kGradThreads) cp16(tok + 4 * i, a.records + (cid + 1) * record_bytes(2 * NM) - 4 * kTok + 16 * i, true);
+    for (int i = tid; i < kTail / 4; i += kGradThreads)
+        cp16(tok + 4 * i, a.records + (cid + 1) * record_bytes(2 * NM) - 4 * kTail + 16 * i, true);
     cp_commit();
-    if (warp == 0) decay_prefix(L, lane, a.log_g, a.decay_kind, h, bh, t0, a.T);
 
     float M[2 * kNB][4] = {}, N[2 * kNB][4] = {};
     float dQ[kJ][4] = {}, Kr[kJ][4] = {}, Z[kJ][4] = {};
@@ -936,8 +933,6 @@ cudaError_t backward_typed(const Plan& p, const Args& a) {
     g.E = p.Er;
     g.dR = p.dR;
     g.records = p.records;
-    g.log_g = a.log_g;
-    g.decay_kind = a.decay_kind;
     g.scale = a.scale;
     g.dq = a.dq;
     g.dk = a.dk;

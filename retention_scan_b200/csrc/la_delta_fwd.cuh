@@ -54,7 +54,7 @@ struct PrepTiles {
     static constexpr int kt = tiles;                              // K, Q tiles; then, over them,
     static constexpr int qt = kt + 2 * NI * C * kRow;
     static constexpr int rec = tiles;                             // the record, as it leaves,
-    static constexpr int diag = rec + (NM + NP) * kSq + 4 * kTok; // fp32 [4][16][20]: diagonal blocks of N,
+    static constexpr int diag = rec + (NM + NP) * kSq + 4 * kTail; // fp32 [4][16][20]: diagonal blocks of N,
     static constexpr int np = diag + 4 * 4 * 16 * 20;             // [3 planes][6 blocks] of N below the diagonal,
     static constexpr int tp = np + 2 * 3 * 6 * kBlock;            // [3 planes][4 blocks] E_ii
     static constexpr int end_a = qt + 2 * NI * C * kRow, end_b = tp + 2 * 3 * 4 * kBlock;
@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
         tk[tid] = decay_between(L[tid], make_float2(0.f, 0.f));
         tk[C + tid] = decay_between(L[C - 1], L[tid]);
         tk[2 * C + tid] = bt[tid];
+        reinterpret_cast<float2*>(tk + kTok)[tid] = L[tid];
     }
     const int g = lane >> 2, tq = (lane & 3) * 2;
     const float2 lt[2] = {L[16 * warp + g], L[16 * warp + g + 8]};

@@ -476,6 +476,51 @@ __device__ __forceinline__ void start_ring(const F& feed, uint32_t base, Ring<Tl
     __syncthreads();
 }
 
+// As release_stage and start_ring where a warp more than the slices need costs no
+// registers that they lack: that warp's first lane refills the stages (feed_ring),
+// and a release is one arrival (a release by count and refill: 200 cycles of a
+// chunk's 5100 at the pair's rate).
+template <int kS>
+struct FedRing {
+    Ring<kS> ring;      // left: unused
+    uint64_t empty[kS];
+};
+template <typename Tl, typename F>
+__device__ __forceinline__ void init_fed(const F& feed, FedRing<Tl::stages>* r) {
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Tl::stages; ++s) {
+            mbar_init(&r->ring.full[s], 1);
+            mbar_init(&r->empty[s], feed.warps);
+            r->ring.issued[s] = 0;
+        }
+        r->ring.abort = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+}
+template <typename Tl, typename F>
+__device__ __forceinline__ void feed_ring(const F& feed, uint32_t base, FedRing<Tl::stages>* r, int n, int first, int step, int* err) {
+    constexpr int kS = Tl::stages;
+    volatile int* abort = &r->ring.abort;
+    int j = 0;
+    for (; j < n; ++j) {
+        const int s = j % kS;
+        if (j >= kS && !mbar_wait_bounded(&r->empty[s], ((j / kS) - 1) & 1, kWaitLimitNs)) {
+            *abort = 1;
+            if (err) atomicCAS(err, 0, kErrTmaWait);
+            break;
+        }
+        if (*abort) break;
+        feed.issue(base, &r->ring, s, first + j * step);
+    }
+    // no copy may be in flight when the block ends
+    for (int i = j > kS ? j - kS : 0; i < j; ++i) mbar_wait_bounded(&r->ring.full[i % kS], (i / kS) & 1, kWaitLimitNs);
+}
+__device__ __forceinline__ void release_fed(uint64_t* empty) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(empty);
+}
+
 // ---------------------------------------------------------------- two warps a slice
 // Where a warp per slice leaves tensor cores idle, two share one.  Warp `half`
 // has half of the key width of S^T in its accumulators and two of the chunk's

@@ -236,7 +236,7 @@ struct RevSpace {  // a slice's exchange, in 16-byte words
 };
 
 template <int DKP, int NI, int NM, int NS, typename TIn>
-__global__ void __launch_bounds__(64 * NS) pair_reverse_kernel(const __grid_constant__ CUtensorMap mk,
+__global__ void __launch_bounds__(64 * NS + 32) pair_reverse_kernel(const __grid_constant__ CUtensorMap mk,
                                                                const __grid_constant__ CUtensorMap mq,
                                                                const __grid_constant__ CUtensorMap my, RevArgs a) {
     constexpr bool kF32 = sizeof(TIn) == 4;
@@ -246,7 +246,8 @@ __global__ void __launch_bounds__(64 * NS) pair_reverse_kernel(const __grid_cons
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     unsigned char* smem = smem_raw + (base - smem_addr(smem_raw));
-    Ring<kS>* ring = reinterpret_cast<Ring<kS>*>(smem + kS * Tl::bytes);
+    FedRing<kS>* fed = reinterpret_cast<FedRing<kS>*>(smem + kS * Tl::bytes);
+    Ring<kS>* ring = &fed->ring;
     const int tid = threadIdx.x, lane = tid & 31, slice = tid >> 6, half = (tid >> 5) & 1;
     uint4* ex = reinterpret_cast<uint4*>(smem + Tl::extra) + slice * Ex::words;
     const int bh = blockIdx.x / a.vblocks;
@@ -266,7 +267,11 @@ __global__ void __launch_bounds__(64 * NS) pair_reverse_kernel(const __grid_cons
     feed.v0 = vb;
     feed.nv = nv;
     feed.warps = 2 * nv;
-    start_ring<Tl>(feed, base, ring, a.n, a.n - 1, -1);
+    init_fed<Tl>(feed, fed);
+    if (slice == NS) {
+        if (tid == 64 * NS) feed_ring<Tl>(feed, base, fed, a.n, a.n - 1, -1, a.err);
+        return;
+    }
     if (slice >= nv) return;
 
     const TIn* ysrc = static_cast<const TIn*>(a.dy) + static_cast<long long>(bh) * a.T * a.Dv;
@@ -276,16 +281,16 @@ __global__ void __launch_bounds__(64 * NS) pair_reverse_kernel(const __grid_cons
     float S[DKP / 16][4];
     state_load<DKP / 2>(S, a.d_final ? a.d_final + static_cast<long long>(bh) * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, v0, lane, d0);
 
+    uint32_t so[kHalf][NM][4];  // this half's planes for the chunk that comes
+#pragma unroll
+    for (int d = 0; d < kHalf; ++d) {
+        split_frag<NM>(S[2 * d], S[2 * d + 1], so[d]);
+        put_planes<NM>(ex + Ex::s + (half * kHalf + d) * NM * 32, lane, so[d]);
+    }
+
     for (int i = 0; i < a.n; ++i) {
         const int stage = i % kS, c = a.n - 1 - i;
         const long long cid = static_cast<long long>(bh) * a.n + c;
-        uint32_t so[kHalf][NM][4];
-#pragma unroll
-        for (int d = 0; d < kHalf; ++d) {
-            split_frag<NM>(S[2 * d], S[2 * d + 1], so[d]);
-            put_planes<NM>(ex + Ex::s + (half * kHalf + d) * NM * 32, lane, so[d]);
-            put_tiles<NM>(so[d], a.dSst + cid * NM * a.DVP * DKP, v0 / 16, DKP / 16, half * kHalf + d, lane);
-        }
         if (!pair_agree(slice, wait_stage(ring, stage, i / kS, a.err))) return;
         const uint32_t st = base + stage * Tl::bytes;
         const uint32_t kt = st + Tl::k, qt = st + Tl::q, et = st + Tl::rec, pt = et + NM * kSq;
@@ -293,6 +298,9 @@ __global__ void __launch_bounds__(64 * NS) pair_reverse_kernel(const __grid_cons
         const float* rest = gam + C;
         const float* beta = gam + 2 * C;
 
+#pragma unroll
+        for (int d = 0; d < kHalf; ++d)
+            put_tiles<NM>(so[d], a.dSst + cid * NM * a.DVP * DKP, v0 / 16, DKP / 16, half * kHalf + d, lane);
         // X = (K dS)^T for this warp's tokens, then dU = e^(L_C - L) X + (P^T dY)
         float X[2][2][4] = {};
 #pragma unroll
@@ -429,8 +437,10 @@ __global__ void __launch_bounds__(64 * NS) pair_reverse_kernel(const __grid_cons
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) S[2 * d + j][x] += acc[j][x];
+            split_frag<NM>(S[2 * d], S[2 * d + 1], so[d]);
+            put_planes<NM>(ex + Ex::s + (half * kHalf + d) * NM * 32, lane, so[d]);
         }
-        release_stage<Tl>(feed, base, ring, stage, c - kS);
+        release_fed(&fed->empty[stage]);
     }
     if (a.d_init) state_store<DKP / 2>(S, a.d_init + static_cast<long long>(bh) * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane, d0);
 }
@@ -893,7 +903,7 @@ cudaError_t pair_reverse_run(const Plan& p, const Args& a, RevArgs r) {
     ScanMaps m;
     if (!scan_maps(p, a, a.dy, &m)) return cudaErrorUnknown;
     r.vblocks = (a.Dv + 16 * NS - 1) / (16 * NS);
-    kern<<<static_cast<unsigned>(p.BH * r.vblocks), 64 * NS, Tl::smem, a.stream>>>(m.k, m.q, m.v, r);
+    kern<<<static_cast<unsigned>(p.BH * r.vblocks), 64 * NS + 32, Tl::smem, a.stream>>>(m.k, m.q, m.v, r);
     return cudaGetLastError();
 }
 

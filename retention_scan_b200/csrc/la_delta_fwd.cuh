@@ -439,7 +439,7 @@ struct PairSpace {  // a slice's exchange, in 16-byte words
 };
 
 template <int DKP, int NI, int NM, int NP, int NS, bool kOut, typename TIn>
-__global__ void __launch_bounds__(64 * NS) pair_scan_kernel(const __grid_constant__ CUtensorMap mk,
+__global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_constant__ CUtensorMap mk,
                                                             const __grid_constant__ CUtensorMap mq,
                                                             const __grid_constant__ CUtensorMap mv, ScanArgs a) {
     constexpr bool kF32 = sizeof(TIn) == 4;
@@ -449,7 +449,8 @@ __global__ void __launch_bounds__(64 * NS) pair_scan_kernel(const __grid_constan
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     unsigned char* smem = smem_raw + (base - smem_addr(smem_raw));
-    Ring<kS>* ring = reinterpret_cast<Ring<kS>*>(smem + kS * Tl::bytes);
+    FedRing<kS>* fed = reinterpret_cast<FedRing<kS>*>(smem + kS * Tl::bytes);
+    Ring<kS>* ring = &fed->ring;
     const int tid = threadIdx.x, lane = tid & 31, slice = tid >> 6, half = (tid >> 5) & 1;
     uint4* ex = reinterpret_cast<uint4*>(smem + Tl::extra) + slice * Ex::words;
     const int bh = blockIdx.x / a.vblocks;
@@ -469,7 +470,11 @@ __global__ void __launch_bounds__(64 * NS) pair_scan_kernel(const __grid_constan
     feed.v0 = vb;
     feed.nv = nv;
     feed.warps = 2 * nv;
-    start_ring<Tl>(feed, base, ring, a.n, 0, 1);
+    init_fed<Tl>(feed, fed);
+    if (slice == NS) {
+        if (tid == 64 * NS) feed_ring<Tl>(feed, base, fed, a.n, 0, 1, a.err);
+        return;
+    }
     if (slice >= nv) return;
 
     const TIn* vsrc = static_cast<const TIn*>(a.v) + static_cast<long long>(bh) * a.T * a.Dv;
@@ -480,17 +485,16 @@ __global__ void __launch_bounds__(64 * NS) pair_scan_kernel(const __grid_constan
     state_load<DKP / 2>(S, a.init_state ? a.init_state + static_cast<long long>(bh) * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, v0,
                         lane, d0);
 
+    uint32_t so[kHalf][NM][4];  // this half's planes for the chunk that comes
+#pragma unroll
+    for (int d = 0; d < kHalf; ++d) {
+        split_frag<NM>(S[2 * d], S[2 * d + 1], so[d]);
+        put_planes<NM>(ex + Ex::s + (half * kHalf + d) * NM * 32, lane, so[d]);
+    }
+
     for (int c = 0; c < a.n; ++c) {
         const int stage = c % kS;
         const long long cid = static_cast<long long>(bh) * a.n + c;
-        uint32_t so[kHalf][NM][4];
-#pragma unroll
-        for (int d = 0; d < kHalf; ++d) {
-            split_frag<NM>(S[2 * d], S[2 * d + 1], so[d]);
-            put_planes<NM>(ex + Ex::s + (half * kHalf + d) * NM * 32, lane, so[d]);
-            if constexpr (!kOut)
-                put_tiles<NM>(so[d], a.Sst + cid * NM * a.DVP * DKP, v0 / 16, DKP / 16, half * kHalf + d, lane);
-        }
         if (!pair_agree(slice, wait_stage(ring, stage, c / kS, a.err))) return;
         const uint32_t st = base + stage * Tl::bytes;
         const uint32_t kt = st + Tl::k, qt = st + Tl::q, et = st + Tl::rec, pt = et + NM * kSq;
@@ -498,6 +502,11 @@ __global__ void __launch_bounds__(64 * NS) pair_scan_kernel(const __grid_constan
         const float* rest = gam + C;
         const float* beta = gam + 2 * C;
 
+        if constexpr (!kOut) {
+#pragma unroll
+            for (int d = 0; d < kHalf; ++d)
+                put_tiles<NM>(so[d], a.Sst + cid * NM * a.DVP * DKP, v0 / 16, DKP / 16, half * kHalf + d, lane);
+        }
         // X = (K S)^T, Y = (Q S)^T for this warp's tokens: its own half of S, then the other's
         float X[2][2][4] = {}, Y[2][2][4] = {};
 #pragma unroll
@@ -598,6 +607,33 @@ __global__ void __launch_bounds__(64 * NS) pair_scan_kernel(const __grid_constan
             put_planes<NM>(ex + Ex::w + (half * 2 + j) * NM * 32, lane, wo[j]);
         }
         pair_sync(slice);
+        // This warp's half of S <- e^(L_C) S + K^T diag(e^(L_C - L)) U, and its planes
+        // for the next chunk (the partner read this chunk's before the last two barriers)
+        uint32_t wp[2][NM][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) get_planes<NM>(ex + Ex::w + ((1 - half) * 2 + j) * NM * 32, lane, wp[j]);
+        const float total = gam[C - 1];
+#pragma unroll
+        for (int d = 0; d < kHalf; ++d) {
+            float acc[2][4] = {};
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int p = 0; p < NI; ++p) {
+                    const uint32_t at = kt + p * Tl::kTile + half_step<DKP>(orow.o[d], half);
+                    uint32_t r[4];
+                    ldsm4t(r, at + 2048 * pair_block(half, j));
+                    mma_planes<NM, NM>(acc[0], acc[1], wo[j], p, r);
+                    ldsm4t(r, at + 2048 * pair_block(1 - half, j));
+                    mma_planes<NM, NM>(acc[0], acc[1], wp[j], p, r);
+                }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[2 * d + j][i] = fmaf(total, S[2 * d + j][i], acc[j][i]);
+            split_frag<NM>(S[2 * d], S[2 * d + 1], so[d]);
+            put_planes<NM>(ex + Ex::s + (half * kHalf + d) * NM * 32, lane, so[d]);
+        }
         if constexpr (kOut) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) block_scale(Y[j], gam, pair_block(half, j), tq, a.scale);
@@ -632,31 +668,7 @@ __global__ void __launch_bounds__(64 * NS) pair_scan_kernel(const __grid_constan
 #pragma unroll
             for (int j = 0; j < 2; ++j) block_to_global(Y[j], out, c * C + 16 * pair_block(half, j), a.T, a.Dv, v0, lane);
         }
-        // This warp's half of S <- e^(L_C) S + K^T diag(e^(L_C - L)) U
-        uint32_t wp[2][NM][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) get_planes<NM>(ex + Ex::w + ((1 - half) * 2 + j) * NM * 32, lane, wp[j]);
-        const float total = gam[C - 1];
-#pragma unroll
-        for (int d = 0; d < kHalf; ++d) {
-            float acc[2][4] = {};
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int p = 0; p < NI; ++p) {
-                    const uint32_t at = kt + p * Tl::kTile + half_step<DKP>(orow.o[d], half);
-                    uint32_t r[4];
-                    ldsm4t(r, at + 2048 * pair_block(half, j));
-                    mma_planes<NM, NM>(acc[0], acc[1], wo[j], p, r);
-                    ldsm4t(r, at + 2048 * pair_block(1 - half, j));
-                    mma_planes<NM, NM>(acc[0], acc[1], wp[j], p, r);
-                }
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) S[2 * d + j][i] = fmaf(total, S[2 * d + j][i], acc[j][i]);
-        }
-        release_stage<Tl>(feed, base, ring, stage, c + kS < a.n ? c + kS : -1);
+        release_fed(&fed->empty[stage]);
     }
     if (a.final_state)
         state_store<DKP / 2>(S, a.final_state + static_cast<long long>(bh) * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane, d0);
@@ -702,7 +714,7 @@ cudaError_t pair_scan_run(const Plan& p, const Args& a) {
     if (!scan_maps(p, a, a.v, &m)) return cudaErrorUnknown;
     ScanArgs s = scan_args(p, a);
     s.vblocks = (a.Dv + 16 * NS - 1) / (16 * NS);
-    kern<<<static_cast<unsigned>(p.BH * s.vblocks), 64 * NS, Tl::smem, a.stream>>>(m.k, m.q, m.v, s);
+    kern<<<static_cast<unsigned>(p.BH * s.vblocks), 64 * NS + 32, Tl::smem, a.stream>>>(m.k, m.q, m.v, s);
     return cudaGetLastError();
 }
 

@@ -867,9 +867,12 @@ __global__ void __launch_bounds__(DKP >= 64 ? 512 : 256) grad_kernel(const __gri
     }
 }
 
-// Sum over the value heads of a key head, in their order.
+// Sum over the value heads of a key head, in their order: dq, then dk (blockIdx.y).
 template <typename TOut>
-__global__ void group_sum_kernel(const float* __restrict__ x, TOut* __restrict__ out, int rep, long long inner, long long total) {
+__global__ void group_sum_kernel(const float* __restrict__ dqh, const float* __restrict__ dkh, TOut* __restrict__ dq,
+                                 TOut* __restrict__ dk, int rep, long long inner, long long total) {
+    const float* x = blockIdx.y ? dkh : dqh;
+    TOut* out = blockIdx.y ? dk : dq;
     const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i >= total) return;
     const long long key = i / inner, at = i % inner;
@@ -969,9 +972,9 @@ cudaError_t backward_typed(const Plan& p, const Args& a) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.dqh) {
         const long long inner = static_cast<long long>(a.T) * a.Dk, total = static_cast<long long>(a.B) * a.Hk * inner;
-        const unsigned grid = static_cast<unsigned>((total + 255) / 256);
-        group_sum_kernel<<<grid, 256, 0, a.stream>>>(p.dqh, static_cast<TIn*>(a.dq), a.H / a.Hk, inner, total);
-        group_sum_kernel<<<grid, 256, 0, a.stream>>>(p.dkh, static_cast<TIn*>(a.dk), a.H / a.Hk, inner, total);
+        const dim3 grid(static_cast<unsigned>((total + 255) / 256), 2);
+        group_sum_kernel<<<grid, 256, 0, a.stream>>>(p.dqh, p.dkh, static_cast<TIn*>(a.dq), static_cast<TIn*>(a.dk), a.H / a.Hk, inner,
+                                                     total);
         e = cudaGetLastError();
     }
     return e;

@@ -32,12 +32,14 @@ __global__ void split_kernel(const float* __restrict__ x, __nv_bfloat16* __restr
 // One block per (b, h, chunk): the decays, P, and E = (I + N)^-1, N = A diag(beta)
 // strictly lower triangular, in blocks of 16:
 //   E_jj by forward substitution in fp32 (a thread per column),
-//   E_ij = -E_ii sum_{j <= k < i} N_ik E_kj  on tensor cores, three bf16 planes an
-//   operand (fp32's accuracy): warp j keeps block column j transposed in its
-//   accumulators, as the scans keep the state.
-// Independent of the state, so every chunk runs at once.  A substitution of
-// the whole 64 x 64 matrix by one thread a column was bound by fetching its
-// 2700 unrolled instructions for two warps.
+//   E_ij = -E_ii sum_{j <= k < i} N_ik E_kj  on tensor cores: warp j keeps block
+//   column j transposed in its accumulators, as the scans keep the state, with as
+//   many planes an operand as the record keeps of E.
+// Independent of the state, so every chunk runs at once.  Bound by the latency of
+// these steps with four blocks an SM.  A substitution of the whole 64 x 64 matrix
+// by one thread a column was bound by fetching its 2700 unrolled instructions for
+// two warps (766 us at B1 H32 T65536 D128); K and Q by cp.async spent 5000 of a
+// block's 17 800 cycles on addresses (531 us).
 constexpr int kPrepThreads = 128;
 constexpr int kBS = 24;                // row stride of a 16 x 16 bf16 block: ldmatrix without bank conflicts
 constexpr int kBlock = 16 * kBS;       // elements of such a block
@@ -47,62 +49,76 @@ __host__ __device__ constexpr int low_block(int i, int k) { return i * (i - 1) /
 
 template <int DKP, int NI, int NM, int NP>
 struct PrepTiles {
-    static constexpr int kRow = DKP + kPad;
-    static constexpr int L = 0;                                   // float2: log2 of the decays' prefix, high and low part
-    static constexpr int bt = L + 8 * C;                          // beta
-    static constexpr int tiles = bt + 4 * C;
-    static constexpr int kt = tiles;                              // K, Q tiles; then, over them,
-    static constexpr int qt = kt + 2 * NI * C * kRow;
-    static constexpr int rec = tiles;                             // the record, as it leaves,
+    static constexpr int kPanels = (DKP + 63) / 64, kTile = kPanels * 8192;
+    static constexpr int kt = 0;                                  // K, Q tiles (64-column panels); then, over them,
+    static constexpr int qt = kt + NI * kTile;
+    static constexpr int rec = 0;                                 // the record, as it leaves,
     static constexpr int diag = rec + (NM + NP) * kSq + 4 * kTail; // fp32 [4][16][20]: diagonal blocks of N,
-    static constexpr int np = diag + 4 * 4 * 16 * 20;             // [3 planes][6 blocks] of N below the diagonal,
-    static constexpr int tp = np + 2 * 3 * 6 * kBlock;            // [3 planes][4 blocks] E_ii
-    static constexpr int end_a = qt + 2 * NI * C * kRow, end_b = tp + 2 * 3 * 4 * kBlock;
-    static constexpr int bytes = end_a > end_b ? end_a : end_b;
+    static constexpr int np = diag + 4 * 4 * 16 * 20;             // [NM planes][6 blocks] of N below the diagonal,
+    static constexpr int tp = np + 2 * NM * 6 * kBlock;           // [NM planes][4 blocks] E_ii
+    static constexpr int end_a = qt + NI * kTile, end_b = tp + 2 * NM * 4 * kBlock;
+    static constexpr int L = end_a > end_b ? end_a : end_b;       // float2: log2 of the decays' prefix, high and low part
+    static constexpr int bt = L + 8 * C;                          // beta
+    static constexpr int bar = bt + 4 * C;
+    static constexpr int bytes = bar + 16 + 1024;                 // and the base's alignment
 };
 
 template <int DKP, int NI, int NM, int NP>
-__global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, const float* __restrict__ beta,
-                                                            const float* __restrict__ log_g, int decay_kind, float scale,
-                                                            int H, int Hk, int T, int n, unsigned char* __restrict__ records) {
+__global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constant__ CUtensorMap mk,
+                                                            const __grid_constant__ CUtensorMap mq,
+                                                            const float* __restrict__ beta, const float* __restrict__ log_g,
+                                                            int decay_kind, float scale, int H, int Hk, int planes_apart,
+                                                            int T, int n, unsigned char* __restrict__ records, int* err) {
     using Tl = PrepTiles<DKP, NI, NM, NP>;
-    extern __shared__ __align__(128) unsigned char smem[];
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+    unsigned char* smem = smem_raw + (base - smem_addr(smem_raw));
     float2* L = reinterpret_cast<float2*>(smem + Tl::L);
     float* bt = reinterpret_cast<float*>(smem + Tl::bt);
     unsigned char* rec = smem + Tl::rec;
     float* diag = reinterpret_cast<float*>(smem + Tl::diag);
-    __nv_bfloat16* kt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::kt);
-    __nv_bfloat16* qt = reinterpret_cast<__nv_bfloat16*>(smem + Tl::qt);
     __nv_bfloat16* np = reinterpret_cast<__nv_bfloat16*>(smem + Tl::np);
     __nv_bfloat16* tp = reinterpret_cast<__nv_bfloat16*>(smem + Tl::tp);
-    constexpr int kRow = Tl::kRow;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Tl::bar);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long bh = blockIdx.x / n;
-    const int chunk = blockIdx.x % n, t0 = chunk * C;
-    const int b = static_cast<int>(bh / H), h = static_cast<int>(bh % H);
-    const long long hk = static_cast<long long>(b) * Hk + h / (H / Hk);
-    load_tile<DKP, NI>(kt, k, hk, t0, tid, kPrepThreads);
-    load_tile<DKP, NI>(qt, q, hk, t0, tid, kPrepThreads);
-    cp_commit();
-
+    const int bh = blockIdx.x / n, chunk = blockIdx.x % n, t0 = chunk * C;
+    const int b = bh / H, h = bh % H;
+    if (tid == 32) {
+        const int hk = b * Hk + h / (H / Hk);
+        mbar_init(bar, 1);
+        fence_barrier_init();
+        fence_async_smem();
+        mbar_arrive_expect_tx(bar, 2 * NI * Tl::kTile);
+        for (int p = 0; p < NI; ++p)
+            for (int i = 0; i < Tl::kPanels; ++i) {
+                tma_load(base + Tl::kt + p * Tl::kTile + 8192 * i, &mk, bar, 64 * i, t0, hk + p * planes_apart);
+                tma_load(base + Tl::qt + p * Tl::kTile + 8192 * i, &mq, bar, 64 * i, t0, hk + p * planes_apart);
+            }
+    }
     if (warp == 0) decay_prefix(L, lane, log_g, decay_kind, h, bh, t0, T);
     if (tid >= C) {
         const int t = t0 + tid - C;
-        bt[tid - C] = t < T ? beta[bh * T + t] : 0.f;
+        bt[tid - C] = t < T ? beta[static_cast<long long>(bh) * T + t] : 0.f;
     }
-    cp_wait<0>();
     __syncthreads();
+    // every thread waits for the copies; a block whose copies do not land in time leaves its record as it was
+    const bool landed = mbar_wait_bounded(bar, 0, kWaitLimitNs);
+    if (!__syncthreads_and(landed)) {
+        if (tid == 0 && err) atomicCAS(err, 0, kErrTmaWait);
+        return;
+    }
 
     // K K^T and Q K^T on and below the diagonal: warp w holds rows 16 w .. 16 w + 15
+    const LaneOffsets oc = swz_cols(lane), orow = swz_rows(lane);
     float kk[8][4] = {}, qk[8][4] = {};
 #pragma unroll
     for (int d = 0; d < DKP / 16; ++d) {
         uint32_t ak[NI][4], aq[NI][4];
 #pragma unroll
         for (int p = 0; p < NI; ++p) {
-            ldsm4(ak[p], smem_addr(kt + (p * C + 16 * warp) * kRow + 16 * d + off_rows(lane, kRow)));
-            ldsm4(aq[p], smem_addr(qt + (p * C + 16 * warp) * kRow + 16 * d + off_rows(lane, kRow)));
+            ldsm4(ak[p], base + Tl::kt + p * Tl::kTile + 8192 * (d / 4) + 2048 * warp + orow.o[d % 4]);
+            ldsm4(aq[p], base + Tl::qt + p * Tl::kTile + 8192 * (d / 4) + 2048 * warp + orow.o[d % 4]);
         }
 #pragma unroll
         for (int nn = 0; nn < 4; ++nn)
@@ -110,7 +126,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
 #pragma unroll
                 for (int p = 0; p < NI; ++p) {
                     uint32_t bk[4];
-                    ldsm4(bk, smem_addr(kt + (p * C + 16 * nn) * kRow + 16 * d + off_cols(lane, kRow)));
+                    ldsm4(bk, base + Tl::kt + p * Tl::kTile + 8192 * (d / 4) + 2048 * nn + oc.o[d % 4]);
                     mma_planes<NI, NM>(kk[2 * nn], kk[2 * nn + 1], ak, p, bk);
                     mma_planes<NI, NM>(qk[2 * nn], qk[2 * nn + 1], aq, p, bk);
                 }
@@ -146,10 +162,10 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
                     y = s + 1 < t ? y : 0.f;
                     *reinterpret_cast<float2*>(diag + t * 20 + (s & 15)) = make_float2(x, y);
                 } else {
-                    uint32_t m[3];
-                    split2<3>(x, y, m);
+                    uint32_t m[NM];
+                    split2<NM>(x, y, m);
 #pragma unroll
-                    for (int i = 0; i < 3; ++i)
+                    for (int i = 0; i < NM; ++i)
                         *reinterpret_cast<uint32_t*>(np + (i * 6 + low_block(warp, j / 2)) * kBlock + (t & 15) * kBS + (s & 15)) = m[i];
                 }
                 uint32_t p[NP];
@@ -175,13 +191,13 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
         }
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
-            uint32_t p[3];
-            split2<3>(x[t], 0.f, p);
+            uint32_t p[NM];
+            split2<NM>(x[t], 0.f, p);
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
+            for (int i = 0; i < NM; ++i) {
                 const unsigned short u = static_cast<unsigned short>(p[i]);
                 *reinterpret_cast<unsigned short*>(tp + (i * 4 + warp) * kBlock + t * kBS + lane) = u;
-                if (i < NM) *reinterpret_cast<unsigned short*>(rec + i * kSq + swz64(16 * warp + t, 16 * warp + lane)) = u;
+                *reinterpret_cast<unsigned short*>(rec + i * kSq + swz64(16 * warp + t, 16 * warp + lane)) = u;
             }
         }
     }
@@ -189,12 +205,12 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
 
     // Block column `warp` of E below the diagonal, transposed: col[i] = E_ij^T as A operand planes.
     if (warp < 3) {
-        uint32_t col[4][3][4];
+        uint32_t col[4][NM][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (i == warp) {
 #pragma unroll
-                for (int p = 0; p < 3; ++p) ldsm4t(col[i][p], smem_addr(tp + (p * 4 + i) * kBlock + off_cols(lane, kBS)));
+                for (int p = 0; p < NM; ++p) ldsm4t(col[i][p], smem_addr(tp + (p * 4 + i) * kBlock + off_cols(lane, kBS)));
             }
 #pragma unroll
         for (int i = 1; i < 4; ++i)
@@ -204,26 +220,26 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
                 for (int m = 0; m < i; ++m)
                     if (m >= warp) {
 #pragma unroll
-                        for (int p = 0; p < 3; ++p) {
+                        for (int p = 0; p < NM; ++p) {
                             uint32_t r[4];
                             ldsm4(r, smem_addr(np + (p * 6 + low_block(i, m)) * kBlock + off_cols(lane, kBS)));
-                            mma_planes<3, 3>(acc[0], acc[1], col[m], p, r);
+                            mma_planes<NM, NM>(acc[0], acc[1], col[m], p, r);
                         }
                     }
-                uint32_t a[3][4];
-                split_frag<3>(acc[0], acc[1], a);
+                uint32_t a[NM][4];
+                split_frag<NM>(acc[0], acc[1], a);
                 float e[2][4] = {};
 #pragma unroll
-                for (int p = 0; p < 3; ++p) {
+                for (int p = 0; p < NM; ++p) {
                     uint32_t r[4];
                     ldsm4(r, smem_addr(tp + (p * 4 + i) * kBlock + off_cols(lane, kBS)));
-                    mma_planes<3, 3>(e[0], e[1], a, p, r);
+                    mma_planes<NM, NM>(e[0], e[1], a, p, r);
                 }
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int y = 0; y < 4; ++y) e[x][y] = -e[x][y];
-                split_frag<3>(e[0], e[1], col[i]);
+                split_frag<NM>(e[0], e[1], col[i]);
 #pragma unroll
                 for (int p = 0; p < NM; ++p)
 #pragma unroll
@@ -238,7 +254,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(Planes q, Planes k, 
     fence_async_smem();
     __syncthreads();
     constexpr long long kRec = record_bytes(NM + NP);
-    if (tid == 0) bulk_store(records + (bh * n + chunk) * kRec, smem_addr(rec), static_cast<uint32_t>(kRec));
+    if (tid == 0) bulk_store(records + static_cast<long long>(blockIdx.x) * kRec, smem_addr(rec), static_cast<uint32_t>(kRec));
 }
 
 // ---------------------------------------------------------------- scan
@@ -507,6 +523,11 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
             for (int d = 0; d < kHalf; ++d)
                 put_tiles<NM>(so[d], a.Sst + cid * NM * a.DVP * DKP, v0 / 16, DKP / 16, half * kHalf + d, lane);
         }
+        float early[kF32 ? 2 : 1][2][4];  // fp32 values come straight from global memory: their latency passes under the products
+        if constexpr (kF32) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) block_from_global(early[j], vsrc, c * C + 16 * pair_block(half, j), a.T, a.Dv, v0, lane);
+        }
         // X = (K S)^T, Y = (Q S)^T for this warp's tokens: its own half of S, then the other's
         float X[2][2][4] = {}, Y[2][2][4] = {};
 #pragma unroll
@@ -544,10 +565,14 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
         for (int j = 0; j < 2; ++j) {
             const int blk = pair_block(half, j);
             float R[2][4];
-            if constexpr (kF32)
-                block_from_global(R, vsrc, c * C + 16 * blk, a.T, a.Dv, v0, lane);
-            else
+            if constexpr (kF32) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) R[x][i] = early[j][x][i];
+            } else {
                 block_from_tile(R, st + Tl::v + 2048 * slice, blk, lane);
+            }
             block_scale(X[j], gam, blk, tq);
 #pragma unroll
             for (int x = 0; x < 2; ++x)
@@ -685,8 +710,11 @@ cudaError_t prep_run(const Plan& p, const Args& a) {
     constexpr int smem = PrepTiles<DKP, NI, NM, NP>::bytes;
     cudaError_t e = allow_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(p.BH * p.n), kPrepThreads, smem, a.stream>>>(p.q, p.k, a.beta, a.log_g, a.decay_kind, a.scale,
-                                                                             a.H, a.Hk, a.T, p.n, p.records);
+    ScanMaps m;
+    if (!scan_maps(p, a, a.v, &m)) return cudaErrorUnknown;
+    kern<<<static_cast<unsigned>(p.BH * p.n), kPrepThreads, smem, a.stream>>>(m.k, m.q, a.beta, a.log_g, a.decay_kind, a.scale,
+                                                                             a.H, a.Hk, a.B * a.Hk, a.T, p.n, p.records,
+                                                                             device_error_word());
     return cudaGetLastError();
 }
 

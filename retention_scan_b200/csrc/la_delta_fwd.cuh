@@ -36,7 +36,7 @@ __global__ void split_kernel(const float* __restrict__ x, __nv_bfloat16* __restr
 //   column j transposed in its accumulators, as the scans keep the state, with as
 //   many planes an operand as the record keeps of E.
 // Independent of the state, so every chunk runs at once.  Bound by the latency of
-// these steps with four blocks an SM.  A substitution of the whole 64 x 64 matrix
+// these steps with five blocks an SM.  A substitution of the whole 64 x 64 matrix
 // by one thread a column was bound by fetching its 2700 unrolled instructions for
 // two warps (766 us at B1 H32 T65536 D128); K and Q by cp.async spent 5000 of a
 // block's 17 800 cycles on addresses (531 us).
@@ -53,10 +53,11 @@ struct PrepTiles {
     static constexpr int kt = 0;                                  // K, Q tiles (64-column panels); then, over them,
     static constexpr int qt = kt + NI * kTile;
     static constexpr int rec = 0;                                 // the record, as it leaves,
-    static constexpr int diag = rec + (NM + NP) * kSq + 4 * kTail; // fp32 [4][16][20]: diagonal blocks of N,
-    static constexpr int np = diag + 4 * 4 * 16 * 20;             // [NM planes][6 blocks] of N below the diagonal,
-    static constexpr int tp = np + 2 * NM * 6 * kBlock;           // [NM planes][4 blocks] E_ii
-    static constexpr int end_a = qt + NI * kTile, end_b = tp + 2 * NM * 4 * kBlock;
+    static constexpr int np = rec + (NM + NP) * kSq + 4 * kTail;  // [NM planes][6 blocks] of N below the diagonal,
+    static constexpr int own = np + 2 * NM * 6 * kBlock;          // and per warp its diagonal block of N (fp32 [16][20]),
+    static constexpr int kOwn = 2 * NM * kBlock;                  // then over it the planes of E_ii
+    static_assert(kOwn >= 4 * 16 * 20, "a diagonal block has to fit its planes' place");
+    static constexpr int end_a = qt + NI * kTile, end_b = own + 4 * kOwn;
     static constexpr int L = end_a > end_b ? end_a : end_b;       // float2: log2 of the decays' prefix, high and low part
     static constexpr int bt = L + 8 * C;                          // beta
     static constexpr int bar = bt + 4 * C;
@@ -76,9 +77,8 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
     float2* L = reinterpret_cast<float2*>(smem + Tl::L);
     float* bt = reinterpret_cast<float*>(smem + Tl::bt);
     unsigned char* rec = smem + Tl::rec;
-    float* diag = reinterpret_cast<float*>(smem + Tl::diag);
     __nv_bfloat16* np = reinterpret_cast<__nv_bfloat16*>(smem + Tl::np);
-    __nv_bfloat16* tp = reinterpret_cast<__nv_bfloat16*>(smem + Tl::tp);
+    __nv_bfloat16* tp = reinterpret_cast<__nv_bfloat16*>(smem + Tl::own);  // [4 warps][NM planes]
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Tl::bar);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
                 tma_load(base + Tl::qt + p * Tl::kTile + 8192 * i, &mq, bar, 64 * i, t0, hk + p * planes_apart);
             }
     }
+    float* diag = reinterpret_cast<float*>(smem + Tl::own + warp * Tl::kOwn);
     if (warp == 0) decay_prefix(L, lane, log_g, decay_kind, h, bh, t0, T);
     if (tid >= C) {
         const int t = t0 + tid - C;
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
                     p1 = s + 1 <= t ? p1 : 0.f;
                     x = s < t ? x : 0.f;
                     y = s + 1 < t ? y : 0.f;
-                    *reinterpret_cast<float2*>(diag + t * 20 + (s & 15)) = make_float2(x, y);
+                    *reinterpret_cast<float2*>(diag + (t & 15) * 20 + (s & 15)) = make_float2(x, y);
                 } else {
                     uint32_t m[NM];
                     split2<NM>(x, y, m);
@@ -183,12 +184,13 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
             float a0 = t == lane ? 1.f : 0.f, a1 = 0.f;
 #pragma unroll
             for (int s = 0; s < t; s += 2) {
-                const float2 m = *reinterpret_cast<const float2*>(diag + (16 * warp + t) * 20 + s);
+                const float2 m = *reinterpret_cast<const float2*>(diag + t * 20 + s);
                 a0 = fmaf(-m.x, x[s], a0);
                 if (s + 1 < t) a1 = fmaf(-m.y, x[s + 1], a1);
             }
             x[t] = a0 + a1;
         }
+        __syncwarp(0xffffu);  // the block's columns are all read
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
             uint32_t p[NM];
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < NM; ++i) {
                 const unsigned short u = static_cast<unsigned short>(p[i]);
-                *reinterpret_cast<unsigned short*>(tp + (i * 4 + warp) * kBlock + t * kBS + lane) = u;
+                *reinterpret_cast<unsigned short*>(tp + (warp * NM + i) * kBlock + t * kBS + lane) = u;
                 *reinterpret_cast<unsigned short*>(rec + i * kSq + swz64(16 * warp + t, 16 * warp + lane)) = u;
             }
         }
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
         for (int i = 0; i < 4; ++i)
             if (i == warp) {
 #pragma unroll
-                for (int p = 0; p < NM; ++p) ldsm4t(col[i][p], smem_addr(tp + (p * 4 + i) * kBlock + off_cols(lane, kBS)));
+                for (int p = 0; p < NM; ++p) ldsm4t(col[i][p], smem_addr(tp + (i * NM + p) * kBlock + off_cols(lane, kBS)));
             }
 #pragma unroll
         for (int i = 1; i < 4; ++i)
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
 #pragma unroll
                 for (int p = 0; p < NM; ++p) {
                     uint32_t r[4];
-                    ldsm4(r, smem_addr(tp + (p * 4 + i) * kBlock + off_cols(lane, kBS)));
+                    ldsm4(r, smem_addr(tp + (i * NM + p) * kBlock + off_cols(lane, kBS)));
                     mma_planes<NM, NM>(e[0], e[1], a, p, r);
                 }
 #pragma unroll

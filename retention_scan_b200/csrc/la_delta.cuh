@@ -33,6 +33,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "la_internal.h"
 #include "la_sm100.cuh"
@@ -527,7 +528,7 @@ __device__ __forceinline__ void release_fed(uint64_t* empty) {
 // four 16-token blocks, {0, 3} or {1, 2}, which have the same share of the
 // triangular products.  What one needs of the other (split operands) passes
 // through shared memory in register order, a 16-byte access a lane.
-__device__ __forceinline__ int pair_block(int half, int j) { return half ? 1 + j : 3 * j; }
+__device__ constexpr int pair_block(int half, int j) { return half ? 1 + j : 3 * j; }
 
 // Planes [N][32 lanes] of an A operand.
 template <int N>

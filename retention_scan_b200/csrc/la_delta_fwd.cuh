@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
     unsigned char* smem = smem_raw + (base - smem_addr(smem_raw));
     FedRing<kS>* fed = reinterpret_cast<FedRing<kS>*>(smem + kS * Tl::bytes);
     Ring<kS>* ring = &fed->ring;
-    const int tid = threadIdx.x, lane = tid & 31, slice = tid >> 6, half = (tid >> 5) & 1;
+    const int tid = threadIdx.x, lane = tid & 31, slice = tid >> 6;
     uint4* ex = reinterpret_cast<uint4*>(smem + Tl::extra) + slice * Ex::words;
     const int bh = blockIdx.x / a.vblocks;
     const int vb = blockIdx.x % a.vblocks * 16 * NS, v0 = vb + 16 * slice;
@@ -498,7 +498,10 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
     const TIn* vsrc = static_cast<const TIn*>(a.v) + static_cast<long long>(bh) * a.T * a.Dv;
     const int tq = (lane & 3) * 2;
     const LaneOffsets oc = swz_cols(lane), orow = swz_rows(lane);
-    const int d0 = half * (DKP / 2);
+    // one body for each half: every block index below is a constant
+    auto scan = [&](auto which) {
+    constexpr int half = decltype(which)::value;
+    constexpr int d0 = half * (DKP / 2);
     float S[DKP / 16][4];
     state_load<DKP / 2>(S, a.init_state ? a.init_state + static_cast<long long>(bh) * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, v0,
                         lane, d0);
@@ -512,10 +515,11 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
 
     for (int c = 0; c < a.n; ++c) {
         const int stage = c % kS;
-        const long long cid = static_cast<long long>(bh) * a.n + c;
+        [[maybe_unused]] const long long cid = static_cast<long long>(bh) * a.n + c;
         if (!pair_agree(slice, wait_stage(ring, stage, c / kS, a.err))) return;
         const uint32_t st = base + stage * Tl::bytes;
-        const uint32_t kt = st + Tl::k, qt = st + Tl::q, et = st + Tl::rec, pt = et + NM * kSq;
+        const uint32_t kt = st + Tl::k, et = st + Tl::rec;
+        [[maybe_unused]] const uint32_t qt = st + Tl::q, pt = et + NM * kSq;
         const float* gam = reinterpret_cast<const float*>(smem + stage * Tl::bytes + Tl::tok);
         const float* rest = gam + C;
         const float* beta = gam + 2 * C;
@@ -525,42 +529,41 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
             for (int d = 0; d < kHalf; ++d)
                 put_tiles<NM>(so[d], a.Sst + cid * NM * a.DVP * DKP, v0 / 16, DKP / 16, half * kHalf + d, lane);
         }
-        float early[kF32 ? 2 : 1][2][4];  // fp32 values come straight from global memory: their latency passes under the products
+        [[maybe_unused]] float early[kF32 ? 2 : 1][2][4];  // fp32 values come straight from global memory: their latency passes under the products
         if constexpr (kF32) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) block_from_global(early[j], vsrc, c * C + 16 * pair_block(half, j), a.T, a.Dv, v0, lane);
         }
-        // X = (K S)^T, Y = (Q S)^T for this warp's tokens: its own half of S, then the other's
-        float X[2][2][4] = {}, Y[2][2][4] = {};
+        // (K S)^T or (Q S)^T for this warp's tokens: its own half of S, then the other's
+        auto through_state = [&](float (&acc)[2][2][4], uint32_t tile) {
 #pragma unroll
-        for (int o = 0; o < 2; ++o) {
-            const int hh = o ? 1 - half : half;
+            for (int o = 0; o < 2; ++o) {
+                const int hh = o ? 1 - half : half;
 #pragma unroll
-            for (int d = 0; d < kHalf; ++d) {
-                uint32_t s[NM][4];
-                if (o) {
-                    get_planes<NM>(ex + Ex::s + (hh * kHalf + d) * NM * 32, lane, s);
-                } else {
+                for (int d = 0; d < kHalf; ++d) {
+                    uint32_t s[NM][4];
+                    if (o) {
+                        get_planes<NM>(ex + Ex::s + (hh * kHalf + d) * NM * 32, lane, s);
+                    } else {
 #pragma unroll
-                    for (int p = 0; p < NM; ++p)
+                        for (int p = 0; p < NM; ++p)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) s[p][i] = so[d][p][i];
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int p = 0; p < NI; ++p) {
-                        const uint32_t at = p * Tl::kTile + 2048 * pair_block(half, j) + half_step<DKP>(oc.o[d], hh);
-                        uint32_t r[4];
-                        ldsm4(r, kt + at);
-                        mma_planes<NM, NM>(X[j][0], X[j][1], s, p, r);
-                        if constexpr (kOut) {
-                            ldsm4(r, qt + at);
-                            mma_planes<NM, NM>(Y[j][0], Y[j][1], s, p, r);
-                        }
+                            for (int i = 0; i < 4; ++i) s[p][i] = so[d][p][i];
                     }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int p = 0; p < NI; ++p) {
+                            uint32_t r[4];
+                            ldsm4(r, tile + p * Tl::kTile + 2048 * pair_block(half, j) + half_step<DKP>(oc.o[d], hh));
+                            mma_planes<NM, NM>(acc[j][0], acc[j][1], s, p, r);
+                        }
+                }
             }
-        }
+        };
+        float X[2][2][4] = {};
+        [[maybe_unused]] float Y[2][2][4] = {};
+        through_state(X, kt);
         // R = V - e^L (K S), exchanged
         uint32_t ro[2][NM][4];
 #pragma unroll
@@ -609,12 +612,14 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
 #pragma unroll
                         for (int p = 0; p < NM; ++p) {
                             uint32_t e[4];
-                            ldsm4(e, et + p * kSq + 2048 * blk + (oc.o[0] ^ (m << 5)));
+                            ldsm4(e, et + p * kSq + 2048 * blk + oc.o[m]);
                             mma_planes<NM, NM>(X[j][0], X[j][1], r, p, e);
                         }
                     }
                 }
             }
+        // Q S is not on the way to the next state: its products fill the waits around E and U
+        if constexpr (kOut) through_state(Y, qt);
         // U = diag(beta) E, and diag(e^(L_C - L)) U for the state, exchanged
         uint32_t uo[2][NM][4], wo[2][NM][4];
 #pragma unroll
@@ -685,7 +690,7 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
 #pragma unroll
                             for (int p = 0; p < NP; ++p) {
                                 uint32_t r[4];
-                                ldsm4(r, pt + p * kSq + 2048 * blk + (oc.o[0] ^ (m << 5)));
+                                ldsm4(r, pt + p * kSq + 2048 * blk + oc.o[m]);
                                 mma_planes<NM, NM>(Y[j][0], Y[j][1], u, p, r);
                             }
                         }
@@ -699,6 +704,11 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
     }
     if (a.final_state)
         state_store<DKP / 2>(S, a.final_state + static_cast<long long>(bh) * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane, d0);
+    };
+    if ((tid >> 5) & 1)
+        scan(std::integral_constant<int, 1>{});
+    else
+        scan(std::integral_constant<int, 0>{});
 }
 
 template <typename K>

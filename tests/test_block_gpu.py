@@ -400,3 +400,44 @@ def test_block_chain_forward_backward_and_token_by_token():
         rows.append(m.gated_norm(y, c["gate"][:, t], c["w"]))
     assert rel(torch.stack(rows, 1), f64(s["out"])) <= 2 * 2.0 ** -7
     assert rel(state, f64(s["S"])) <= 2.0 ** -14
+
+
+def test_refusals_on_the_gpu():
+    m = la()
+    x = torch.randn(2, 3, 5, 16, device="cuda")
+    w, f = torch.ones(16, device="cuda"), torch.ones(4, device="cuda")
+    for bad, error in [
+        (lambda: m.gated_norm(x, x[:1]), ValueError), (lambda: m.gated_norm(x, x.bfloat16()), TypeError),
+        (lambda: m.gated_norm(x.transpose(2, 3)), ValueError), (lambda: m.gated_norm(x, None, w[:8]), ValueError),
+        (lambda: m.gated_norm(x, None, w.bfloat16()), TypeError), (lambda: m.gated_norm(x.half()), TypeError),
+        (lambda: m.gated_norm(x, out=x[:1].expand(2, 3, 5, 16)), ValueError), (lambda: m.gated_norm(x, kind=4), m.LAError),
+        (lambda: m.gated_norm(x, eps=-1.0), m.LAError), (lambda: m.gated_norm(x, x.cpu()), ValueError),
+        (lambda: m.gated_norm(torch.zeros(2, 8200, device="cuda")), m.LAError),
+        (lambda: m.gated_norm_backward(None, x), ValueError), (lambda: m.gated_norm_backward(x[:1], x), ValueError),
+        (lambda: m.gated_norm_backward(x, x, out=(None, None, None)), ValueError),
+        (lambda: m.gated_norm_backward(x, x, x, out=(x.clone(), None, None)), ValueError),
+        (lambda: m.gated_norm_backward(x, x, None, w, workspace=torch.zeros(8, dtype=torch.uint8, device="cuda")), m.LAError),
+        (lambda: m.rotary(x, torch.ones(9, device="cuda")), ValueError), (lambda: m.rotary(x, f.double()), TypeError),
+        (lambda: m.rotary(x[0], f), ValueError), (lambda: m.rotary(x, f, torch.zeros(4, dtype=torch.int64, device="cuda")), ValueError),
+        (lambda: m.rotary(x, f, torch.zeros(5, dtype=torch.int32, device="cuda")), TypeError),
+        (lambda: m.rotary(x, f, torch.zeros(5, dtype=torch.int64, device="cuda"), start=3), ValueError),
+        (lambda: m.rotary(x, f, None, x[:1]), ValueError), (lambda: m.rotary(x, f, out2=x), ValueError),
+        (lambda: m.rotary(x, f, layout=3), m.LAError), (lambda: m.rotary(x, f, mscale=float("inf")), m.LAError),
+    ]:
+        with pytest.raises(error):
+            bad()
+
+
+def test_rows_outside_a_view_stay_as_they_were():
+    wide = torch.full((3, 7, 200), 7.0, device="cuda").bfloat16()
+    x = torch.randn(3, 5, 64, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    view = wide[:, 1:6, 65:129]
+    la().gated_norm(x, out=view)
+    assert torch.equal(view, la().gated_norm(x))
+    mask = torch.ones_like(wide, dtype=torch.bool)
+    mask[:, 1:6, 65:129] = False
+    assert (wide[mask] == 7.0).all()
+    freq, _ = la().rotary_frequencies(32, device="cuda")
+    q = x.view(3, 1, 5, 64)
+    la().rotary(q, freq, out=view.unsqueeze(1))
+    assert torch.equal(view.unsqueeze(1), la().rotary(q, freq)) and (wide[mask] == 7.0).all()

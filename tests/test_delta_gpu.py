@@ -389,3 +389,75 @@ def test_decode_in_a_graph_moves_the_state_on_each_replay():
         graph.replay()
         y = la().delta_decode_step(q, k, v, beta, want, 2, lg)
         assert torch.equal(state, want) and torch.equal(out, y)
+
+
+# ------------------------------------------------------------------ around the calls
+def banded(shape, dtype, fill=0x5A):
+    """A contiguous tensor inside a larger buffer of one byte pattern, and a check that the rest still has it."""
+    n = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+    pad = 4096
+    raw = torch.full((n + 2 * pad,), fill, dtype=torch.uint8, device="cuda")
+    t = raw[pad:pad + n].view(dtype).view(shape)
+
+    def intact():
+        return bool((raw[:pad] == fill).all() and (raw[pad + n:] == fill).all())
+    return t, intact
+
+
+@pytest.mark.parametrize("T,Dk,Dv,dtype", [(1, 16, 16, torch.bfloat16), (67, 48, 80, torch.bfloat16), (130, 128, 112, torch.bfloat16),
+                                           (67, 33, 21, torch.float32), (65, 128, 127, torch.float32)])
+def test_nothing_is_written_outside(T, Dk, Dv, dtype):
+    B, H, Hk = 2, 4, 2
+    q, k, v, beta, lg, S0 = dev(*make(B, H, Hk, T, Dk, Dv, dtype, seed=T))
+    y, c1 = banded((B, H, T, Dv), dtype)
+    S, c2 = banded((B, H, Dk, Dv), torch.float32)
+    ws, c3 = banded((la().delta_workspace_size(B, H, T, Dk, Dv, dtype, key_heads=Hk),), torch.uint8)
+    la().delta_forward(q, k, v, beta, 2, lg, S0, out=y, final_state=S, workspace=ws)
+    outs, checks = zip(*(banded(t.shape, t.dtype) for t in (q, k, v, beta, lg, S0)))
+    wb, c4 = banded((la().delta_backward_workspace_size(B, H, T, Dk, Dv, dtype, key_heads=Hk),), torch.uint8)
+    la().delta_backward(q, k, v, beta, v, 2, lg, S0, S0, workspace=wb, out=outs)
+    state, c5 = banded(S0.shape, torch.float32)
+    state.copy_(S0)
+    o, c6 = banded((B, H, Dv), dtype)
+    la().delta_decode_step(*(x[:, :, 0].contiguous() for x in (q, k, v, beta)), state, 2, lg[:, :, 0].contiguous(), out=o)
+    torch.cuda.synchronize()
+    assert all(c() for c in (c1, c2, c3, c4, c5, c6, *checks))
+
+
+def test_two_streams_at_once():
+    a, b = (dev(*make(2, 8, 4, 300, 64, 64, seed=s)) for s in (1, 2))
+    want = [la().delta_backward(*x[:4], x[2], 2, *x[4:]) for x in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, (s, x) in enumerate(zip(streams, (a, b))):
+            got[i].append(la().delta_backward(*x[:4], x[2], 2, *x[4:], stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(p, q) for p, q in zip(r, want[i]))
+
+
+def test_refusals_on_the_gpu():
+    q, k, v, beta, lg, S0 = dev(*make(1, 4, 2, 5, 16, 16))
+    f, m = la().delta_forward, la()
+    for bad, error in [
+        (lambda: f(q, k[:, :, :4], v, beta), ValueError), (lambda: f(q, k, v[:, :3], beta), ValueError),
+        (lambda: f(q, k, v.float(), beta), TypeError), (lambda: f(q, k, v, beta.double()), TypeError),
+        (lambda: f(q, k, v, beta.cpu()), ValueError), (lambda: f(q.transpose(2, 3), k, v, beta), ValueError),
+        (lambda: f(q.half(), k.half(), v.half(), beta), TypeError), (lambda: f(q, k, v, beta, 2), ValueError),
+        (lambda: f(q, k, v, beta, 7, lg), ValueError), (lambda: f(q, k, v, beta, 1, lg), ValueError),
+        (lambda: f(q, k, v, beta, init_state=S0[:, :2]), ValueError), (lambda: f(q, k, v, None), ValueError),
+        (lambda: f(q, k, v, beta, out=torch.empty_like(v).float()), TypeError),
+        (lambda: f(q, k, v, beta, q_scale=float("nan")), m.LAError),
+        (lambda: f(q, k, v, beta, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), m.LAError),
+        (lambda: f(q, k, v, beta, workspace=torch.empty(1 << 20, device="cuda")), ValueError),
+        (lambda: m.delta_backward(q, k, v, beta, None), ValueError),
+        (lambda: m.delta_backward(q, k, v, beta, v[:, :, :3]), ValueError),
+        (lambda: m.delta_backward(q, k, v, beta, v, out=(None,) * 6), ValueError),
+        (lambda: m.delta_decode_step(q[:, :, 0], k[:, :, 0], v[:, :, 0], beta[:, :, 0], S0), ValueError),
+        (lambda: m.delta_decode_step(*(x[:, :, 0].contiguous() for x in (q, k, v, beta)), None), ValueError),
+    ]:
+        with pytest.raises(error):
+            bad()

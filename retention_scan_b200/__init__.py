@@ -136,7 +136,7 @@ def lib():
         L.la_delta_backward_workspace_size.restype = sz
         L.la_delta_decode_step.argtypes = [vp, vp, vp, vp, ctypes.POINTER(_Decay), f, vp, vp, i, i, i, i, i, i, vp]
         L.la_delta_decode_step.restype = i
-        vw = ctypes.POINTER(_View)
+        vw = vp  # address of an la_view
         L.la_gated_norm.argtypes = [vw, vw, vp, vw, vw, i, i, i, i, i, i, f, f, i, vp]
         L.la_gated_norm.restype = i
         L.la_gated_norm_backward.argtypes = [vw, vw, vw, vp, vw, vw, vp, i, i, i, i, i, i, f, f, i, vp, sz, vp]

@@ -7,40 +7,60 @@ Tensors are read and written through their strides (the last dimension dense),
 so projections laid out [B,T,H,D] and the scans' [B,H,T,D] need no copy
 between them: pass x.transpose(1, 2).
 """
-import ctypes
+import array
+import functools
 import math
 
 import torch
 
 from . import (GATE_SIGMOID, GATE_SILU, NORM_L2, NORM_LAYER, NORM_RMS, ROTARY_HALF, ROTARY_INTERLEAVED, _check, _device,
-               _dtype_code, _need, _raw_stream, _View, lib)
+               _dtype_code, _need, _raw_stream, lib)
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _view(t, name, shape, dtype, device, output=False):
-    """The tensor as a view of rows (its leading dimensions padded to three)."""
-    if t is None:
-        return None
+def _check_view(t, name, shape, dtype, device, output=False):
+    """The tensor's strides, after the checks that make it a view of rows."""
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
-    lead, n = t.stride(), len(shape)
+    lead = t.stride()
     if lead[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be dense")
     if output and 0 in lead and any(k > 1 and s == 0 for k, s in zip(shape[:-1], lead)):
         raise ValueError(f"{name}: an output's rows must not share memory")
-    if n == 4:
-        return _View(t.data_ptr(), lead[0], lead[1], lead[2])
-    return _View(t.data_ptr(), *([0] * (4 - n)), *lead[:-1])
+    return lead
 
 
-def _ref(v):
-    return ctypes.byref(v) if v is not None else None
+class _Views:
+    """la_view records of a call's tensors, side by side in one buffer (a
+    structure object each took as long as the checks)."""
+
+    def __init__(self, shape, dtype, device):
+        self.shape, self.dtype, self.device, self.words, self.at = shape, dtype, device, [], []
+
+    def add(self, t, name, output=False, shape=None):
+        if t is None:
+            self.at.append(None)
+            return
+        shape = shape if shape is not None else self.shape
+        lead = _check_view(t, name, shape, self.dtype, self.device, output)
+        self.at.append(len(self.words))
+        n = len(shape)
+        if n == 4:
+            self.words += (t.data_ptr(), lead[0], lead[1], lead[2])
+        else:  # fewer leading dimensions: padded to three in front
+            self.words += (t.data_ptr(), *((0,) * (4 - n)), *lead[:-1])
+
+    def addresses(self):
+        """Addresses of the records in the order they were added (None: absent); the buffer lives as long as self."""
+        self.buffer = array.array("q", self.words)
+        base = self.buffer.buffer_info()[0]
+        return [None if i is None else base + 8 * i for i in self.at]
 
 
 def _rows(x, name="x"):
@@ -69,15 +89,22 @@ def gated_norm(x, gate=None, weight=None, residual=None, kind=NORM_RMS, activati
     D, code = shape[-1], _dtype_code(dtype)
     if out is None:
         out = x.new_empty(shape)
-    xv = _view(x, "x", shape, dtype, dev)
-    gv = _view(gate, "gate", shape, dtype, dev)
-    rv = _view(residual, "residual", shape, dtype, dev)
-    ov = _view(out, "out", shape, dtype, dev, output=True)
+    views = _Views(shape, dtype, dev)
+    views.add(x, "x")
+    views.add(gate, "gate")
+    views.add(residual, "residual")
+    views.add(out, "out", True)
+    xv, gv, rv, ov = views.addresses()
     _need(weight, "weight", (D,), torch.float32, dev)
     with _device(dev):
-        _check(lib().la_gated_norm(_ref(xv), _ref(gv), _ptr(weight), _ref(rv), _ref(ov), *n, D, int(kind), int(activation),
-                                   float(eps), float(scale), code, _raw_stream(stream, dev)))
+        _check(lib().la_gated_norm(xv, gv, _ptr(weight), rv, ov, *n, D, kind, activation, eps, scale, code,
+                                   _raw_stream(stream, dev)))
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace_size(n, D):
+    return int(lib().la_gated_norm_backward_workspace_size(*n, D))
 
 
 def gated_norm_backward(dout, x, gate=None, weight=None, kind=NORM_RMS, activation=GATE_SILU, eps=1e-5, scale=1.0,
@@ -90,8 +117,8 @@ def gated_norm_backward(dout, x, gate=None, weight=None, kind=NORM_RMS, activati
     need_weight=False.  The residual's gradient is dout itself.  out: None,
     or the tuple of outputs preallocated."""
     n = _rows(x)
-    dev, D = x.device, x.shape[-1]
-    code = _dtype_code(x.dtype)
+    dev, shape, dtype = x.device, x.shape, x.dtype
+    D, code = shape[-1], _dtype_code(dtype)
     if dout is None:
         raise ValueError("dout is required")
     if out is None:
@@ -102,23 +129,25 @@ def gated_norm_backward(dout, x, gate=None, weight=None, kind=NORM_RMS, activati
         dx, dgate, dweight = out
         if dx is None or (dgate is None) != (gate is None) or (dweight is not None and weight is None):
             raise ValueError("out: dx and, with a gate, dgate are always written; dweight needs a weight")
-    dv = _view(dout, "dout", x.shape, x.dtype, dev)
-    xv, gv = (_view(t, name, x.shape, x.dtype, dev) for t, name in ((x, "x"), (gate, "gate")))
-    dxv, dgv = (_view(t, name, x.shape, x.dtype, dev, output=True) for t, name in ((dx, "dx"), (dgate, "dgate")))
+    views = _Views(shape, dtype, dev)
+    views.add(dout, "dout")
+    views.add(x, "x")
+    views.add(gate, "gate")
+    views.add(dx, "dx", True)
+    views.add(dgate, "dgate", True)
+    dv, xv, gv, dxv, dgv = views.addresses()
     _need(weight, "weight", (D,), torch.float32, dev)
     _need(dweight, "dweight", (D,), torch.float32, dev)
     with _device(dev):
-        if dweight is not None and workspace is None:
-            nbytes = int(lib().la_gated_norm_backward_workspace_size(*n, D))
-            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        if workspace is not None:
+            if workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+                raise ValueError("workspace: expected a contiguous uint8 tensor on the inputs' device")
+        elif dweight is not None:
+            workspace = torch.empty(max(_norm_workspace_size(n, D), 1), dtype=torch.uint8, device=dev)
             if stream is not None:
                 workspace.record_stream(stream)
-        elif workspace is not None and (workspace.device != dev or workspace.dtype != torch.uint8
-                                        or not workspace.is_contiguous()):
-            raise ValueError("workspace: expected a contiguous uint8 tensor on the inputs' device")
         _check(lib().la_gated_norm_backward(
-            _ref(dv), _ref(xv), _ref(gv), _ptr(weight), _ref(dxv), _ref(dgv), _ptr(dweight), *n, D, int(kind),
-            int(activation), float(eps), float(scale), code, _ptr(workspace),
+            dv, xv, gv, _ptr(weight), dxv, dgv, _ptr(dweight), *n, D, kind, activation, eps, scale, code, _ptr(workspace),
             0 if workspace is None else workspace.numel(), _raw_stream(stream, dev)))
     return dx, dgate, dweight
 
@@ -171,12 +200,15 @@ def rotary(x, freq, positions=None, x2=None, start=0, layout=ROTARY_HALF, mscale
         out = x.new_empty(shape)
     if out2 is None and x2 is not None:
         out2 = x.new_empty(shape2)
-    xv, ov = _view(x, "x", shape, dtype, dev), _view(out, "out", shape, dtype, dev, output=True)
-    xv2, ov2 = _view(x2, "x2", shape2, dtype, dev), _view(out2, "out2", shape2, dtype, dev, output=True)
+    views = _Views(shape, dtype, dev)
+    views.add(x, "x")
+    views.add(x2, "x2", shape=shape2)
+    views.add(out, "out", True)
+    views.add(out2, "out2", True, shape2)
+    xv, xv2, ov, ov2 = views.addresses()
     with _device(dev):
-        _check(lib().la_rotary(_ref(xv), H, _ref(xv2), H2, _ref(ov), _ref(ov2), _ptr(freq), _ptr(positions), pstride,
-                               int(start), B, T, D, R, int(layout), float(mscale), int(bool(backward)), code,
-                               _raw_stream(stream, dev)))
+        _check(lib().la_rotary(xv, H, xv2, H2, ov, ov2, freq.data_ptr(), _ptr(positions), pstride, start, B, T, D, R, layout,
+                               mscale, 1 if backward else 0, code, _raw_stream(stream, dev)))
     return (out, out2) if x2 is not None else out
 
 

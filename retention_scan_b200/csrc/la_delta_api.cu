@@ -49,13 +49,16 @@ static bool make_map(CUtensorMap* map, const void* base, int width, long long ro
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool scan_maps(const Plan& p, const Args& a, const void* values, ScanMaps* m) {
+bool make_maps(Plan* p, const Args& a) {
+    p->err = device_error_word();
     const long long keys = static_cast<long long>(a.B) * a.Hk * (a.dtype == LA_F32 ? 3 : 1);
-    if (!make_map(&m->k, p.k.base, p.k.cols, p.k.rows, keys, p.k.row, 64, true)) return false;
-    if (!make_map(&m->q, p.q.base, p.q.cols, p.q.rows, keys, p.q.row, 64, true)) return false;
-    // fp32 values are read without a map; any valid one stands in
-    m->v = m->k;
-    return a.dtype == LA_F32 || make_map(&m->v, values, a.Dv, a.T, p.BH, a.Dv, 16, false);
+    Maps* m = &p->maps;
+    if (!make_map(&m->k, p->k.base, p->k.cols, p->k.rows, keys, p->k.row, 64, true)) return false;
+    if (!make_map(&m->q, p->q.base, p->q.cols, p->q.rows, keys, p->q.row, 64, true)) return false;
+    m->v = m->dy = m->k;  // fp32 values are read without a map; any valid one stands in
+    if (a.dtype == LA_F32) return true;
+    if (!make_map(&m->v, a.v, a.Dv, a.T, p->BH, a.Dv, 16, false)) return false;
+    return !a.dy || make_map(&m->dy, a.dy, a.Dv, a.T, p->BH, a.Dv, 16, false);
 }
 
 Plan make_plan(const Args& a, bool backward, void* workspace) {
@@ -221,7 +224,8 @@ la_status la_delta_forward_ws(const void* q, const void* k, const void* v, const
     a.init_state = init_state;
     a.out = out;
     a.final_state = final_state;
-    return delta::launch_forward(delta::make_plan(a, false, workspace), a, true) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+    delta::Plan p = delta::make_plan(a, false, workspace);
+    return delta::make_maps(&p, a) && delta::launch_forward(p, a, true) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 
 la_status la_delta_backward_ws(const void* q, const void* k, const void* v, const float* beta, const la_decay* decay,
@@ -270,7 +274,8 @@ la_status la_delta_backward_ws(const void* q, const void* k, const void* v, cons
     a.dbeta = dbeta;
     a.d_log_g = d_log_g;
     a.d_init_state = d_init_state;
-    const delta::Plan p = delta::make_plan(a, true, workspace);
+    delta::Plan p = delta::make_plan(a, true, workspace);
+    if (!delta::make_maps(&p, a)) return LA_ERR_CUDA;
     cudaError_t e = delta::launch_forward(p, a, false);
     if (e == cudaSuccess) e = delta::launch_backward(p, a);
     return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;

@@ -890,10 +890,8 @@ cudaError_t reverse_run(const Plan& p, const Args& a, RevArgs r) {
     using Tl = ScanTiles<DKP, NI, 2 * NM, NW, true, sizeof(TIn) == 2>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tl::smem);
     if (e != cudaSuccess) return e;
-    ScanMaps m;
-    if (!scan_maps(p, a, a.dy, &m)) return cudaErrorUnknown;
     r.vblocks = (a.Dv + 16 * NW - 1) / (16 * NW);
-    kern<<<static_cast<unsigned>(p.BH * r.vblocks), 32 * NW, Tl::smem, a.stream>>>(m.k, m.q, m.v, r);
+    kern<<<static_cast<unsigned>(p.BH * r.vblocks), 32 * NW, Tl::smem, a.stream>>>(p.maps.k, p.maps.q, p.maps.dy, r);
     return cudaGetLastError();
 }
 
@@ -903,10 +901,8 @@ cudaError_t pair_reverse_run(const Plan& p, const Args& a, RevArgs r) {
     using Tl = ScanTiles<DKP, NI, 2 * NM, NS, true, sizeof(TIn) == 2, 16 * RevSpace<DKP, NM>::words * NS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tl::smem);
     if (e != cudaSuccess) return e;
-    ScanMaps m;
-    if (!scan_maps(p, a, a.dy, &m)) return cudaErrorUnknown;
     r.vblocks = (a.Dv + 16 * NS - 1) / (16 * NS);
-    kern<<<static_cast<unsigned>(p.BH * r.vblocks), 64 * NS + 32, Tl::smem, a.stream>>>(m.k, m.q, m.v, r);
+    kern<<<static_cast<unsigned>(p.BH * r.vblocks), 64 * NS + 32, Tl::smem, a.stream>>>(p.maps.k, p.maps.q, p.maps.dy, r);
     return cudaGetLastError();
 }
 
@@ -915,7 +911,7 @@ cudaError_t backward_typed(const Plan& p, const Args& a) {
     RevArgs r{};
     r.dy = a.dy;
     r.records = p.records;
-    r.err = device_error_word();
+    r.err = p.err;
     r.planes_apart = a.B * a.Hk;
     r.d_final = a.d_final_state;
     r.d_init = a.d_init_state;
@@ -966,9 +962,7 @@ cudaError_t backward_typed(const Plan& p, const Args& a) {
     using Tl = GradTiles<DKP, NI, NM, sizeof(TIn) == 4>;
     static_assert(Tl::smem <= 227 * 1024, "the gradient kernel's tiles have to fit an SM");
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tl::smem)) != cudaSuccess) return e;
-    ScanMaps m;
-    if (!scan_maps(p, a, a.dy, &m)) return cudaErrorUnknown;
-    kern<<<static_cast<unsigned>(p.BH * p.n), Tl::kThreads, Tl::smem, a.stream>>>(m.v, g);
+    kern<<<static_cast<unsigned>(p.BH * p.n), Tl::kThreads, Tl::smem, a.stream>>>(p.maps.dy, g);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.dqh) {
         const long long inner = static_cast<long long>(a.T) * a.Dk, total = static_cast<long long>(a.B) * a.Hk * inner;

@@ -722,11 +722,9 @@ cudaError_t prep_run(const Plan& p, const Args& a) {
     constexpr int smem = PrepTiles<DKP, NI, NM, NP>::bytes;
     cudaError_t e = allow_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    ScanMaps m;
-    if (!scan_maps(p, a, a.v, &m)) return cudaErrorUnknown;
-    kern<<<static_cast<unsigned>(p.BH * p.n), kPrepThreads, smem, a.stream>>>(m.k, m.q, a.beta, a.log_g, a.decay_kind, a.scale,
+    kern<<<static_cast<unsigned>(p.BH * p.n), kPrepThreads, smem, a.stream>>>(p.maps.k, p.maps.q, a.beta, a.log_g, a.decay_kind, a.scale,
                                                                              a.H, a.Hk, a.B * a.Hk, a.T, p.n, p.records,
-                                                                             device_error_word());
+                                                                             p.err);
     return cudaGetLastError();
 }
 
@@ -736,11 +734,9 @@ cudaError_t scan_run(const Plan& p, const Args& a) {
     using Tl = ScanTiles<DKP, NI, kOut ? NM + NP : NM, NW, kOut, sizeof(TIn) == 2>;
     cudaError_t e = allow_smem(kern, Tl::smem);
     if (e != cudaSuccess) return e;
-    ScanMaps m;
-    if (!scan_maps(p, a, a.v, &m)) return cudaErrorUnknown;
     ScanArgs s = scan_args(p, a);
     s.vblocks = (a.Dv + 16 * NW - 1) / (16 * NW);
-    kern<<<static_cast<unsigned>(p.BH * s.vblocks), 32 * NW, Tl::smem, a.stream>>>(m.k, m.q, m.v, s);
+    kern<<<static_cast<unsigned>(p.BH * s.vblocks), 32 * NW, Tl::smem, a.stream>>>(p.maps.k, p.maps.q, p.maps.v, s);
     return cudaGetLastError();
 }
 
@@ -750,11 +746,9 @@ cudaError_t pair_scan_run(const Plan& p, const Args& a) {
     using Tl = ScanTiles<DKP, NI, kOut ? NM + NP : NM, NS, kOut, sizeof(TIn) == 2, 16 * PairSpace<DKP, NM>::words * NS>;
     cudaError_t e = allow_smem(kern, Tl::smem);
     if (e != cudaSuccess) return e;
-    ScanMaps m;
-    if (!scan_maps(p, a, a.v, &m)) return cudaErrorUnknown;
     ScanArgs s = scan_args(p, a);
     s.vblocks = (a.Dv + 16 * NS - 1) / (16 * NS);
-    kern<<<static_cast<unsigned>(p.BH * s.vblocks), 64 * NS + 32, Tl::smem, a.stream>>>(m.k, m.q, m.v, s);
+    kern<<<static_cast<unsigned>(p.BH * s.vblocks), 64 * NS + 32, Tl::smem, a.stream>>>(p.maps.k, p.maps.q, p.maps.v, s);
     return cudaGetLastError();
 }
 

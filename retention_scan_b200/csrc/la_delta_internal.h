@@ -35,8 +35,16 @@ struct Args {
     float* d_init_state;         // or null
 };
 
+// Tensor maps of the kernels' tiles: K and Q by 64 columns of 64 tokens (128-byte
+// swizzle), the value-side operands v and dy (bf16 only) by 16 columns.
+struct Maps {
+    CUtensorMap k, q, v, dy;
+};
+
 // Where the workspace's regions start; everything a launch needs beyond Args.
 struct Plan {
+    Maps maps;    // set by make_maps, once a call
+    int* err;     // the device error word
     long long BH;
     int n;        // chunks per sequence
     int DKP, DVP; // key width of the kernels, value width in whole 16-column slices
@@ -66,18 +74,13 @@ struct ScanArgs {
     int H, Hk, T, Dk, Dv, DVP, n, vblocks;
 };
 
-// Tensor maps of the scans' tiles: K and Q by 64 columns of 64 tokens (128-byte
-// swizzle), the value-side operand (v, dy; bf16 only) by 16 columns.
-struct ScanMaps {
-    CUtensorMap k, q, v;
-};
-bool scan_maps(const Plan& p, const Args& a, const void* values, ScanMaps* m);
+bool make_maps(Plan* p, const Args& a);
 
 inline ScanArgs scan_args(const Plan& p, const Args& a) {
     ScanArgs s{};
     s.v = a.v;
     s.records = p.records;
-    s.err = device_error_word();
+    s.err = p.err;
     s.planes_apart = a.B * a.Hk;
     s.init_state = a.init_state;
     s.out = a.out;

@@ -5,6 +5,7 @@ the library's kernels.
     S' = g_t S_{t-1}    e_t = v_t - S'^T k_t    S_t = S' + k_t (beta_t e_t)^T    y_t = q_scale S_t^T q_t
 """
 import ctypes
+import functools
 
 import torch
 
@@ -58,9 +59,15 @@ def _scratch(workspace, nbytes, dev, stream):
     return workspace
 
 
+@functools.lru_cache(maxsize=256)
+def _size(backward, *sizes):
+    L = lib()
+    return int((L.la_delta_backward_workspace_size if backward else L.la_delta_workspace_size)(*sizes))
+
+
 def delta_workspace_size(B, H, T, Dk, Dv, dtype=torch.bfloat16, key_heads=None):
     """Scratch bytes delta_forward needs (la_delta_workspace_size)."""
-    return int(lib().la_delta_workspace_size(B, H, key_heads or H, T, Dk, Dv, _dtype_code(dtype)))
+    return _size(False, B, H, key_heads or H, T, Dk, Dv, _dtype_code(dtype))
 
 
 def delta_forward(q, k, v, beta, decay_kind=DECAY_NONE, log_g=None, init_state=None, q_scale=1.0, out=None,
@@ -96,7 +103,7 @@ def delta_forward(q, k, v, beta, decay_kind=DECAY_NONE, log_g=None, init_state=N
 
 def delta_backward_workspace_size(B, H, T, Dk, Dv, dtype=torch.bfloat16, key_heads=None):
     """Scratch bytes delta_backward needs (la_delta_backward_workspace_size)."""
-    return int(lib().la_delta_backward_workspace_size(B, H, key_heads or H, T, Dk, Dv, _dtype_code(dtype)))
+    return _size(True, B, H, key_heads or H, T, Dk, Dv, _dtype_code(dtype))
 
 
 def delta_backward(q, k, v, beta, dy, decay_kind=DECAY_NONE, log_g=None, init_state=None, d_final_state=None,
@@ -120,7 +127,7 @@ def delta_backward(q, k, v, beta, dy, decay_kind=DECAY_NONE, log_g=None, init_st
     _need(init_state, "init_state", (B, H, Dk, Dv), torch.float32, dev)
     _need(d_final_state, "d_final_state", (B, H, Dk, Dv), torch.float32, dev)
     if out is None:
-        dq, dk, dv, dbeta = (torch.empty_like(x) for x in (q, k, v, beta))
+        dq, dk, dv, dbeta = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(beta)
         d_log_g = torch.empty_like(log_g) if decay_kind != DECAY_NONE and need_log_g else None
         d_init = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev) if need_init_state else None
     else:

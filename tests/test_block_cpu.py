@@ -92,7 +92,7 @@ def view(data=64, s0=96, s1=32, s2=16):
 
 
 def ref(v):
-    return ctypes.byref(v) if v is not None else None
+    return ctypes.addressof(v) if v is not None else None
 
 
 def norm(lib, **over):

@@ -522,13 +522,17 @@ __device__ __forceinline__ void release_fed(uint64_t* empty) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(empty);
 }
 
-// ---------------------------------------------------------------- two warps a slice
-// Where a warp per slice leaves tensor cores idle, two share one.  Warp `half`
-// has half of the key width of S^T in its accumulators and two of the chunk's
-// four 16-token blocks, {0, 3} or {1, 2}, which have the same share of the
-// triangular products.  What one needs of the other (split operands) passes
-// through shared memory in register order, a 16-byte access a lane.
-__device__ constexpr int pair_block(int half, int j) { return half ? 1 + j : 3 * j; }
+// ---------------------------------------------------------------- several warps a slice
+// Where a warp per slice leaves tensor cores idle, G = 2 or 4 share one.  Warp w has
+// 1 / G of the key width of S^T in its accumulators and 4 / G of the chunk's
+// 16-token blocks: {0, 3} or {1, 2} for two, which have the same share of the
+// triangular products, block w for four.  What one needs of the others (split
+// operands) passes through shared memory in register order, a 16-byte access a
+// lane.
+template <int G>
+__device__ __forceinline__ int own_block(int w, int j) {
+    return G == 4 ? w : w ? 1 + j : 3 * j;
+}
 
 // Planes [N][32 lanes] of an A operand.
 template <int N>
@@ -548,27 +552,35 @@ __device__ __forceinline__ void get_planes(const uint4* at, int lane, uint32_t (
     }
 }
 
-// The pair's barrier (64 threads).  It is reached by both warps or, once a wait
-// gave up, by neither: pair_agree() ends both.
-__device__ __forceinline__ void pair_sync(int slice) { asm volatile("bar.sync %0, 64;" ::"r"(1 + slice) : "memory"); }
-__device__ __forceinline__ bool pair_agree(int slice, bool ok) {
+// The group's barrier (32 G threads).  It is reached by all its warps or, once a
+// wait gave up, by none: group_agree() ends them together.
+template <int G>
+__device__ __forceinline__ void group_sync(int slice) {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + slice), "n"(32 * G) : "memory");
+}
+template <int G>
+__device__ __forceinline__ bool group_agree(int slice, bool ok) {
     uint32_t all;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %2, 0;\n\t"
-        "bar.red.and.pred q, %1, 64, p;\n\t"
+        "bar.red.and.pred q, %1, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}\n"
         : "=r"(all)
-        : "r"(1 + slice), "r"(ok ? 1u : 0u)
+        : "r"(1 + slice), "r"(ok ? 1u : 0u), "n"(32 * G)
         : "memory");
     return all != 0;
 }
 
-// Byte offset, within a K or Q tile's row band, of k-step d of the `half`th half
-// of the key width, from the lane's offset of k-step d of the first half.
-template <int DKP>
-__device__ __forceinline__ uint32_t half_step(uint32_t o, int half) {
-    return DKP == 128 ? o + 8192 * half : o ^ (half * DKP);  // DKP / 2 columns of 2 bytes, within the swizzle
+// Byte offset, within a K or Q tile's row band, of 16-column step d of warp x's part
+// of the key width (64-column panels, swizzled rows), from the lane's offsets of
+// the first panel's four steps.
+template <int DKP, int G>
+__device__ __forceinline__ uint32_t step_offset(const LaneOffsets& l, int x, int d) {
+    constexpr int kSteps = DKP / 16 / G;
+    if constexpr (kSteps == 4) return l.o[d] + 8192 * x;
+    if constexpr (kSteps == 2 && G == 4) return (l.o[d] ^ ((x & 1) << 6)) + 8192 * (x >> 1);
+    return l.o[d] ^ (x * kSteps << 5);
 }
 
 // One 16-token block in accumulator layout, from the warp's tile or (fp32) from global memory ...

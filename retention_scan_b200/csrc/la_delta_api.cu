@@ -15,16 +15,18 @@ bool supports(int Dk, int Dv, la_dtype dtype) {
 }
 
 // Blocks of the scans.  A block fills an SM's shared memory, so blocks beyond the
-// SMs run in another round.  Few slices (16 value columns of a (b, h)): two warps
-// each, one or two slices a block, one round.  Else a warp each: up to four have a
+// SMs run in another round.  Few slices (16 value columns of a (b, h)) take one round
+// with several warps each: four where a block has one slice (T777 D64 fp32, 16
+// slices: 33 us against 43 with two), two where it has two (four's exchange fills
+// shared memory's bandwidth: B1 H32 T65536 D128 2324 us against 2258).  Else a warp each: up to four have a
 // tensor core of their own, eight share them and take about 1.7 times as long;
 // the fewest rounds win, then the wider block.
 static void plan_scan(Plan* p) {
     const int slices = p->DVP / 16;
-    p->pair = true;
+    p->group = true;
     for (p->warps = 1; p->warps <= 2; ++p->warps)
         if (p->BH * ((slices + p->warps - 1) / p->warps) <= 148) return;
-    p->pair = false;
+    p->group = false;
     double least = 0;
     for (int w = 1; w <= 8; w *= 2) {
         if (w > 1 && w / 2 >= slices) break;

@@ -224,31 +224,31 @@ __global__ void __launch_bounds__(32 * NW) reverse_kernel(const __grid_constant_
     if (a.d_init) state_store<DKP>(S, a.d_init + static_cast<long long>(bh) * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane);
 }
 
-// The same with two warps a slice (la_delta.cuh).  dY is read by both; the
-// halves of dS, diag(beta) dU and diag(e^L) dR are exchanged.
-template <int DKP, int NM>
+// The same with G warps a slice (la_delta.cuh).  dY is read by all; the parts of
+// dS, and diag(beta) dU and diag(e^L) dR by token block, are exchanged.
+template <int DKP, int NM, int G>
 struct RevSpace {  // a slice's exchange, in 16-byte words
-    static constexpr int kHalf = DKP / 32;
-    static constexpr int s = 0;                        // [2][kHalf][NM][32]
-    static constexpr int u = s + 2 * kHalf * NM * 32;  // [2][2][NM][32]
-    static constexpr int w = u + 2 * 2 * NM * 32;
-    static constexpr int words = w + 2 * 2 * NM * 32;
+    static constexpr int kSteps = DKP / 16 / G, kBlocks = 4 / G;
+    static constexpr int s = 0;                       // [DKP / 16][NM][32]
+    static constexpr int u = s + DKP / 16 * NM * 32;  // [4][NM][32]
+    static constexpr int w = u + 4 * NM * 32;
+    static constexpr int words = w + 4 * NM * 32;
 };
 
-template <int DKP, int NI, int NM, int NS, typename TIn>
-__global__ void __launch_bounds__(64 * NS + 32) pair_reverse_kernel(const __grid_constant__ CUtensorMap mk,
-                                                               const __grid_constant__ CUtensorMap mq,
-                                                               const __grid_constant__ CUtensorMap my, RevArgs a) {
+template <int DKP, int NI, int NM, int G, int NS, typename TIn>
+__global__ void __launch_bounds__(32 * G * NS + 32) group_reverse_kernel(const __grid_constant__ CUtensorMap mk,
+                                                                         const __grid_constant__ CUtensorMap mq,
+                                                                         const __grid_constant__ CUtensorMap my, RevArgs a) {
     constexpr bool kF32 = sizeof(TIn) == 4;
-    using Ex = RevSpace<DKP, NM>;
+    using Ex = RevSpace<DKP, NM, G>;
     using Tl = ScanTiles<DKP, NI, 2 * NM, NS, true, !kF32, 16 * Ex::words * NS>;
-    constexpr int kS = Tl::stages, kHalf = Ex::kHalf;
+    constexpr int kS = Tl::stages, kSteps = Ex::kSteps, kBlocks = Ex::kBlocks, kCols = DKP / G;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     unsigned char* smem = smem_raw + (base - smem_addr(smem_raw));
     FedRing<kS>* fed = reinterpret_cast<FedRing<kS>*>(smem + kS * Tl::bytes);
     Ring<kS>* ring = &fed->ring;
-    const int tid = threadIdx.x, lane = tid & 31, slice = tid >> 6, half = (tid >> 5) & 1;
+    const int tid = threadIdx.x, lane = tid & 31, slice = tid / (32 * G), w = (tid >> 5) % G;
     uint4* ex = reinterpret_cast<uint4*>(smem + Tl::extra) + slice * Ex::words;
     const int bh = blockIdx.x / a.vblocks;
     const int vb = blockIdx.x % a.vblocks * 16 * NS, v0 = vb + 16 * slice;
@@ -266,10 +266,10 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_reverse_kernel(const __grid
     feed.bh = bh;
     feed.v0 = vb;
     feed.nv = nv;
-    feed.warps = 2 * nv;
+    feed.warps = G * nv;
     init_fed<Tl>(feed, fed);
     if (slice == NS) {
-        if (tid == 64 * NS) feed_ring<Tl>(feed, base, fed, a.n, a.n - 1, -1, a.err);
+        if (tid == 32 * G * NS) feed_ring<Tl>(feed, base, fed, a.n, a.n - 1, -1, a.err);
         return;
     }
     if (slice >= nv) return;
@@ -277,21 +277,20 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_reverse_kernel(const __grid
     const TIn* ysrc = static_cast<const TIn*>(a.dy) + static_cast<long long>(bh) * a.T * a.Dv;
     const int tq = (lane & 3) * 2;
     const LaneOffsets oc = swz_cols(lane), orow = swz_rows(lane);
-    const int d0 = half * (DKP / 2);
-    float S[DKP / 16][4];
-    state_load<DKP / 2>(S, a.d_final ? a.d_final + static_cast<long long>(bh) * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, v0, lane, d0);
-
-    uint32_t so[kHalf][NM][4];  // this half's planes for the chunk that comes
+    float S[kCols / 8][4];
+    state_load<kCols>(S, a.d_final ? a.d_final + static_cast<long long>(bh) * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, v0, lane,
+                      w * kCols);
+    uint32_t so[kSteps][NM][4];  // this part's planes for the chunk that comes
 #pragma unroll
-    for (int d = 0; d < kHalf; ++d) {
+    for (int d = 0; d < kSteps; ++d) {
         split_frag<NM>(S[2 * d], S[2 * d + 1], so[d]);
-        put_planes<NM>(ex + Ex::s + (half * kHalf + d) * NM * 32, lane, so[d]);
+        put_planes<NM>(ex + Ex::s + (w * kSteps + d) * NM * 32, lane, so[d]);
     }
 
     for (int i = 0; i < a.n; ++i) {
         const int stage = i % kS, c = a.n - 1 - i;
         const long long cid = static_cast<long long>(bh) * a.n + c;
-        if (!pair_agree(slice, wait_stage(ring, stage, i / kS, a.err))) return;
+        if (!group_agree<G>(slice, wait_stage(ring, stage, i / kS, a.err))) return;
         const uint32_t st = base + stage * Tl::bytes;
         const uint32_t kt = st + Tl::k, qt = st + Tl::q, et = st + Tl::rec, pt = et + NM * kSq;
         const float* gam = reinterpret_cast<const float*>(smem + stage * Tl::bytes + Tl::tok);
@@ -299,40 +298,40 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_reverse_kernel(const __grid
         const float* beta = gam + 2 * C;
 
 #pragma unroll
-        for (int d = 0; d < kHalf; ++d)
-            put_tiles<NM>(so[d], a.dSst + cid * NM * a.DVP * DKP, v0 / 16, DKP / 16, half * kHalf + d, lane);
+        for (int d = 0; d < kSteps; ++d)
+            put_tiles<NM>(so[d], a.dSst + cid * NM * a.DVP * DKP, v0 / 16, DKP / 16, w * kSteps + d, lane);
         // X = (K dS)^T for this warp's tokens, then dU = e^(L_C - L) X + (P^T dY)
-        float X[2][2][4] = {};
+        float X[kBlocks][2][4] = {};
 #pragma unroll
-        for (int o = 0; o < 2; ++o) {
-            const int hh = o ? 1 - half : half;
+        for (int o = 0; o < G; ++o) {
+            const int x = (w + o) % G;
 #pragma unroll
-            for (int d = 0; d < kHalf; ++d) {
+            for (int d = 0; d < kSteps; ++d) {
                 uint32_t s[NM][4];
                 if (o) {
-                    get_planes<NM>(ex + Ex::s + (hh * kHalf + d) * NM * 32, lane, s);
+                    get_planes<NM>(ex + Ex::s + (x * kSteps + d) * NM * 32, lane, s);
                 } else {
 #pragma unroll
                     for (int p = 0; p < NM; ++p)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) s[p][x] = so[d][p][x];
+                        for (int y = 0; y < 4; ++y) s[p][y] = so[d][p][y];
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < kBlocks; ++j)
 #pragma unroll
                     for (int p = 0; p < NI; ++p) {
                         uint32_t r[4];
-                        ldsm4(r, kt + p * Tl::kTile + 2048 * pair_block(half, j) + half_step<DKP>(oc.o[d], hh));
+                        ldsm4(r, kt + p * Tl::kTile + 2048 * own_block<G>(w, j) + step_offset<DKP, G>(oc, x, d));
                         mma_planes<NM, NM>(X[j][0], X[j][1], s, p, r);
                     }
             }
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) block_scale(X[j], rest, pair_block(half, j), tq);
+        for (int j = 0; j < kBlocks; ++j) block_scale(X[j], rest, own_block<G>(w, j), tq);
         // dY block by block: into dU of the tokens up to it, and with its factors into dS's update
         const float total = gam[C - 1];
 #pragma unroll
-        for (int d = 0; d < 2 * kHalf; ++d)
+        for (int d = 0; d < 2 * kSteps; ++d)
 #pragma unroll
             for (int x = 0; x < 4; ++x) S[d][x] *= total;
 #pragma unroll
@@ -345,8 +344,8 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_reverse_kernel(const __grid
             uint32_t x[NI][4], y[NM][4];
             split_frag<NI>(Y[0], Y[1], x);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int blk = pair_block(half, j);
+            for (int j = 0; j < kBlocks; ++j) {
+                const int blk = own_block<G>(w, j);
                 if (blk <= m) {
 #pragma unroll
                     for (int p = 0; p < NM; ++p) {
@@ -359,32 +358,33 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_reverse_kernel(const __grid
             block_scale(Y, gam, m, tq, a.scale);
             split_frag<NM>(Y[0], Y[1], y);
 #pragma unroll
-            for (int d = 0; d < kHalf; ++d)
+            for (int d = 0; d < kSteps; ++d)
 #pragma unroll
                 for (int p = 0; p < NI; ++p) {
                     uint32_t r[4];
-                    ldsm4t(r, qt + p * Tl::kTile + half_step<DKP>(orow.o[d], half) + 2048 * m);
+                    ldsm4t(r, qt + p * Tl::kTile + step_offset<DKP, G>(orow, w, d) + 2048 * m);
                     mma_planes<NM, NM>(S[2 * d], S[2 * d + 1], y, p, r);
                 }
         }
-        uint32_t uo[2][NM][4];
+        uint32_t uo[kBlocks][NM][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            block_scale(X[j], beta, pair_block(half, j), tq);
+        for (int j = 0; j < kBlocks; ++j) {
+            const int blk = own_block<G>(w, j);
+            block_scale(X[j], beta, blk, tq);
             split_frag<NM>(X[j][0], X[j][1], uo[j]);
-            put_planes<NM>(ex + Ex::u + (half * 2 + j) * NM * 32, lane, uo[j]);
+            put_planes<NM>(ex + Ex::u + blk * NM * 32, lane, uo[j]);
         }
-        pair_sync(slice);
+        group_sync<G>(slice);
         // dR = T^T diag(beta) dU for this warp's tokens
-        float R[2][2][4] = {};
+        float R[kBlocks][2][4] = {};
 #pragma unroll
-        for (int o = 0; o < 2; ++o)
+        for (int o = 0; o < G; ++o)
 #pragma unroll
-            for (int jm = 0; jm < 2; ++jm) {
-                const int hh = o ? 1 - half : half, m = pair_block(hh, jm);
+            for (int jm = 0; jm < kBlocks; ++jm) {
+                const int m = own_block<G>((w + o) % G, jm);
                 uint32_t u[NM][4];
                 if (o) {
-                    get_planes<NM>(ex + Ex::u + (hh * 2 + jm) * NM * 32, lane, u);
+                    get_planes<NM>(ex + Ex::u + m * NM * 32, lane, u);
                 } else {
 #pragma unroll
                     for (int p = 0; p < NM; ++p)
@@ -392,8 +392,8 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_reverse_kernel(const __grid
                         for (int x = 0; x < 4; ++x) u[p][x] = uo[jm][p][x];
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int blk = pair_block(half, j);
+                for (int j = 0; j < kBlocks; ++j) {
+                    const int blk = own_block<G>(w, j);
                     if (blk <= m) {
 #pragma unroll
                         for (int p = 0; p < NM; ++p) {
@@ -404,45 +404,52 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_reverse_kernel(const __grid
                     }
                 }
             }
-        uint32_t wo[2][NM][4], wp[2][NM][4];
+        uint32_t wo[kBlocks][NM][4], wp[4 - kBlocks][NM][4];
         TIn* out = static_cast<TIn*>(a.dv) + static_cast<long long>(bh) * a.T * a.Dv;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int blk = pair_block(half, j);
+        for (int j = 0; j < kBlocks; ++j) {
+            const int blk = own_block<G>(w, j);
             block_to_global(R[j], out, c * C + 16 * blk, a.T, a.Dv, v0, lane);
             split_frag<NM>(R[j][0], R[j][1], wo[j]);
             put_tiles<NM>(wo[j], a.dRst + cid * NM * a.DVP * C, v0 / 16, C / 16, blk, lane);
             block_scale(R[j], gam, blk, tq, -1.f);
             split_frag<NM>(R[j][0], R[j][1], wo[j]);
-            put_planes<NM>(ex + Ex::w + (half * 2 + j) * NM * 32, lane, wo[j]);
+            put_planes<NM>(ex + Ex::w + blk * NM * 32, lane, wo[j]);
         }
-        pair_sync(slice);
+        group_sync<G>(slice);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) get_planes<NM>(ex + Ex::w + ((1 - half) * 2 + j) * NM * 32, lane, wp[j]);
+        for (int o = 1; o < G; ++o)
 #pragma unroll
-        for (int d = 0; d < kHalf; ++d) {
+            for (int j = 0; j < kBlocks; ++j)
+                get_planes<NM>(ex + Ex::w + own_block<G>((w + o) % G, j) * NM * 32, lane, wp[(o - 1) * kBlocks + j]);
+#pragma unroll
+        for (int d = 0; d < kSteps; ++d) {
             float acc[2][4] = {};
+            const uint32_t at = kt + step_offset<DKP, G>(orow, w, d);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int o = 0; o < G; ++o)
 #pragma unroll
-                for (int p = 0; p < NI; ++p) {
-                    const uint32_t at = kt + p * Tl::kTile + half_step<DKP>(orow.o[d], half);
-                    uint32_t r[4];
-                    ldsm4t(r, at + 2048 * pair_block(half, j));
-                    mma_planes<NM, NM>(acc[0], acc[1], wo[j], p, r);
-                    ldsm4t(r, at + 2048 * pair_block(1 - half, j));
-                    mma_planes<NM, NM>(acc[0], acc[1], wp[j], p, r);
-                }
+                for (int j = 0; j < kBlocks; ++j)
+#pragma unroll
+                    for (int p = 0; p < NI; ++p) {
+                        uint32_t r[4];
+                        ldsm4t(r, at + p * Tl::kTile + 2048 * own_block<G>((w + o) % G, j));
+                        if (o)
+                            mma_planes<NM, NM>(acc[0], acc[1], wp[(o ? o - 1 : 0) * kBlocks + j], p, r);
+                        else
+                            mma_planes<NM, NM>(acc[0], acc[1], wo[j], p, r);
+                    }
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) S[2 * d + j][x] += acc[j][x];
             split_frag<NM>(S[2 * d], S[2 * d + 1], so[d]);
-            put_planes<NM>(ex + Ex::s + (half * kHalf + d) * NM * 32, lane, so[d]);
+            put_planes<NM>(ex + Ex::s + (w * kSteps + d) * NM * 32, lane, so[d]);
         }
         release_fed(&fed->empty[stage]);
     }
-    if (a.d_init) state_store<DKP / 2>(S, a.d_init + static_cast<long long>(bh) * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane, d0);
+    if (a.d_init)
+        state_store<kCols>(S, a.d_init + static_cast<long long>(bh) * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane, w * kCols);
 }
 
 // ---------------------------------------------------------------- gradients of a chunk
@@ -895,14 +902,14 @@ cudaError_t reverse_run(const Plan& p, const Args& a, RevArgs r) {
     return cudaGetLastError();
 }
 
-template <int DKP, int NI, int NM, int NS, typename TIn>
-cudaError_t pair_reverse_run(const Plan& p, const Args& a, RevArgs r) {
-    auto kern = pair_reverse_kernel<DKP, NI, NM, NS, TIn>;
-    using Tl = ScanTiles<DKP, NI, 2 * NM, NS, true, sizeof(TIn) == 2, 16 * RevSpace<DKP, NM>::words * NS>;
+template <int DKP, int NI, int NM, int G, int NS, typename TIn>
+cudaError_t group_reverse_run(const Plan& p, const Args& a, RevArgs r) {
+    auto kern = group_reverse_kernel<DKP, NI, NM, G, NS, TIn>;
+    using Tl = ScanTiles<DKP, NI, 2 * NM, NS, true, sizeof(TIn) == 2, 16 * RevSpace<DKP, NM, G>::words * NS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tl::smem);
     if (e != cudaSuccess) return e;
     r.vblocks = (a.Dv + 16 * NS - 1) / (16 * NS);
-    kern<<<static_cast<unsigned>(p.BH * r.vblocks), 64 * NS + 32, Tl::smem, a.stream>>>(p.maps.k, p.maps.q, p.maps.dy, r);
+    kern<<<static_cast<unsigned>(p.BH * r.vblocks), 32 * G * NS + 32, Tl::smem, a.stream>>>(p.maps.k, p.maps.q, p.maps.dy, r);
     return cudaGetLastError();
 }
 
@@ -926,7 +933,11 @@ cudaError_t backward_typed(const Plan& p, const Args& a) {
     r.Dv = a.Dv;
     r.DVP = p.DVP;
     r.n = p.n;
-    cudaError_t e = p.pair ? (p.warps == 1 ? pair_reverse_run<DKP, NI, NM, 1, TIn>(p, a, r) : pair_reverse_run<DKP, NI, NM, 2, TIn>(p, a, r))
+    // four warps a slice, two where the key width has two 16-column steps (at B2 H16 T4096 D128,
+    // two slices a block: four 163 us, two 169)
+    constexpr int G = DKP >= 64 ? 4 : 2;
+    cudaError_t e = p.group ? (p.warps == 1 ? group_reverse_run<DKP, NI, NM, G, 1, TIn>(p, a, r)
+                                            : group_reverse_run<DKP, NI, NM, G, 2, TIn>(p, a, r))
                     : p.warps == 1 ? reverse_run<DKP, NI, NM, 1, TIn>(p, a, r)
                     : p.warps == 2 ? reverse_run<DKP, NI, NM, 2, TIn>(p, a, r)
                     : p.warps == 4 ? reverse_run<DKP, NI, NM, 4, TIn>(p, a, r)

@@ -443,33 +443,35 @@ __global__ void __launch_bounds__(32 * NW) scan_kernel(const __grid_constant__ C
         state_store<DKP>(S, a.final_state + static_cast<long long>(bh) * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane);
 }
 
-// The same scan with two warps a slice (la_delta.cuh), for few (b, h): NS slices
-// a block.  Per chunk and pair three barriers: the state's halves, the
-// right-hand sides R, and U are exchanged.
-template <int DKP, int NM>
-struct PairSpace {  // a slice's exchange, in 16-byte words
-    static constexpr int kHalf = DKP / 32;           // k-steps of half the key width
-    static constexpr int s = 0;                      // [2][kHalf][NM][32]
-    static constexpr int r = s + 2 * kHalf * NM * 32;  // [2][2][NM][32]
-    static constexpr int u = r + 2 * 2 * NM * 32;
-    static constexpr int w = u + 2 * 2 * NM * 32;
-    static constexpr int words = w + 2 * 2 * NM * 32;
+// The same scan with G warps a slice (la_delta.cuh), for few (b, h): NS slices a
+// block and a warp that feeds the stages.  Per chunk and slice three barriers:
+// the state's parts, the right-hand sides R, and U are exchanged.  At B1 H32
+// T65536 D128 (256 slices): one warp a slice 3.3 us a chunk, two 2.2 us.
+template <int DKP, int NM, int G>
+struct GroupSpace {  // a slice's exchange, in 16-byte words
+    static constexpr int kSteps = DKP / 16 / G;       // k-steps of a warp's part of the key width
+    static constexpr int kBlocks = 4 / G;             // token blocks of a warp
+    static constexpr int s = 0;                       // [DKP / 16][NM][32]
+    static constexpr int r = s + DKP / 16 * NM * 32;  // [4][NM][32], by token block
+    static constexpr int u = r + 4 * NM * 32;
+    static constexpr int w = u + 4 * NM * 32;
+    static constexpr int words = w + 4 * NM * 32;
 };
 
-template <int DKP, int NI, int NM, int NP, int NS, bool kOut, typename TIn>
-__global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_constant__ CUtensorMap mk,
-                                                            const __grid_constant__ CUtensorMap mq,
-                                                            const __grid_constant__ CUtensorMap mv, ScanArgs a) {
+template <int DKP, int NI, int NM, int NP, int G, int NS, bool kOut, typename TIn>
+__global__ void __launch_bounds__(32 * G * NS + 32) group_scan_kernel(const __grid_constant__ CUtensorMap mk,
+                                                                      const __grid_constant__ CUtensorMap mq,
+                                                                      const __grid_constant__ CUtensorMap mv, ScanArgs a) {
     constexpr bool kF32 = sizeof(TIn) == 4;
-    using Ex = PairSpace<DKP, NM>;
+    using Ex = GroupSpace<DKP, NM, G>;
     using Tl = ScanTiles<DKP, NI, kOut ? NM + NP : NM, NS, kOut, !kF32, 16 * Ex::words * NS>;
-    constexpr int kS = Tl::stages, kHalf = Ex::kHalf;
+    constexpr int kS = Tl::stages, kSteps = Ex::kSteps, kBlocks = Ex::kBlocks, kCols = DKP / G;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     unsigned char* smem = smem_raw + (base - smem_addr(smem_raw));
     FedRing<kS>* fed = reinterpret_cast<FedRing<kS>*>(smem + kS * Tl::bytes);
     Ring<kS>* ring = &fed->ring;
-    const int tid = threadIdx.x, lane = tid & 31, slice = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 31, slice = tid / (32 * G);
     uint4* ex = reinterpret_cast<uint4*>(smem + Tl::extra) + slice * Ex::words;
     const int bh = blockIdx.x / a.vblocks;
     const int vb = blockIdx.x % a.vblocks * 16 * NS, v0 = vb + 16 * slice;
@@ -487,10 +489,10 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
     feed.bh = bh;
     feed.v0 = vb;
     feed.nv = nv;
-    feed.warps = 2 * nv;
+    feed.warps = G * nv;
     init_fed<Tl>(feed, fed);
     if (slice == NS) {
-        if (tid == 64 * NS) feed_ring<Tl>(feed, base, fed, a.n, 0, 1, a.err);
+        if (tid == 32 * G * NS) feed_ring<Tl>(feed, base, fed, a.n, 0, 1, a.err);
         return;
     }
     if (slice >= nv) return;
@@ -498,25 +500,24 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
     const TIn* vsrc = static_cast<const TIn*>(a.v) + static_cast<long long>(bh) * a.T * a.Dv;
     const int tq = (lane & 3) * 2;
     const LaneOffsets oc = swz_cols(lane), orow = swz_rows(lane);
-    // one body for each half: every block index below is a constant
+    // two warps a slice: a body for each, whose block indices are constants (2258 us at the
+    // size above against 2530); four run one body (four would not fit the instruction cache)
     auto scan = [&](auto which) {
-    constexpr int half = decltype(which)::value;
-    constexpr int d0 = half * (DKP / 2);
-    float S[DKP / 16][4];
-    state_load<DKP / 2>(S, a.init_state ? a.init_state + static_cast<long long>(bh) * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, v0,
-                        lane, d0);
-
-    uint32_t so[kHalf][NM][4];  // this half's planes for the chunk that comes
+    const int w = which;
+    float S[kCols / 8][4];
+    state_load<kCols>(S, a.init_state ? a.init_state + static_cast<long long>(bh) * a.Dk * a.Dv : nullptr, a.Dk, a.Dv, v0, lane,
+                      w * kCols);
+    uint32_t so[kSteps][NM][4];  // this part's planes for the chunk that comes
 #pragma unroll
-    for (int d = 0; d < kHalf; ++d) {
+    for (int d = 0; d < kSteps; ++d) {
         split_frag<NM>(S[2 * d], S[2 * d + 1], so[d]);
-        put_planes<NM>(ex + Ex::s + (half * kHalf + d) * NM * 32, lane, so[d]);
+        put_planes<NM>(ex + Ex::s + (w * kSteps + d) * NM * 32, lane, so[d]);
     }
 
     for (int c = 0; c < a.n; ++c) {
         const int stage = c % kS;
         [[maybe_unused]] const long long cid = static_cast<long long>(bh) * a.n + c;
-        if (!pair_agree(slice, wait_stage(ring, stage, c / kS, a.err))) return;
+        if (!group_agree<G>(slice, wait_stage(ring, stage, c / kS, a.err))) return;
         const uint32_t st = base + stage * Tl::bytes;
         const uint32_t kt = st + Tl::k, et = st + Tl::rec;
         [[maybe_unused]] const uint32_t qt = st + Tl::q, pt = et + NM * kSq;
@@ -526,24 +527,25 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
 
         if constexpr (!kOut) {
 #pragma unroll
-            for (int d = 0; d < kHalf; ++d)
-                put_tiles<NM>(so[d], a.Sst + cid * NM * a.DVP * DKP, v0 / 16, DKP / 16, half * kHalf + d, lane);
+            for (int d = 0; d < kSteps; ++d)
+                put_tiles<NM>(so[d], a.Sst + cid * NM * a.DVP * DKP, v0 / 16, DKP / 16, w * kSteps + d, lane);
         }
-        [[maybe_unused]] float early[kF32 ? 2 : 1][2][4];  // fp32 values come straight from global memory: their latency passes under the products
+        [[maybe_unused]] float early[kF32 ? kBlocks : 1][2][4];  // fp32 values come from global memory: their latency passes under the products
         if constexpr (kF32) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) block_from_global(early[j], vsrc, c * C + 16 * pair_block(half, j), a.T, a.Dv, v0, lane);
+            for (int j = 0; j < kBlocks; ++j)
+                block_from_global(early[j], vsrc, c * C + 16 * own_block<G>(w, j), a.T, a.Dv, v0, lane);
         }
-        // (K S)^T or (Q S)^T for this warp's tokens: its own half of S, then the other's
-        auto through_state = [&](float (&acc)[2][2][4], uint32_t tile) {
+        // (K S)^T or (Q S)^T for this warp's tokens: its own part of S, then the others'
+        auto through_state = [&](float (&acc)[kBlocks][2][4], uint32_t tile) {
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                const int hh = o ? 1 - half : half;
+            for (int o = 0; o < G; ++o) {
+                const int x = (w + o) % G;
 #pragma unroll
-                for (int d = 0; d < kHalf; ++d) {
+                for (int d = 0; d < kSteps; ++d) {
                     uint32_t s[NM][4];
                     if (o) {
-                        get_planes<NM>(ex + Ex::s + (hh * kHalf + d) * NM * 32, lane, s);
+                        get_planes<NM>(ex + Ex::s + (x * kSteps + d) * NM * 32, lane, s);
                     } else {
 #pragma unroll
                         for (int p = 0; p < NM; ++p)
@@ -551,24 +553,56 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
                             for (int i = 0; i < 4; ++i) s[p][i] = so[d][p][i];
                     }
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                    for (int j = 0; j < kBlocks; ++j)
 #pragma unroll
                         for (int p = 0; p < NI; ++p) {
                             uint32_t r[4];
-                            ldsm4(r, tile + p * Tl::kTile + 2048 * pair_block(half, j) + half_step<DKP>(oc.o[d], hh));
+                            ldsm4(r, tile + p * Tl::kTile + 2048 * own_block<G>(w, j) + step_offset<DKP, G>(oc, x, d));
                             mma_planes<NM, NM>(acc[j][0], acc[j][1], s, p, r);
                         }
                 }
             }
         };
-        float X[2][2][4] = {};
-        [[maybe_unused]] float Y[2][2][4] = {};
+        // acc += (lower triangular matrix) x (exchanged blocks at and before each of this warp's)
+        auto through_blocks = [&](float (&acc)[kBlocks][2][4], uint32_t mat, int planes, const uint4* from,
+                                  const uint32_t (&mine)[kBlocks][NM][4]) {
+#pragma unroll
+            for (int o = 0; o < G; ++o)
+#pragma unroll
+                for (int jm = 0; jm < kBlocks; ++jm) {
+                    const int m = own_block<G>((w + o) % G, jm);
+                    uint32_t r[NM][4];
+                    if (o) {
+                        get_planes<NM>(from + m * NM * 32, lane, r);
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < NM; ++p)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) r[p][i] = mine[jm][p][i];
+                    }
+#pragma unroll
+                    for (int j = 0; j < kBlocks; ++j) {
+                        const int blk = own_block<G>(w, j);
+                        if (m <= blk) {
+#pragma unroll
+                            for (int p = 0; p < NM; ++p)
+                                if (p < planes) {
+                                    uint32_t e[4];
+                                    ldsm4(e, mat + p * kSq + 2048 * blk + (oc.o[0] ^ (m << 5)));
+                                    mma_planes<NM, NM>(acc[j][0], acc[j][1], r, p, e);
+                                }
+                        }
+                    }
+                }
+        };
+        float X[kBlocks][2][4] = {};
+        [[maybe_unused]] float Y[kBlocks][2][4] = {};
         through_state(X, kt);
         // R = V - e^L (K S), exchanged
-        uint32_t ro[2][NM][4];
+        uint32_t ro[kBlocks][NM][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int blk = pair_block(half, j);
+        for (int j = 0; j < kBlocks; ++j) {
+            const int blk = own_block<G>(w, j);
             float R[2][4];
             if constexpr (kF32) {
 #pragma unroll
@@ -587,44 +621,18 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
                     X[j][x][i] = 0.f;
                 }
             split_frag<NM>(R[0], R[1], ro[j]);
-            put_planes<NM>(ex + Ex::r + (half * 2 + j) * NM * 32, lane, ro[j]);
+            put_planes<NM>(ex + Ex::r + blk * NM * 32, lane, ro[j]);
         }
-        pair_sync(slice);
+        group_sync<G>(slice);
         // E for this warp's tokens: the blocks of (I + A diag(beta))^-1 R at and before each
-#pragma unroll
-        for (int o = 0; o < 2; ++o)
-#pragma unroll
-            for (int jm = 0; jm < 2; ++jm) {
-                const int hh = o ? 1 - half : half, m = pair_block(hh, jm);
-                uint32_t r[NM][4];
-                if (o) {
-                    get_planes<NM>(ex + Ex::r + (hh * 2 + jm) * NM * 32, lane, r);
-                } else {
-#pragma unroll
-                    for (int p = 0; p < NM; ++p)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) r[p][i] = ro[jm][p][i];
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int blk = pair_block(half, j);
-                    if (m <= blk) {
-#pragma unroll
-                        for (int p = 0; p < NM; ++p) {
-                            uint32_t e[4];
-                            ldsm4(e, et + p * kSq + 2048 * blk + oc.o[m]);
-                            mma_planes<NM, NM>(X[j][0], X[j][1], r, p, e);
-                        }
-                    }
-                }
-            }
+        through_blocks(X, et, NM, ex + Ex::r, ro);
         // Q S is not on the way to the next state: its products fill the waits around E and U
         if constexpr (kOut) through_state(Y, qt);
         // U = diag(beta) E, and diag(e^(L_C - L)) U for the state, exchanged
-        uint32_t uo[2][NM][4], wo[2][NM][4];
+        uint32_t uo[kBlocks][NM][4], wo[kBlocks][NM][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int blk = pair_block(half, j);
+        for (int j = 0; j < kBlocks; ++j) {
+            const int blk = own_block<G>(w, j);
             if constexpr (!kOut) {
                 split_frag<NM>(X[j][0], X[j][1], uo[j]);
                 put_tiles<NM>(uo[j], a.Est + cid * NM * a.DVP * C, v0 / 16, C / 16, blk, lane);
@@ -632,83 +640,68 @@ __global__ void __launch_bounds__(64 * NS + 32) pair_scan_kernel(const __grid_co
             block_scale(X[j], beta, blk, tq);
             if constexpr (kOut) {
                 split_frag<NM>(X[j][0], X[j][1], uo[j]);
-                put_planes<NM>(ex + Ex::u + (half * 2 + j) * NM * 32, lane, uo[j]);
+                put_planes<NM>(ex + Ex::u + blk * NM * 32, lane, uo[j]);
             }
             block_scale(X[j], rest, blk, tq);
             split_frag<NM>(X[j][0], X[j][1], wo[j]);
-            put_planes<NM>(ex + Ex::w + (half * 2 + j) * NM * 32, lane, wo[j]);
+            put_planes<NM>(ex + Ex::w + blk * NM * 32, lane, wo[j]);
         }
-        pair_sync(slice);
-        // This warp's half of S <- e^(L_C) S + K^T diag(e^(L_C - L)) U, and its planes
-        // for the next chunk (the partner read this chunk's before the last two barriers)
-        uint32_t wp[2][NM][4];
+        group_sync<G>(slice);
+        // This warp's part of S <- e^(L_C) S + K^T diag(e^(L_C - L)) U, and its planes for
+        // the next chunk (the others read this chunk's before the last barrier)
+        uint32_t wp[4 - kBlocks][NM][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) get_planes<NM>(ex + Ex::w + ((1 - half) * 2 + j) * NM * 32, lane, wp[j]);
+        for (int o = 1; o < G; ++o)
+#pragma unroll
+            for (int j = 0; j < kBlocks; ++j)
+                get_planes<NM>(ex + Ex::w + own_block<G>((w + o) % G, j) * NM * 32, lane, wp[(o - 1) * kBlocks + j]);
         const float total = gam[C - 1];
 #pragma unroll
-        for (int d = 0; d < kHalf; ++d) {
+        for (int d = 0; d < kSteps; ++d) {
             float acc[2][4] = {};
+            const uint32_t at = kt + step_offset<DKP, G>(orow, w, d);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int o = 0; o < G; ++o)
 #pragma unroll
-                for (int p = 0; p < NI; ++p) {
-                    const uint32_t at = kt + p * Tl::kTile + half_step<DKP>(orow.o[d], half);
-                    uint32_t r[4];
-                    ldsm4t(r, at + 2048 * pair_block(half, j));
-                    mma_planes<NM, NM>(acc[0], acc[1], wo[j], p, r);
-                    ldsm4t(r, at + 2048 * pair_block(1 - half, j));
-                    mma_planes<NM, NM>(acc[0], acc[1], wp[j], p, r);
-                }
+                for (int j = 0; j < kBlocks; ++j)
+#pragma unroll
+                    for (int p = 0; p < NI; ++p) {
+                        uint32_t r[4];
+                        ldsm4t(r, at + p * Tl::kTile + 2048 * own_block<G>((w + o) % G, j));
+                        if (o)
+                            mma_planes<NM, NM>(acc[0], acc[1], wp[(o ? o - 1 : 0) * kBlocks + j], p, r);
+                        else
+                            mma_planes<NM, NM>(acc[0], acc[1], wo[j], p, r);
+                    }
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) S[2 * d + j][i] = fmaf(total, S[2 * d + j][i], acc[j][i]);
             split_frag<NM>(S[2 * d], S[2 * d + 1], so[d]);
-            put_planes<NM>(ex + Ex::s + (half * kHalf + d) * NM * 32, lane, so[d]);
+            put_planes<NM>(ex + Ex::s + (w * kSteps + d) * NM * 32, lane, so[d]);
         }
         if constexpr (kOut) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) block_scale(Y[j], gam, pair_block(half, j), tq, a.scale);
-#pragma unroll
-            for (int o = 0; o < 2; ++o)
-#pragma unroll
-                for (int jm = 0; jm < 2; ++jm) {
-                    const int hh = o ? 1 - half : half, m = pair_block(hh, jm);
-                    uint32_t u[NM][4];
-                    if (o) {
-                        get_planes<NM>(ex + Ex::u + (hh * 2 + jm) * NM * 32, lane, u);
-                    } else {
-#pragma unroll
-                        for (int p = 0; p < NM; ++p)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) u[p][i] = uo[jm][p][i];
-                    }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int blk = pair_block(half, j);
-                        if (m <= blk) {
-#pragma unroll
-                            for (int p = 0; p < NP; ++p) {
-                                uint32_t r[4];
-                                ldsm4(r, pt + p * kSq + 2048 * blk + oc.o[m]);
-                                mma_planes<NM, NM>(Y[j][0], Y[j][1], u, p, r);
-                            }
-                        }
-                    }
-                }
+            for (int j = 0; j < kBlocks; ++j) block_scale(Y[j], gam, own_block<G>(w, j), tq, a.scale);
+            through_blocks(Y, pt, NP, ex + Ex::u, uo);
             TIn* out = static_cast<TIn*>(a.out) + static_cast<long long>(bh) * a.T * a.Dv;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) block_to_global(Y[j], out, c * C + 16 * pair_block(half, j), a.T, a.Dv, v0, lane);
+            for (int j = 0; j < kBlocks; ++j) block_to_global(Y[j], out, c * C + 16 * own_block<G>(w, j), a.T, a.Dv, v0, lane);
         }
         release_fed(&fed->empty[stage]);
     }
     if (a.final_state)
-        state_store<DKP / 2>(S, a.final_state + static_cast<long long>(bh) * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane, d0);
+        state_store<kCols>(S, a.final_state + static_cast<long long>(bh) * a.Dk * a.Dv, a.Dk, a.Dv, v0, lane, w * kCols);
     };
-    if ((tid >> 5) & 1)
-        scan(std::integral_constant<int, 1>{});
-    else
-        scan(std::integral_constant<int, 0>{});
+    const int w = (tid >> 5) % G;
+    if constexpr (G == 2) {
+        if (w)
+            scan(std::integral_constant<int, 1>{});
+        else
+            scan(std::integral_constant<int, 0>{});
+    } else {
+        scan(w);
+    }
 }
 
 template <typename K>
@@ -740,22 +733,23 @@ cudaError_t scan_run(const Plan& p, const Args& a) {
     return cudaGetLastError();
 }
 
-template <int DKP, int NI, int NM, int NP, int NS, bool kOut, typename TIn>
-cudaError_t pair_scan_run(const Plan& p, const Args& a) {
-    auto kern = pair_scan_kernel<DKP, NI, NM, NP, NS, kOut, TIn>;
-    using Tl = ScanTiles<DKP, NI, kOut ? NM + NP : NM, NS, kOut, sizeof(TIn) == 2, 16 * PairSpace<DKP, NM>::words * NS>;
+template <int DKP, int NI, int NM, int NP, int G, int NS, bool kOut, typename TIn>
+cudaError_t group_scan_run(const Plan& p, const Args& a) {
+    auto kern = group_scan_kernel<DKP, NI, NM, NP, G, NS, kOut, TIn>;
+    using Tl = ScanTiles<DKP, NI, kOut ? NM + NP : NM, NS, kOut, sizeof(TIn) == 2, 16 * GroupSpace<DKP, NM, G>::words * NS>;
     cudaError_t e = allow_smem(kern, Tl::smem);
     if (e != cudaSuccess) return e;
     ScanArgs s = scan_args(p, a);
     s.vblocks = (a.Dv + 16 * NS - 1) / (16 * NS);
-    kern<<<static_cast<unsigned>(p.BH * s.vblocks), 64 * NS + 32, Tl::smem, a.stream>>>(p.maps.k, p.maps.q, p.maps.v, s);
+    kern<<<static_cast<unsigned>(p.BH * s.vblocks), 32 * G * NS + 32, Tl::smem, a.stream>>>(p.maps.k, p.maps.q, p.maps.v, s);
     return cudaGetLastError();
 }
 
 template <int DKP, int NI, int NM, int NP, bool kOut, typename TIn>
 cudaError_t scan_widths(const Plan& p, const Args& a) {
-    if (p.pair)
-        return p.warps == 1 ? pair_scan_run<DKP, NI, NM, NP, 1, kOut, TIn>(p, a) : pair_scan_run<DKP, NI, NM, NP, 2, kOut, TIn>(p, a);
+    constexpr int G = DKP >= 64 ? 4 : 2;  // each warp needs a 16-column step of the key width
+    if (p.group)
+        return p.warps == 1 ? group_scan_run<DKP, NI, NM, NP, G, 1, kOut, TIn>(p, a) : group_scan_run<DKP, NI, NM, NP, 2, 2, kOut, TIn>(p, a);
     switch (p.warps) {
         case 1: return scan_run<DKP, NI, NM, NP, 1, kOut, TIn>(p, a);
         case 2: return scan_run<DKP, NI, NM, NP, 2, kOut, TIn>(p, a);

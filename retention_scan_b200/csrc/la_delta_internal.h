@@ -49,7 +49,7 @@ struct Plan {
     int n;        // chunks per sequence
     int DKP, DVP; // key width of the kernels, value width in whole 16-column slices
     int warps;    // 16-column slices per block of the scans
-    bool pair;    // two warps a slice
+    bool group;   // several warps a slice
     Planes q, k;
     unsigned char* records;     // [BH][n][record_bytes(planes of both matrices)]
     __nv_bfloat16 *qs, *ks;     // fp32 inputs' planes

@@ -29,7 +29,9 @@ namespace delta {
 namespace {
 
 // ---------------------------------------------------------------- reverse scan
-// Warp = 16 value columns, dS^T in its accumulators, as in the forward scan.
+// Warp = 16 value columns, dS^T in its accumulators, as in the forward scan; bound
+// as that by the tensor rate with eight warps an SM, by its chain with fewer (2.5 us
+// a chunk at B2 H16 T4096 D128, four warps a slice: 160 us).
 struct RevArgs {
     const void* dy;
     const unsigned char* records;
@@ -457,8 +459,11 @@ __global__ void __launch_bounds__(32 * G * NS + 32) group_reverse_kernel(const _
 // (w % 4, w / 4) holds rows 16 r .. of every product and column group c.  The
 // contraction over the value columns streams 16 of them at a time (S, dS, E, dR,
 // dY) through a ring of bulk copies; then the C x C gradients go through shared
-// memory as A operands of the products with K and Q.
-
+// memory as A operands of the products with K and Q.  At B2 H16 T4096 D128 (2048
+// chunks) 260 us: 15 000 of a block's 33 000 cycles in the slices, at 60-75% of
+// the tensor rate, the rest in its first loads and its epilogue, which overlap
+// nothing with one block an SM (16 warps hold all registers).  8 warps took 287 us;
+// blocks that run on into the next chunk, 278 us (the loop's registers spill).
 template <int DKP, int NI, int NM, bool kF32>
 struct GradTiles {
     static constexpr int kGroups = DKP >= 64 ? 4 : 2;         // column groups

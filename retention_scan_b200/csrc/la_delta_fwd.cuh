@@ -39,7 +39,7 @@ __global__ void split_kernel(const float* __restrict__ x, __nv_bfloat16* __restr
 // these steps with five blocks an SM.  A substitution of the whole 64 x 64 matrix
 // by one thread a column was bound by fetching its 2700 unrolled instructions for
 // two warps (766 us at B1 H32 T65536 D128); K and Q by cp.async spent 5000 of a
-// block's 17 800 cycles on addresses (531 us).
+// block's 17 800 cycles on addresses (531 us); now 350 us.
 constexpr int kPrepThreads = 128;
 constexpr int kBS = 24;                // row stride of a 16 x 16 bf16 block: ldmatrix without bank conflicts
 constexpr int kBlock = 16 * kBS;       // elements of such a block
@@ -266,6 +266,9 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
 // one's loads and splits fill another's waits.
 // kOut: 1 = outputs y, 0 = the backward's recomputation: the incoming state
 // and the errors E of every chunk, as bf16 planes.
+// Bound by the tensor core's rate for mma.sync: 484 instructions a warp and chunk
+// at D128 (bf16), 8 cycles each on a scheduler; with eight warps an SM a chunk
+// takes 9 000 cycles against 7 740 (B8 H16 T4096: 376 us).
 template <int DKP, int NI, int NM, int NP, int NW, bool kOut, typename TIn>
 __global__ void __launch_bounds__(32 * NW) scan_kernel(const __grid_constant__ CUtensorMap mk,
                                                              const __grid_constant__ CUtensorMap mq,

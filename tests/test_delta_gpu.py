@@ -461,3 +461,43 @@ def test_refusals_on_the_gpu():
     ]:
         with pytest.raises(error):
             bad()
+
+
+def test_systems_far_from_the_identity():
+    # I + A diag(beta) for one key repeated: row sums up to 64 beta.  A solution's error is bounded by the
+    # condition number times the operands' rounding: ||I + N|| <= 1 + 63 beta, and the inverse's columns are
+    # beta (1 - beta)^n: ||inverse|| <= 1 + beta (beta = 1), 1 + 1.9 / (1 - 0.9) = 20 (beta = 1.9, sign of the
+    # key alternating or not).  Four split operands in a row, as in BAR_STATE.
+    for beta_value, sign, inverse in ((1.0, 1, 2.0), (1.9, 1, 20.0), (1.9, -1, 20.0)):
+        for dtype, unit in ((torch.bfloat16, BAR_STATE), (torch.float32, BAR32)):
+            q, k, v, beta, lg, S0 = make(1, 2, 2, 300, 64, 64, dtype, kind=0, seed=12)
+            k = k[:, :, :1].expand_as(k).contiguous()
+            k[:, :, ::2] *= sign
+            beta[:] = beta_value
+            y, S = la().delta_forward(*dev(q, k, v, beta), 0, None, *dev(S0))
+            ry, rS = oracle.delta_forward(q, k, v, beta, 0, None, S0)
+            assert slice_err(S, rS) <= (1 + 63 * beta_value) * inverse * unit
+            assert slice_err(y, ry) <= (1 + 63 * beta_value) * inverse * unit + (BAR16 if dtype == torch.bfloat16 else 0)
+
+
+def test_the_first_call_of_a_process_inside_a_capture():
+    import subprocess
+    import sys
+    code = r'''
+import torch, retention_scan_b200 as la
+q = torch.nn.functional.normalize(torch.randn(1, 2, 100, 64, device="cuda"), dim=-1).bfloat16()
+beta, out, fin = torch.rand(1, 2, 100, device="cuda"), torch.empty_like(q), torch.empty(1, 2, 64, 64, device="cuda")
+ws = torch.empty(la.delta_workspace_size(1, 2, 100, 64, 64), dtype=torch.uint8, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    la.delta_forward(q, q, q, beta, out=out, final_state=fin, workspace=ws)
+g.replay()
+y, S = la.delta_forward(q, q, q, beta)
+torch.cuda.synchronize()
+assert torch.equal(out, y) and torch.equal(fin, S) and la.device_error() == 0
+print("same")
+'''
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root, timeout=120)
+    assert r.stdout.strip().endswith("same"), r.stderr[-2000:]

@@ -181,9 +181,26 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(Args a) {
     }
 }
 
+// Rows on their way to a thread: where its accesses are 16 bytes, cp.async into
+// slots of its own (no register holds a row in flight, and no barrier is needed);
+// else none, the row is loaded when its turn comes.
+template <typename T, int V, int NV>
+struct Ahead {
+    static constexpr bool on = V * sizeof(T) == 16;
+    static constexpr int slots = !on ? 0 : NV <= 2 ? 3 : 2;
+    static constexpr int bytes = slots * 3 * NV * kThreads * 16;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <typename T, int V, int G, int NV>
 __global__ void __launch_bounds__(kThreads, NV * V > 16 ? 1 : 2) backward_kernel(Args a) {
-    extern __shared__ __align__(16) float shared[];  // 32 floats, scale * weight, a partial dw row per team
+    using Ring = Ahead<T, V, NV>;
+    // rows ahead (later a partial dw row per team), 32 floats, scale * weight
+    extern __shared__ __align__(16) unsigned char ring[];
+    float* shared = reinterpret_cast<float*>(ring + a.ahead);
     float* red = shared;
     float* ws = shared + 32;
     const int lane = threadIdx.x % G, team = threadIdx.x / G;
@@ -202,64 +219,102 @@ __global__ void __launch_bounds__(kThreads, NV * V > 16 ? 1 : 2) backward_kernel
     // the same number of rounds.
     const unsigned teams = gridDim.x * kTeams, run = static_cast<unsigned>((a.rows + teams - 1) / teams);
     const long long row0 = static_cast<long long>(blockIdx.x * kTeams + team) * run;
-    unsigned i0, i1, i2;
-    const T *xp, *mp, *zp;
-    T *op, *gp;  // of the row before, whose results are still to come
-    auto place = [&](long long row) {
-        i0 = a.n1.divmod(a.n2.divmod(static_cast<unsigned>(row < a.rows ? row : a.rows - 1), i2), i1);
-        xp = static_cast<const T*>(a.x.data) + at(a.x, i0, i1, i2);
-        mp = static_cast<const T*>(a.dout.data) + at(a.dout, i0, i1, i2);
-        op = static_cast<T*>(a.dx.data) + at(a.dx, i0, i1, i2);
-        if (gated) {
-            zp = static_cast<const T*>(a.gate.data) + at(a.gate, i0, i1, i2);
-            gp = static_cast<T*>(a.dgate.data) + at(a.dgate, i0, i1, i2);
+    struct {
+        unsigned i0, i1, i2;
+        const T *x, *m, *z;
+    } in;  // the next row to ask for
+    struct {
+        unsigned i0, i1, i2;
+        T *x, *z;
+    } to;  // the row worked on
+    auto place_in = [&](long long row) {
+        in.i0 = a.n1.divmod(a.n2.divmod(static_cast<unsigned>(row < a.rows ? row : a.rows - 1), in.i2), in.i1);
+        in.x = static_cast<const T*>(a.x.data) + at(a.x, in.i0, in.i1, in.i2);
+        in.m = static_cast<const T*>(a.dout.data) + at(a.dout, in.i0, in.i1, in.i2);
+        in.z = static_cast<const T*>(a.gate.data) + (gated ? at(a.gate, in.i0, in.i1, in.i2) : 0);
+    };
+    auto place_to = [&](long long row) {
+        to.i0 = a.n1.divmod(a.n2.divmod(static_cast<unsigned>(row < a.rows ? row : a.rows - 1), to.i2), to.i1);
+        to.x = static_cast<T*>(a.dx.data) + at(a.dx, to.i0, to.i1, to.i2);
+        to.z = static_cast<T*>(a.dgate.data) + (gated ? at(a.dgate, to.i0, to.i1, to.i2) : 0);
+    };
+    const uint32_t mine16 = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16 * threadIdx.x;
+    auto slot = [&](unsigned k, int tensor, int u) {
+        return ((k % (Ring::on ? Ring::slots : 1)) * 3 + tensor) * NV * kThreads * 16 + u * kThreads * 16;
+    };
+    auto advance_in = [&](unsigned k) {  // from row k to the next
+        if (in.i2 + 1 < static_cast<unsigned>(a.n[2])) {
+            ++in.i2;
+            in.x += a.x.stride[2];
+            in.m += a.dout.stride[2];
+            in.z += a.gate.stride[2];
+        } else {
+            place_in(row0 + k + 1);
         }
     };
-    // The next row is on its way while this one is worked on.
-    Raw<T, V> xr[NV], mr[NV], zr[NV];
-    auto fetch = [&] {
+    auto ask = [&](unsigned k) {
+        if (k < run && row0 + k < a.rows) {
 #pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            const int c = (u * G + lane) * V;
-            if (c < a.D) {
-                xr[u].load(xp + c);
-                mr[u].load(mp + c);
-                if (gated) zr[u].load(zp + c);
+            for (int u = 0; u < NV; ++u) {
+                const int c = (u * G + lane) * V;
+                if (c < a.D) {
+                    copy16(mine16 + slot(k, 0, u), in.x + c);
+                    copy16(mine16 + slot(k, 1, u), in.m + c);
+                    if (gated) copy16(mine16 + slot(k, 2, u), in.z + c);
+                }
             }
+            advance_in(k);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    place(row0);
-    fetch();
+    place_in(row0);
+    place_to(row0);
+    if constexpr (Ring::on) {
+#pragma unroll
+        for (int k = 0; k < Ring::slots; ++k) ask(k);
+    }
     for (unsigned k = 0; k < run; ++k) {
         const bool live = row0 + k < a.rows;
         float x[NV][V], m[NV][V];
         Raw<T, V> z_raw[NV];
+        if constexpr (Ring::on) asm volatile("cp.async.wait_group %0;" ::"n"(Ring::slots - 1) : "memory");
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
-            if ((u * G + lane) * V < a.D) {
-                xr[u].unpack(x[u]);
-                mr[u].unpack(m[u]);
-                z_raw[u] = zr[u];
-            } else {
+            const int c = (u * G + lane) * V;
+            if (c < a.D && live) {
+                Raw<T, V> xr, mr;
+                if constexpr (Ring::on) {
+                    const unsigned char* at16 = ring + 16 * threadIdx.x;
+                    xr.load(reinterpret_cast<const T*>(at16 + slot(k, 0, u)));
+                    mr.load(reinterpret_cast<const T*>(at16 + slot(k, 1, u)));
+                    if (gated) z_raw[u].load(reinterpret_cast<const T*>(at16 + slot(k, 2, u)));
+                } else {
+                    xr.load(in.x + c);
+                    mr.load(in.m + c);
+                    if (gated) z_raw[u].load(in.z + c);
+                }
+                xr.unpack(x[u]);
+                mr.unpack(m[u]);
+            } else {  // behind the row, or a team behind the last row: zeros add nothing anywhere
+                z_raw[u] = {};
 #pragma unroll
                 for (int i = 0; i < V; ++i) x[u][i] = m[u][i] = 0.f;
             }
         }
-        T *dxp = op, *dgp = gp;
-        if (row0 + k + 1 < a.rows && k + 1 < run) {
-            if (i2 + 1 < static_cast<unsigned>(a.n[2])) {
-                ++i2;
-                xp += a.x.stride[2];
-                mp += a.dout.stride[2];
-                op += a.dx.stride[2];
-                zp += a.gate.stride[2];
-                gp += a.dgate.stride[2];
-            } else {
-                place(row0 + k + 1);
-            }
-            fetch();
+        if constexpr (Ring::on)
+            ask(k + Ring::slots);
+        else if (live)
+            advance_in(k);
+        T *dxp = to.x, *dgp = to.z;
+        if (to.i2 + 1 < static_cast<unsigned>(a.n[2])) {
+            ++to.i2;
+            to.x += a.dx.stride[2];
+            to.z += a.dgate.stride[2];
+        } else {
+            place_to(row0 + k + 1);
         }
-        const float r = normalise<V, G, NV>(x, a.D, a.inv, lane, a.kind, a.eps, red);
+        const float rn = normalise<V, G, NV>(x, a.D, a.inv, lane, a.kind, a.eps, red);
+        const float r = live ? rn : 0.f;  // eps = 0: infinite for the zeros of no row
         float inner = 0.f, sum = 0.f;
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
@@ -271,22 +326,31 @@ __global__ void __launch_bounds__(kThreads, NV * V > 16 ? 1 : 2) backward_kernel
                 if (gated) {
                     float z[V];
                     z_raw[u].unpack(z);
+                    if (silu) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float s = sigmoid(z[i]), act = silu ? z[i] * s : s, n = x[u][i] * r;
-                        const float t = m[u][i] * w[i];
-                        // silu' = s + z s (1 - s), sigmoid' = s (1 - s)
-                        dg[i] = t * n * fmaf(act, 1.f - s, silu ? s : 0.f);
-                        x[u][i] = n;
-                        dw[u][i] = fmaf(m[u][i] * act, live ? n : 0.f, dw[u][i]);
-                        m[u][i] = t * act;
+                        for (int i = 0; i < V; ++i) {
+                            const float s = sigmoid(z[i]), act = z[i] * s, n = x[u][i] * r, t = m[u][i] * w[i];
+                            dg[i] = t * n * fmaf(act, 1.f - s, s);  // silu' = s + z s (1 - s)
+                            x[u][i] = n;
+                            dw[u][i] = fmaf(m[u][i] * act, n, dw[u][i]);
+                            m[u][i] = t * act;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            const float s = sigmoid(z[i]), n = x[u][i] * r, t = m[u][i] * w[i], d = t * s;
+                            dg[i] = d * n * (1.f - s);  // sigmoid' = s (1 - s)
+                            x[u][i] = n;
+                            dw[u][i] = fmaf(m[u][i] * s, n, dw[u][i]);
+                            m[u][i] = d;
+                        }
                     }
                     if (live) store_row<T, V>(dgp + c, dg);
                 } else {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         x[u][i] *= r;
-                        dw[u][i] = fmaf(m[u][i], live ? x[u][i] : 0.f, dw[u][i]);
+                        dw[u][i] = fmaf(m[u][i], x[u][i], dw[u][i]);
                         m[u][i] *= w[i];
                     }
                 }
@@ -325,18 +389,19 @@ __global__ void __launch_bounds__(kThreads, NV * V > 16 ? 1 : 2) backward_kernel
                 for (int i = 0; i < V; ++i) part[c + i] = a.scale * dw[u][i];
         }
     } else {
-        float* mine = ws + (1 + team) * a.D;
+        __syncthreads();  // the rows ahead have all been used
+        float* rows = reinterpret_cast<float*>(ring);
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             const int c = (u * G + lane) * V;
             if (c < a.D)
 #pragma unroll
-                for (int i = 0; i < V; ++i) mine[c + i] = dw[u][i];
+                for (int i = 0; i < V; ++i) rows[team * a.D + c + i] = dw[u][i];
         }
         __syncthreads();
         for (int c = threadIdx.x; c < a.D; c += kThreads) {
             float s = 0.f;
-            for (int t = 0; t < kTeams; ++t) s += ws[(1 + t) * a.D + c];
+            for (int t = 0; t < kTeams; ++t) s += rows[t * a.D + c];
             part[c] = a.scale * s;
         }
     }
@@ -371,8 +436,16 @@ cudaError_t run(const Args& a, bool backward) {
         return cudaGetLastError();
     }
     const int blocks = team_blocks(a.rows, kTeams);
-    const size_t smem = sizeof(float) * (32 + static_cast<size_t>(kTeams > 1 && a.partial ? 1 + kTeams : 1) * a.D);
-    backward_kernel<T, V, G, NV><<<blocks, kThreads, smem, a.stream>>>(a);
+    // the rows ahead and, after them in the same place, the teams' partial rows; then 32 floats and the weight
+    const size_t teams = kTeams > 1 && a.partial ? sizeof(float) * static_cast<size_t>(kTeams) * a.D : 0;
+    const size_t rows_ahead = Ahead<T, V, NV>::bytes, ahead = teams <= rows_ahead ? rows_ahead : check::round256(teams);
+    const size_t smem = ahead + sizeof(float) * (32 + static_cast<size_t>(a.D));
+    Args b = a;
+    b.ahead = static_cast<int>(ahead);
+    cudaError_t s = cudaFuncSetAttribute(backward_kernel<T, V, G, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (s != cudaSuccess) return s;
+    backward_kernel<T, V, G, NV><<<blocks, kThreads, smem, a.stream>>>(b);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && a.partial) {
         weight_kernel<<<(a.D + 31) / 32, dim3(32, 32), 0, a.stream>>>(a.partial, a.dweight, blocks, a.D);

@@ -23,6 +23,7 @@ struct Args {
     const float* weight;          // [D] or null
     float* dweight;               // backward, or null
     float* partial;               // its workspace, or null
+    int ahead;                    // backward: bytes of shared memory before the reductions'
     int n[3];
     FastDiv n1, n2;               // division by n[1], n[2]
     long long rows;

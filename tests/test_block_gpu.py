@@ -204,6 +204,14 @@ def test_norm_extreme_values():
     assert torch.equal(y[rows], y0[rows]) and torch.isnan(y[6]).all() and torch.isnan(y[3, 5])
 
 
+@pytest.mark.parametrize("rows,D", [(1, 128), (5, 128), (3, 64), (9, 100), (2, 2048), (300, 36)])
+def test_teams_without_a_row_add_nothing(rows, D):
+    # eps = 0: what a team behind the last row computes must not reach dweight
+    x, gate, w, _, d = tensors((rows, D), torch.bfloat16, rows, "silu", True, False)
+    check_norm_backward(d, x, gate, w, "rms", "silu", eps=0.0)
+    check_norm_backward(d, x, None, w, "l2", "none", eps=0.0)
+
+
 def test_norm_empty():
     x = torch.empty(0, 5, 64, device="cuda")
     assert la().gated_norm(x).shape == (0, 5, 64)

@@ -672,7 +672,10 @@ LA_API la_status la_decode_step(const void* q, const void* k, const void* v,
  * inputs; final states are 2e-6 to 8e-6, 2-norm, from the rule in 64 bits for keys of
  * norm 1 and beta in (0, 1)) or 24 (fp32 inputs: about 1e-6).  A system far from
  * the identity amplifies that: one key repeated with beta = 1, 3e-5; repeated
- * with alternating sign and beta = 1.9, 4e-3 (fp32 inputs: 1e-5).
+ * with alternating sign and beta = 1.9, 4e-3 (fp32 inputs: 1e-5).  The gradients
+ * in fp32 are within 1e-5 of the rule's in 64 bits, 2-norm, for such keys; a
+ * decay per head of a single head can be further off (2e-5), its gradient being
+ * what is left of one long sum of terms of both signs.
  *
  * Inputs are finite (log g may be -infinity).  A NaN or an infinity spoils the
  * outputs of the whole 64-token chunk it lies in and everything after it, so fill
@@ -711,7 +714,10 @@ LA_API size_t la_delta_workspace_size(int B, int H, int Hk, int T, int Dk, int D
  *   d_init_state      NULL or [B,H,Dk,Dv] fp32.
  *   workspace         la_delta_backward_workspace_size(...) bytes: the
  *                     states and their gradients at every 64th token among them
- *                     (about 3.8 KB a token and head at Dk = Dv = 128, bf16).
+ *                     (about 3.8 KB a token and head at Dk = Dv = 128, bf16; half
+ *                     as much again where operands are kept in 24 bits rather than
+ *                     16: a decay per head, Dk <= 32 or B H T < 4096; a call
+ *                     smaller than another can so need more).
  *
  * Every output is written whole; no atomics, the same bits on every run.
  * T == 0 copies d_final_state (or 0) to d_init_state and writes zeros to a
@@ -724,8 +730,9 @@ LA_API la_status la_delta_backward_ws(const void* q, const void* k, const void* 
                                       int H, int Hk, int T, int Dk, int Dv, la_dtype dtype, void* workspace,
                                       size_t workspace_bytes, la_stream_t stream);
 
-/* Bytes la_delta_backward_ws needs. */
-LA_API size_t la_delta_backward_workspace_size(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype);
+/* Bytes la_delta_backward_ws needs, for an la_decay_kind. */
+LA_API size_t la_delta_backward_workspace_size(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype,
+                                               int decay_kind);
 
 /*
  * la_delta_decode_step - one token of the gated delta rule, `state` updated in

@@ -132,7 +132,7 @@ def lib():
         L.la_delta_backward_ws.argtypes = [vp, vp, vp, vp, ctypes.POINTER(_Decay), f, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                            i, i, i, i, i, i, i, vp, sz, vp]
         L.la_delta_backward_ws.restype = i
-        L.la_delta_backward_workspace_size.argtypes = [i, i, i, i, i, i, i]
+        L.la_delta_backward_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
         L.la_delta_backward_workspace_size.restype = sz
         L.la_delta_decode_step.argtypes = [vp, vp, vp, vp, ctypes.POINTER(_Decay), f, vp, vp, i, i, i, i, i, i, vp]
         L.la_delta_decode_step.restype = i

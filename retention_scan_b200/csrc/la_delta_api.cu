@@ -71,7 +71,7 @@ Plan make_plan(const Args& a, bool backward, void* workspace) {
     p.DVP = (a.Dv + 15) / 16 * 16;
     plan_scan(&p);
     const bool f32 = a.dtype == LA_F32;
-    const size_t nm = f32 ? 3 : 2, np = f32 ? 3 : backward ? 2 : 1, bf = sizeof(__nv_bfloat16);
+    const size_t nm = operand_planes(a, backward), np = f32 || backward ? nm : 1, bf = sizeof(__nv_bfloat16);
     const size_t chunks = static_cast<size_t>(p.BH) * p.n, keys = static_cast<size_t>(a.B) * a.Hk;
     size_t at = 0;
     auto region = [&](size_t bytes) {
@@ -171,9 +171,11 @@ delta::Args size_args(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtyp
     return a;
 }
 
-size_t workspace_bytes(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype, bool backward) {
+size_t workspace_bytes(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype, int decay_kind, bool backward) {
     if (check_sizes(B, H, Hk, T, Dk, Dv, dtype) != LA_OK || B == 0 || H == 0 || T == 0) return 0;
-    return delta::make_plan(size_args(B, H, Hk, T, Dk, Dv, dtype), backward, nullptr).bytes;
+    delta::Args a = size_args(B, H, Hk, T, Dk, Dv, dtype);
+    a.decay_kind = decay_kind;
+    return delta::make_plan(a, backward, nullptr).bytes;
 }
 
 cudaError_t copy_or_zero(float* dst, const float* src, size_t bytes, cudaStream_t s) {
@@ -186,11 +188,11 @@ cudaError_t copy_or_zero(float* dst, const float* src, size_t bytes, cudaStream_
 extern "C" {
 
 size_t la_delta_workspace_size(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype) {
-    return workspace_bytes(B, H, Hk, T, Dk, Dv, dtype, false);
+    return workspace_bytes(B, H, Hk, T, Dk, Dv, dtype, LA_DECAY_NONE, false);
 }
 
-size_t la_delta_backward_workspace_size(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype) {
-    return workspace_bytes(B, H, Hk, T, Dk, Dv, dtype, true);
+size_t la_delta_backward_workspace_size(int B, int H, int Hk, int T, int Dk, int Dv, la_dtype dtype, int decay_kind) {
+    return workspace_bytes(B, H, Hk, T, Dk, Dv, dtype, decay_kind, true);
 }
 
 la_status la_delta_forward_ws(const void* q, const void* k, const void* v, const float* beta, const la_decay* decay,
@@ -251,7 +253,7 @@ la_status la_delta_backward_ws(const void* q, const void* k, const void* v, cons
             if (!p || !aligned16(p)) return LA_ERR_INVALID_ARG;
         if (!beta || !aligned4(beta) || !dbeta || !aligned4(dbeta)) return LA_ERR_INVALID_ARG;
         if (!workspace || !aligned16(workspace) ||
-            workspace_bytes < la_delta_backward_workspace_size(B, H, Hk, T, Dk, Dv, dtype))
+            workspace_bytes < la_delta_backward_workspace_size(B, H, Hk, T, Dk, Dv, dtype, kind))
             return LA_ERR_INVALID_ARG;
     }
     if (H == 0 || (BH == 0 && !(d_log_g && kind == LA_DECAY_PER_HEAD))) return LA_OK;

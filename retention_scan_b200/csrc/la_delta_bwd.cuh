@@ -992,7 +992,10 @@ cudaError_t backward_typed(const Plan& p, const Args& a) {
 
 template <int DKP>
 cudaError_t backward_width(const Plan& p, const Args& a) {
-    return a.dtype == LA_F32 ? backward_typed<DKP, 3, 3, float>(p, a) : backward_typed<DKP, 1, 2, __nv_bfloat16>(p, a);
+    if (a.dtype == LA_F32) return backward_typed<DKP, 3, 3, float>(p, a);
+    if constexpr (DKP > kNarrowKeys)
+        if (operand_planes(a, true) == 2) return backward_typed<DKP, 1, 2, __nv_bfloat16>(p, a);
+    return backward_typed<DKP, 1, 3, __nv_bfloat16>(p, a);
 }
 
 }  // namespace

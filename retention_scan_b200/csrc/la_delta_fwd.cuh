@@ -783,8 +783,14 @@ cudaError_t forward_width(const Plan& p, const Args& a, bool outputs) {
         if ((e = prep_run<DKP, 1, 2, 1>(p, a)) != cudaSuccess) return e;
         return scan_widths<DKP, 1, 2, 1, true, __nv_bfloat16>(p, a);
     }
-    if ((e = prep_run<DKP, 1, 2, 2>(p, a)) != cudaSuccess) return e;
-    return scan_widths<DKP, 1, 2, 2, false, __nv_bfloat16>(p, a);
+    if constexpr (DKP > kNarrowKeys) {
+        if (operand_planes(a, true) == 2) {
+            if ((e = prep_run<DKP, 1, 2, 2>(p, a)) != cudaSuccess) return e;
+            return scan_widths<DKP, 1, 2, 2, false, __nv_bfloat16>(p, a);
+        }
+    }
+    if ((e = prep_run<DKP, 1, 3, 3>(p, a)) != cudaSuccess) return e;
+    return scan_widths<DKP, 1, 3, 3, false, __nv_bfloat16>(p, a);
 }
 
 }  // namespace

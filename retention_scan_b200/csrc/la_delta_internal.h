@@ -99,6 +99,26 @@ inline ScanArgs scan_args(const Plan& p, const Args& a) {
 }
 
 bool supports(int Dk, int Dv, la_dtype dtype);
+
+// bf16 planes of an fp32 operand.  Two keep 16 bits, enough for states and for
+// gradients of many values, whose errors average: 4e-6 of their norm, 7e-6 at worst.
+// fp32 inputs take three, and so do three kinds of bf16 backward whose fp32 outputs
+// (dbeta, the decay's gradient) two planes leave above 1e-5 of 64 bits:
+// - a decay per head, whose gradient sums over the whole sequence terms of both signs
+//   that leave a small rest (7.6e-5 with two planes, 8e-6 with three, and 2e-5 where
+//   the output is one head's only);
+// - few tokens times heads, where one cancelling value can be the norm (up to 5e-5
+//   below 64 of them, 9.2e-6 at 566);
+// - keys of at most 32 dimensions, which average little (8.8e-6 at 1206 of them).
+// Three planes take 1.3 to 1.45 times as long: 573 and 827 us at B2 H16 T4096 D128, 63
+// and 88 at B1 H8 T512 D128, 123 and 172 at B2 H8 T2048 Dk32 Dv64.
+constexpr int kNarrowKeys = 32;
+constexpr long long kFewTokens = 4096;
+inline int operand_planes(const Args& a, bool backward) {
+    if (a.dtype == LA_F32) return 3;
+    return backward && (a.decay_kind == LA_DECAY_PER_HEAD || a.Dk <= kNarrowKeys ||
+                        static_cast<long long>(a.B) * a.H * a.T < kFewTokens) ? 3 : 2;
+}
 // Regions from `workspace` on (null: sizes only).
 Plan make_plan(const Args& a, bool backward, void* workspace);
 

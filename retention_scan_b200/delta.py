@@ -101,9 +101,10 @@ def delta_forward(q, k, v, beta, decay_kind=DECAY_NONE, log_g=None, init_state=N
     return out, final_state
 
 
-def delta_backward_workspace_size(B, H, T, Dk, Dv, dtype=torch.bfloat16, key_heads=None):
-    """Scratch bytes delta_backward needs (la_delta_backward_workspace_size)."""
-    return _size(True, B, H, key_heads or H, T, Dk, Dv, _dtype_code(dtype))
+def delta_backward_workspace_size(B, H, T, Dk, Dv, dtype=torch.bfloat16, key_heads=None,
+                                  decay_kind=DECAY_PER_HEAD):
+    """Scratch bytes delta_backward needs (la_delta_backward_workspace_size): by default for any decay."""
+    return _size(True, B, H, key_heads or H, T, Dk, Dv, _dtype_code(dtype), decay_kind)
 
 
 def delta_backward(q, k, v, beta, dy, decay_kind=DECAY_NONE, log_g=None, init_state=None, d_final_state=None,
@@ -145,7 +146,8 @@ def delta_backward(q, k, v, beta, dy, decay_kind=DECAY_NONE, log_g=None, init_st
         _need(d_init, "d_init_state", (B, H, Dk, Dv), torch.float32, dev)
     d = _decay(decay_kind, log_g)
     with _device(dev):
-        workspace = _scratch(workspace, delta_backward_workspace_size(B, H, T, Dk, Dv, q.dtype, Hk), dev, stream)
+        workspace = _scratch(workspace, delta_backward_workspace_size(B, H, T, Dk, Dv, q.dtype, Hk, decay_kind),
+                             dev, stream)
         _check(lib().la_delta_backward_ws(
             _ptr(q), _ptr(k), _ptr(v), _ptr(beta), ctypes.byref(d) if d is not None else None, float(q_scale),
             _ptr(init_state), _ptr(dy), _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbeta), _ptr(d_log_g),

@@ -173,13 +173,18 @@ def test_nothing_to_do(L):  # noqa: F811
 
 def test_workspace_sizes(L):  # noqa: F811
     size = lambda *a: int(L.la_delta_workspace_size(*a))  # noqa: E731
-    back = lambda *a: int(L.la_delta_backward_workspace_size(*a))  # noqa: E731
+    back = lambda *a, kind=2: int(L.la_delta_backward_workspace_size(*a, kind))  # noqa: E731
     rec = 8192 * 3 + 5 * 64 * 4  # two planes of the inverse, one of the scores, the factors
     assert size(2, 4, 2, 65, 64, 64, 1) == -(-2 * 4 * 2 * rec // 256) * 256
     assert size(2, 4, 2, 0, 64, 64, 1) == size(0, 4, 2, 65, 64, 64, 1) == 0
     assert size(2, 4, 3, 65, 64, 64, 1) == 0 and size(2, 4, 2, 65, 40, 64, 1) == 0
     assert back(2, 4, 2, 65, 64, 64, 1) > size(2, 4, 2, 65, 64, 64, 1)
     assert back(2, 4, 2, 65, 64, 64, 1) > back(2, 4, 4, 65, 64, 64, 1)  # partial sums of shared heads
+    # a third plane: a decay per head, Dk <= 32, fewer than 4096 tokens times heads
+    assert back(2, 4, 2, 512, 64, 64, 1, kind=1) > back(2, 4, 2, 512, 64, 64, 1) == back(2, 4, 2, 512, 64, 64, 1, kind=0)
+    assert back(2, 4, 2, 511, 64, 64, 1, kind=1) == back(2, 4, 2, 511, 64, 64, 1) > back(2, 4, 2, 512, 64, 64, 1)
+    assert back(2, 4, 2, 512, 32, 64, 1, kind=1) == back(2, 4, 2, 512, 32, 64, 1)
+    assert back(2, 4, 2, 512, 64, 64, 0, kind=1) == back(2, 4, 2, 512, 64, 64, 0)
     assert size(1, 32, 32, 1 << 20, 128, 128, 1) == 32 * (1 << 14) * rec  # beyond 2^33: no 32-bit size
 
 

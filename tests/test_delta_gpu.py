@@ -263,6 +263,21 @@ def test_backward_without_states_and_with_correlated_keys():
     check_backward(make(2, 2, 2, 200, 64, 64, kind=1, init=False, seed=6), 1, d_final=False)
 
 
+@pytest.mark.parametrize("B,H,T,Dk,Dv", [(2, 2, 1057, 16, 32), (1, 2, 334, 128, 128), (3, 6, 200, 64, 48), (40, 8, 65, 32, 64)])
+def test_a_heads_decay_keeps_its_digits(B, H, T, Dk, Dv):
+    # a per-head decay's gradient is what is left of terms of both signs: with three planes an operand
+    # they are fp32 sums', 192 2^-24 of their absolute sum (twice: the scan and its reverse) and no more
+    args = make(B, H, H, T, Dk, Dv, kind=1, init=False, seed=T)
+    q, k, v, beta, lg, _ = args
+    dy = torch.randn(v.shape, generator=torch.Generator().manual_seed(5)).bfloat16()
+    got = la().delta_backward(*dev(q, k, v, beta, dy), 1, *dev(lg), q_scale=Dk ** -0.5)[4].cpu().double().numpy()
+    want = oracle.delta_backward(q, k, v, beta, dy, 1, lg, None, None, Dk ** -0.5)[4]
+    per_step = lg[None, :, None].expand(B, H, T)
+    terms = np.abs(oracle.delta_backward(q, k, v, beta, dy, 2, per_step, None, None, Dk ** -0.5)[4]).sum((0, 2))
+    assert (np.abs(got - want) <= 2 * BAR32 * terms).all()
+    assert np.linalg.norm(got - want) <= 1e-5 * np.linalg.norm(terms)
+
+
 def test_backward_of_zero_beta_and_hard_resets():
     # beta = 0 writes nothing, but its gradient is the error it would have written
     q, k, v, beta, lg, S0 = make(1, 2, 2, 150, 64, 64, seed=9)

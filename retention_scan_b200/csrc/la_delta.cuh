@@ -25,8 +25,8 @@
 // x = x0 + x1 (+ x2), each x_i the bf16 rounding of what is left, and a product
 // of operands with planes i and j is accumulated for i + j < NM: with NM = 2
 // a product is within about 2^-16 of fp32's, with NM = 3 within 2^-23.  bf16
-// inputs are exact in one plane and run with NM = 2; fp32 inputs take three
-// planes and NM = 3.  Plain bf16 or tf32 operands (2^-9, 2^-12) would leave
+// inputs are exact in one plane and run with NM = 2, or 3 where a gradient needs it
+// (operand_planes); fp32 inputs take three planes and NM = 3.  Plain bf16 or tf32 operands (2^-9, 2^-12) would leave
 // the fp32 state and the fp32 gradients with three digits.
 #pragma once
 #include <cuda_bf16.h>

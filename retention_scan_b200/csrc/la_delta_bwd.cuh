@@ -521,6 +521,7 @@ struct GradArgs {
     float* d_log_g;        // per step, or null
     double* dlog;          // per chunk (per-head decay), or null
     int* err;
+    int from_zero;         // no initial state: the first token's decay multiplies nothing
     int H, Hk, T, Dk, Dv, DVP, n;
 };
 
@@ -864,8 +865,8 @@ __global__ void __launch_bounds__(DKP >= 64 ? 512 : 256) grad_kernel(const __gri
             const double y = __shfl_down_sync(0xffffffffu, s, o);
             if (lane + o < 32) s += y;
         }
-        const double d0 = s + end, d1 = s - dl[0] + end;
         const int t = t0 + 2 * lane;
+        const double d0 = t == 0 && a.from_zero ? 0.0 : s + end, d1 = s - dl[0] + end;
         if (a.d_log_g) {
             if (t < a.T) a.d_log_g[bh * a.T + t] = static_cast<float>(d0);
             if (t + 1 < a.T) a.d_log_g[bh * a.T + t + 1] = static_cast<float>(d1);
@@ -966,6 +967,7 @@ cudaError_t backward_typed(const Plan& p, const Args& a) {
     g.dbeta = a.dbeta;
     g.d_log_g = a.decay_kind == LA_DECAY_PER_STEP ? a.d_log_g : nullptr;
     g.dlog = a.decay_kind == LA_DECAY_PER_HEAD && a.d_log_g ? p.dlog : nullptr;
+    g.from_zero = !a.init_state;
     g.H = a.H;
     g.Hk = a.Hk;
     g.T = a.T;

@@ -286,6 +286,18 @@ def test_backward_of_zero_beta_and_hard_resets():
     check_backward((q, k, v, beta, lg, S0), 2)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_first_decay_of_nothing_has_no_gradient(dtype):
+    # without an initial state the first token's decay multiplies zero: its gradient is 0, not a rounding
+    for T in (1, 66):
+        q, k, v, beta, lg, _ = make(2, 3, 3, T, 32, 48, dtype, init=False, seed=4)
+        dy = torch.randn(v.shape, generator=torch.Generator().manual_seed(6)).to(dtype)
+        d = la().delta_backward(*dev(q, k, v, beta, dy), 2, *dev(lg))[4]
+        assert (d[:, :, 0] == 0).all() and (T == 1 or (d[:, :, 1:] != 0).all())
+        d = la().delta_backward(*dev(q, k, v, beta, dy), 1, *dev(lg[0, :, 0]))[4]
+        assert (d == 0).all() == (T == 1)
+
+
 def test_backward_against_differences():
     # fp32, along a random direction of every input, by central differences of the library's forward
     q, k, v, beta, lg, S0 = make(1, 2, 1, 75, 24, 20, torch.float32, seed=21)

@@ -525,6 +525,23 @@ struct GradArgs {
     int H, Hk, T, Dk, Dv, DVP, n;
 };
 
+// A warp's rows 16 row .. of every product, its column group, and the 16 rows of
+// <S, dS> that it sums (none from DKP / 16 on).  Of 16 warps, the ten on or below
+// the diagonal also have a block of M and N: three of them on each of two
+// schedulers (warp % 4), two on the others, which take more of <S, dS> (row =
+// warp % 4 put four on one scheduler and one on another).
+struct GradPlace {
+    int row, col, inner;
+};
+template <int kGroups>
+__device__ __forceinline__ GradPlace grad_place(int warp) {
+    if constexpr (kGroups < 4) return {warp & 3, warp >> 2, warp};
+    // row | col << 2 of warps 0 .. 15: above the diagonal are warps 0, 1, 2, 3, 6 and 7
+    constexpr unsigned long long kPlaces = 0xFB73'A625'ED10'9C84ull;
+    const int at = static_cast<int>(kPlaces >> (4 * warp)) & 15;
+    return {at & 3, at >> 2, warp < 4 ? warp : warp < 12 && (warp & 2) ? 2 * (warp >> 2) + (warp & 1) + 2 : 16};
+}
+
 // Two neighbouring elements of a K or Q tile, its planes summed.
 template <int NI, int kRow>
 __device__ __forceinline__ float2 tile_pair(const __nv_bfloat16* tile, int t, int col) {
@@ -557,7 +574,8 @@ __global__ void __launch_bounds__(DKP >= 64 ? 512 : 256) grad_kernel(const __gri
     float* colsum = rowsum + 2 * kGroups * C;                             // [4 row groups][C]
     float* wsum = colsum + 4 * C;                               // per warp
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int wr = warp & 3, wc = warp >> 2;
+    const GradPlace place = grad_place<kGroups>(warp);
+    const int wr = place.row, wc = place.col;
     const int g = lane >> 2, tq = (lane & 3) * 2;
     const int bh = blockIdx.x / a.n;
     const int chunk = blockIdx.x % a.n, t0 = chunk * C;
@@ -645,14 +663,14 @@ __global__ void __launch_bounds__(DKP >= 64 ? 512 : 256) grad_kernel(const __gri
                 ldsm4t(r, at + Tl::ds);
                 mma_planes<NM, NM>(Z[2 * d], Z[2 * d + 1], ae, p, r);
             }
-        if (warp < DKP / 16) {
+        if (place.inner < DKP / 16) {
             uint32_t as[NM][4];
 #pragma unroll
-            for (int p = 0; p < NM; ++p) ldsm4(as[p], st + Tl::s + (p * (DKP / 16) + warp) * 512 + lo);
+            for (int p = 0; p < NM; ++p) ldsm4(as[p], st + Tl::s + (p * (DKP / 16) + place.inner) * 512 + lo);
 #pragma unroll
             for (int p = 0; p < NM; ++p) {
                 uint32_t r[4], x[4];
-                ldsm4(r, st + Tl::ds + (p * (DKP / 16) + warp) * 512 + lo);
+                ldsm4(r, st + Tl::ds + (p * (DKP / 16) + place.inner) * 512 + lo);
                 x[0] = r[0];
                 x[1] = r[2];
                 x[2] = r[1];

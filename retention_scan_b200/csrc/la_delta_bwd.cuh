@@ -460,10 +460,12 @@ __global__ void __launch_bounds__(32 * G * NS + 32) group_reverse_kernel(const _
 // contraction over the value columns streams 16 of them at a time (S, dS, E, dR,
 // dY) through a ring of bulk copies; then the C x C gradients go through shared
 // memory as A operands of the products with K and Q.  At B2 H16 T4096 D128 (2048
-// chunks) 260 us: 15 000 of a block's 33 000 cycles in the slices, at 60-75% of
-// the tensor rate, the rest in its first loads and its epilogue, which overlap
-// nothing with one block an SM (16 warps hold all registers).  8 warps took 287 us;
-// blocks that run on into the next chunk, 278 us (the loop's registers spill).
+// chunks) 255 us.  Of a block's 32 000 cycles 4 000 are its first loads, 16 000 the
+// slices (the tensor pipe's 11 000 and as many of shared memory's reads), 3 000 the
+// scores, 1 500 dP' and dA', 5 000 their products, 2 500 the outputs; nothing
+// overlaps between blocks with one an SM (16 warps hold all registers).  8 warps took
+// 287 us; blocks that run on into the next chunk, 278 (the loop's registers spill);
+// eight stages instead of three, 255; a warp each for the stages' first copies, 265.
 template <int DKP, int NI, int NM, bool kF32>
 struct GradTiles {
     static constexpr int kGroups = DKP >= 64 ? 4 : 2;         // column groups

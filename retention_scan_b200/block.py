@@ -88,7 +88,7 @@ def gated_norm(x, gate=None, weight=None, residual=None, kind=NORM_RMS, activati
     dev, shape, dtype = x.device, x.shape, x.dtype
     D, code = shape[-1], _dtype_code(dtype)
     if out is None:
-        out = x.new_empty(shape)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     views = _Views(shape, dtype, dev)
     views.add(x, "x")
     views.add(gate, "gate")
@@ -197,9 +197,9 @@ def rotary(x, freq, positions=None, x2=None, start=0, layout=ROTARY_HALF, mscale
         pstride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
     shape, shape2, dtype = (B, H, T, D), (B, H2, T, D), x.dtype
     if out is None:
-        out = x.new_empty(shape)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     if out2 is None and x2 is not None:
-        out2 = x.new_empty(shape2)
+        out2 = torch.empty_like(x2, memory_format=torch.contiguous_format)
     views = _Views(shape, dtype, dev)
     views.add(x, "x")
     views.add(x2, "x2", shape=shape2)

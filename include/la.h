@@ -670,7 +670,9 @@ LA_API la_status la_decode_step(const void* q, const void* k, const void* v,
  * Accuracy: states and sums are fp32.  Chunks of 64 tokens are solved as
  * triangular systems on tensor cores, whose operands carry 16 bits (bf16
  * inputs; final states are 2e-6 to 8e-6, 2-norm, from the rule in 64 bits for keys of
- * norm 1 and beta in (0, 1)) or 24 (fp32 inputs: about 1e-6).  A system far from
+ * norm 1 and beta in (0, 1)) or 24 (fp32 inputs: 1e-6 to 3e-6).  A bf16 y is as far
+ * off as its own rounding makes it (1.7e-3, 2-norm), also where keys and queries
+ * close to one another make the chunk's terms cancel.  A system far from
  * the identity amplifies that: one key repeated with beta = 1, 3e-5; repeated
  * with alternating sign and beta = 1.9, 4e-3 (fp32 inputs: 1e-5).  The gradients
  * in fp32 are within 1e-5 of the rule's in 64 bits, 2-norm, for such keys; a

@@ -55,6 +55,15 @@ constexpr float kLogFloor = -128.f;  // a decay below e^-128 is zero in fp32 nex
 // read, so that one bulk copy brings them into shared memory.
 constexpr long long record_bytes(int planes) { return static_cast<long long>(planes) * kSq + sizeof(float) * kTail; }
 
+// Both matrices are lower triangular, so their tiles' 16 x 16 blocks above the
+// diagonal are free.  The forward of bf16 inputs keeps one tile of P and the second
+// plane of P there (a third fewer bytes of P in the record and in a stage): its block
+// (i, k), k < i, at (k, i) of P's own tile, its diagonal blocks above the diagonal of
+// the first tile.  Byte offset of the block's 16-row band from the record's start,
+// and its column block.
+__host__ __device__ constexpr int fold_band(int nm, int i, int k) { return k < i ? nm * kSq + 2048 * k : i < 3 ? 0 : 2048; }
+__host__ __device__ constexpr int fold_col(int i, int k) { return k < i ? i : i < 3 ? i + 1 : 2; }
+
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
 // Byte offset of (row, col) of a 64-column bf16 tile whose 16-byte pieces are

@@ -64,12 +64,14 @@ struct PrepTiles {
     static constexpr int bytes = bar + 16 + 1024;                 // and the base's alignment
 };
 
+// NP: P's planes with a tile of their own, all NM of them or (NM = 2) one, the other folded.
 template <int DKP, int NI, int NM, int NP>
 __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constant__ CUtensorMap mk,
                                                             const __grid_constant__ CUtensorMap mq,
                                                             const float* __restrict__ beta, const float* __restrict__ log_g,
                                                             int decay_kind, float scale, int H, int Hk, int planes_apart,
                                                             int T, int n, unsigned char* __restrict__ records, int* err) {
+    static_assert(NP == NM || (NP == 1 && NM == 2), "one plane fits above the diagonals");
     using Tl = PrepTiles<DKP, NI, NM, NP>;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
@@ -169,10 +171,14 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
                     for (int i = 0; i < NM; ++i)
                         *reinterpret_cast<uint32_t*>(np + (i * 6 + low_block(warp, j / 2)) * kBlock + (t & 15) * kBS + (s & 15)) = m[i];
                 }
-                uint32_t p[NP];
-                split2<NP>(p0, p1, p);
+                uint32_t p[NM];
+                split2<NM>(p0, p1, p);
 #pragma unroll
                 for (int i = 0; i < NP; ++i) *reinterpret_cast<uint32_t*>(rec + (NM + i) * kSq + swz64(t, s)) = p[i];
+                if constexpr (NP < NM) {
+                    const int col = 16 * fold_col(warp, j / 2) + (s & 15);
+                    *reinterpret_cast<uint32_t*>(rec + fold_band(NM, warp, j / 2) + swz64(t & 15, col)) = p[NP];
+                }
             }
         }
     __syncwarp();
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
                     }
             }
     }
-    // Above the diagonal the record keeps what shared memory held: no scan reads there.
+    // Above the diagonal, where no plane is folded, the record keeps what shared memory held: no scan reads there.
     fence_async_smem();
     __syncthreads();
     constexpr long long kRec = record_bytes(NM + NP);
@@ -266,9 +272,9 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
 // one's loads and splits fill another's waits.
 // kOut: 1 = outputs y, 0 = the backward's recomputation: the incoming state
 // and the errors E of every chunk, as bf16 planes.
-// Bound by the tensor core's rate for mma.sync: 484 instructions a warp and chunk
-// at D128 (bf16), 8 cycles each on a scheduler; with eight warps an SM a chunk
-// takes 9 000 cycles against 7 740 (B8 H16 T4096: 376 us).
+// Bound by the tensor core's rate for mma.sync: 504 instructions a warp and chunk
+// at D128 (bf16), 8 cycles each on a scheduler, 8 060 cycles a chunk with eight warps
+// an SM (B8 H16 T4096: 376 us with P in one plane and 484 instructions, 392 with two).
 template <int DKP, int NI, int NM, int NP, int NW, bool kOut, typename TIn>
 __global__ void __launch_bounds__(32 * NW) scan_kernel(const __grid_constant__ CUtensorMap mk,
                                                              const __grid_constant__ CUtensorMap mq,
@@ -399,9 +405,9 @@ __global__ void __launch_bounds__(32 * NW) scan_kernel(const __grid_constant__ C
 #pragma unroll
                 for (int nn = m; nn < 4; ++nn)
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) {
+                    for (int p = 0; p < NM; ++p) {
                         uint32_t r[4];
-                        ldsm4(r, pt + p * kSq + 2048 * nn + oc.o[m]);
+                        ldsm4(r, p < NP ? pt + p * kSq + 2048 * nn + oc.o[m] : et + fold_band(NM, nn, m) + oc.o[fold_col(nn, m)]);
                         mma_planes<NM, NM>(Y[2 * nn], Y[2 * nn + 1], u, p, r);
                     }
             }
@@ -566,8 +572,9 @@ __global__ void __launch_bounds__(32 * G * NS + 32) group_scan_kernel(const __gr
                 }
             }
         };
-        // acc += (lower triangular matrix) x (exchanged blocks at and before each of this warp's)
-        auto through_blocks = [&](float (&acc)[kBlocks][2][4], uint32_t mat, int planes, const uint4* from,
+        // acc += (lower triangular matrix) x (exchanged blocks at and before each of this warp's);
+        // whole: its planes with a tile of their own
+        auto through_blocks = [&](float (&acc)[kBlocks][2][4], uint32_t mat, int whole, const uint4* from,
                                   const uint32_t (&mine)[kBlocks][NM][4]) {
 #pragma unroll
             for (int o = 0; o < G; ++o)
@@ -588,12 +595,12 @@ __global__ void __launch_bounds__(32 * G * NS + 32) group_scan_kernel(const __gr
                         const int blk = own_block<G>(w, j);
                         if (m <= blk) {
 #pragma unroll
-                            for (int p = 0; p < NM; ++p)
-                                if (p < planes) {
-                                    uint32_t e[4];
-                                    ldsm4(e, mat + p * kSq + 2048 * blk + (oc.o[0] ^ (m << 5)));
-                                    mma_planes<NM, NM>(acc[j][0], acc[j][1], r, p, e);
-                                }
+                            for (int p = 0; p < NM; ++p) {
+                                uint32_t e[4];
+                                ldsm4(e, p < whole ? mat + p * kSq + 2048 * blk + (oc.o[0] ^ (m << 5))
+                                                   : et + fold_band(NM, blk, m) + (oc.o[0] ^ (fold_col(blk, m) << 5)));
+                                mma_planes<NM, NM>(acc[j][0], acc[j][1], r, p, e);
+                            }
                         }
                     }
                 }
@@ -779,7 +786,8 @@ cudaError_t forward_width(const Plan& p, const Args& a, bool outputs) {
         return outputs ? scan_widths<DKP, 3, 3, 3, true, float>(p, a) : scan_widths<DKP, 3, 3, 3, false, float>(p, a);
     }
     if (outputs) {
-        // y is rounded to bf16: one plane of P adds 2^-9 of the chunk's own part to that
+        // P's second plane is folded.  Without it (P rounded to bf16) y was off by 2^-9 of each term of P U,
+        // which keys and queries close to one another make several times y: 0.007 to 0.013 of it
         if ((e = prep_run<DKP, 1, 2, 1>(p, a)) != cudaSuccess) return e;
         return scan_widths<DKP, 1, 2, 1, true, __nv_bfloat16>(p, a);
     }

@@ -528,3 +528,26 @@ print("same")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root, timeout=120)
     assert r.stdout.strip().endswith("same"), r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ keys and queries close to one another
+@pytest.mark.parametrize("B,H", [(1, 2), (5, 4), (10, 4)])  # four and two warps a slice, one
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 64), (32, 48)])
+@pytest.mark.parametrize("noise,beta_value", [(0.5, 0.99), (0.1, 1.0), (0.5, 0.5)])
+def test_outputs_of_scores_that_cancel(B, H, Dk, Dv, noise, beta_value):
+    # Keys and queries around one direction: the chunk's scores are all about 1 and the errors they meet are
+    # differences, so that P U is what is left of terms several times as large.  y has its own rounding, half a
+    # step (2^-8 of each value), and the split operands' 2^-14 of those terms, at most 16 times y here (64 tokens,
+    # whose errors fall off with beta): 2^-8 + 2^-10.  P rounded to bf16 (2^-9 of a term) would not hold it.
+    g = torch.Generator().manual_seed(B + Dk)
+    rn = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True)  # noqa: E731
+    T = 150
+    c = unit(rn(B, H, 1, Dk)) * Dk ** 0.5
+    k, q = (unit(c + noise * rn(B, H, T, Dk)).bfloat16() for _ in range(2))
+    v = rn(B, H, T, Dv).bfloat16()
+    beta, lg = torch.full((B, H, T), beta_value), torch.full((B, H, T), -0.01)
+    y, S = la().delta_forward(*dev(q, k, v, beta), 2, *dev(lg))
+    ry, rS = oracle.delta_forward(q, k, v, beta, 2, lg)
+    assert slice_err(y, ry) <= 2.0 ** -8 + 2.0 ** -10
+    assert slice_err(S, rS) <= BAR_STATE

@@ -551,3 +551,26 @@ def test_outputs_of_scores_that_cancel(B, H, Dk, Dv, noise, beta_value):
     ry, rS = oracle.delta_forward(q, k, v, beta, 2, lg)
     assert slice_err(y, ry) <= 2.0 ** -8 + 2.0 ** -10
     assert slice_err(S, rS) <= BAR_STATE
+
+
+@pytest.mark.parametrize("dtype,unit", [(torch.float32, BAR32), (torch.bfloat16, BAR_STATE)])
+@pytest.mark.parametrize("Dk,Dv", [(128, 32), (64, 16), (32, 16)])  # four and two warps a slice
+def test_long_gradients_of_states_do_not_drift(Dk, Dv, dtype, unit):
+    # No decay and small beta: the state's gradient is carried over 64 chunks.  Each chunk adds to it with two
+    # rounded operations, at most half a step of 2^-23 each, and 128 half steps in all; products and operands
+    # within a chunk as in BAR32 and BAR_STATE, for what that chunk adds.  All values positive, so that nothing cancels and a
+    # one-sided error shows.  Its mean has a tenth of that bound from the roundings, which go either way, and from
+    # the tensor core's truncations at most 24 additions (4 blocks, 6 pairs of planes) of 2^-24 each in a chunk's
+    # own products; into the carried gradient they would make 64 times as many.
+    q, k, v, beta, _, S0 = make(1, 2, 2, 4096, Dk, Dv, dtype, kind=0, seed=13)
+    g = torch.Generator().manual_seed(14)
+    beta, q, dy = 0.02 * beta, q.abs(), torch.randn(v.shape, generator=g).abs().to(dtype)
+    dS = 10 * torch.randn(1, 2, Dk, Dv, generator=g).abs()
+    got = la().delta_backward(*dev(q, k, v, beta, dy), 0, None, *dev(S0, dS))
+    want = oracle.delta_backward(q, k, v, beta, dy, 0, None, S0, dS)
+    bar = 128 * 2.0 ** -24
+    assert slice_err(got[5], want[5]) <= bar + unit / 8
+    bias = (got[5].cpu().double().numpy() - want[5]).mean() / np.abs(want[5]).mean()
+    assert abs(bias) <= bar / 10 + 24 * 2.0 ** -24
+    for x, r in zip(got[:3], want[:3]):
+        assert slice_err(x, r) <= bar + unit + (2.0 ** -8 if dtype == torch.bfloat16 else 0)

@@ -194,21 +194,67 @@ def _decay(kind, log_g):
 
 
 class _Here:
-    """Stands for the device context of the device that is current already."""
+    """The context of a call on the current device and its current stream, which has them already."""
 
     def __enter__(self):
-        return None
+        return _as_is
 
     def __exit__(self, *exc):
         return False
 
 
+class _There(torch.cuda.device):
+    """The context of a call on another device than the current one."""
+
+    def __enter__(self):
+        super().__enter__()
+        return _as_is
+
+
+class _On(torch.cuda.StreamContext):
+    """The context of a call with a stream of its own.  What the call allocates
+    comes from that stream's pool, in order with its kernels: memory of the
+    caller's current stream may still be in use by work queued there, and what
+    the caller drops at once would go back to it while the call still writes.
+    An output is recorded on the caller's stream too, where it is likely read,
+    and the caller's tensors on the call's, where they are."""
+
+    def __init__(self, stream, dev, used):
+        if stream.device != dev:
+            raise ValueError(f"stream: expected a stream of {dev}, got one of {stream.device}")
+        super().__init__(stream)
+        self.caller = torch.cuda.current_stream(dev)
+        if self.caller != stream:
+            for t in used:
+                if t is not None:
+                    t.record_stream(stream)
+
+    def __enter__(self):
+        super().__enter__()
+        return self.output
+
+    def output(self, t):
+        if self.caller != self.stream:
+            t.record_stream(self.caller)
+        return t
+
+
+def _as_is(t):
+    return t
+
+
 _here = _Here()
 
 
-def _device(dev):
-    """torch.cuda.device(dev), which costs a small call's launch again, only where it changes the device."""
-    return _here if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def _device(dev, stream=None, used=()):
+    """The context in which a call on `dev` and `stream` (None: the current one)
+    allocates and launches; it gives the function that every output it allocates
+    goes through.  used: the caller's tensors that the call reads or writes (or
+    None).  torch's own contexts, which cost a small call's launch again, only
+    where they change something."""
+    if stream is not None:
+        return _On(stream, dev, used)
+    return _here if dev.index == torch.cuda.current_device() else _There(dev)
 
 
 def _raw_stream(stream, dev):

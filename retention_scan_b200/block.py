@@ -6,6 +6,10 @@ in the library's kernels.
 Tensors are read and written through their strides (the last dimension dense),
 so projections laid out [B,T,H,D] and the scans' [B,H,T,D] need no copy
 between them: pass x.transpose(1, 2).
+
+stream (every call): None, the current one, or a stream that the caller has
+ordered behind the inputs; the call runs and allocates on it, and tensors may
+be dropped while it runs.
 """
 import array
 import functools
@@ -87,16 +91,16 @@ def gated_norm(x, gate=None, weight=None, residual=None, kind=NORM_RMS, activati
     n = _rows(x)
     dev, shape, dtype = x.device, x.shape, x.dtype
     D, code = shape[-1], _dtype_code(dtype)
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     views = _Views(shape, dtype, dev)
     views.add(x, "x")
     views.add(gate, "gate")
     views.add(residual, "residual")
-    views.add(out, "out", True)
-    xv, gv, rv, ov = views.addresses()
     _need(weight, "weight", (D,), torch.float32, dev)
-    with _device(dev):
+    with _device(dev, stream, (x, gate, weight, residual, out)) as output:
+        if out is None:
+            out = output(torch.empty_like(x, memory_format=torch.contiguous_format))
+        views.add(out, "out", True)
+        xv, gv, rv, ov = views.addresses()
         _check(lib().la_gated_norm(xv, gv, _ptr(weight), rv, ov, *n, D, kind, activation, eps, scale, code,
                                    _raw_stream(stream, dev)))
     return out
@@ -121,11 +125,7 @@ def gated_norm_backward(dout, x, gate=None, weight=None, kind=NORM_RMS, activati
     D, code = shape[-1], _dtype_code(dtype)
     if dout is None:
         raise ValueError("dout is required")
-    if out is None:
-        dx = torch.empty_like(x)
-        dgate = torch.empty_like(gate) if gate is not None else None
-        dweight = torch.empty_like(weight) if weight is not None and need_weight else None
-    else:
+    if out is not None:
         dx, dgate, dweight = out
         if dx is None or (dgate is None) != (gate is None) or (dweight is not None and weight is None):
             raise ValueError("out: dx and, with a gate, dgate are always written; dweight needs a weight")
@@ -133,19 +133,21 @@ def gated_norm_backward(dout, x, gate=None, weight=None, kind=NORM_RMS, activati
     views.add(dout, "dout")
     views.add(x, "x")
     views.add(gate, "gate")
-    views.add(dx, "dx", True)
-    views.add(dgate, "dgate", True)
-    dv, xv, gv, dxv, dgv = views.addresses()
     _need(weight, "weight", (D,), torch.float32, dev)
-    _need(dweight, "dweight", (D,), torch.float32, dev)
-    with _device(dev):
+    with _device(dev, stream, (dout, x, gate, weight, workspace, *(out or ()))) as output:
+        if out is None:
+            dx = output(torch.empty_like(x))
+            dgate = output(torch.empty_like(gate)) if gate is not None else None
+            dweight = output(torch.empty_like(weight)) if weight is not None and need_weight else None
+        views.add(dx, "dx", True)
+        views.add(dgate, "dgate", True)
+        dv, xv, gv, dxv, dgv = views.addresses()
+        _need(dweight, "dweight", (D,), torch.float32, dev)
         if workspace is not None:
             if workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
                 raise ValueError("workspace: expected a contiguous uint8 tensor on the inputs' device")
         elif dweight is not None:
             workspace = torch.empty(max(_norm_workspace_size(n, D), 1), dtype=torch.uint8, device=dev)
-            if stream is not None:
-                workspace.record_stream(stream)
         _check(lib().la_gated_norm_backward(
             dv, xv, gv, _ptr(weight), dxv, dgv, _ptr(dweight), *n, D, kind, activation, eps, scale, code, _ptr(workspace),
             0 if workspace is None else workspace.numel(), _raw_stream(stream, dev)))
@@ -196,17 +198,17 @@ def rotary(x, freq, positions=None, x2=None, start=0, layout=ROTARY_HALF, mscale
             raise ValueError("start applies only without positions")
         pstride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
     shape, shape2, dtype = (B, H, T, D), (B, H2, T, D), x.dtype
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    if out2 is None and x2 is not None:
-        out2 = torch.empty_like(x2, memory_format=torch.contiguous_format)
     views = _Views(shape, dtype, dev)
     views.add(x, "x")
     views.add(x2, "x2", shape=shape2)
-    views.add(out, "out", True)
-    views.add(out2, "out2", True, shape2)
-    xv, xv2, ov, ov2 = views.addresses()
-    with _device(dev):
+    with _device(dev, stream, (x, x2, freq, positions, out, out2)) as output:
+        if out is None:
+            out = output(torch.empty_like(x, memory_format=torch.contiguous_format))
+        if out2 is None and x2 is not None:
+            out2 = output(torch.empty_like(x2, memory_format=torch.contiguous_format))
+        views.add(out, "out", True)
+        views.add(out2, "out2", True, shape2)
+        xv, xv2, ov, ov2 = views.addresses()
         _check(lib().la_rotary(xv, H, xv2, H2, ov, ov2, freq.data_ptr(), _ptr(positions), pstride, start, B, T, D, R, layout,
                                mscale, 1 if backward else 0, code, _raw_stream(stream, dev)))
     return (out, out2) if x2 is not None else out

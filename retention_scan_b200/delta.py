@@ -49,11 +49,9 @@ def _heads(q, k, v, beta, decay_kind, log_g, token):
     return B, H, Hk, (1 if token else shape[2]), Dk, Dv
 
 
-def _scratch(workspace, nbytes, dev, stream):
+def _scratch(workspace, nbytes, dev):
     if workspace is None:
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-        if stream is not None:
-            workspace.record_stream(stream)
     elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous uint8 tensor on the inputs' device")
     return workspace
@@ -78,22 +76,23 @@ def delta_forward(q, k, v, beta, decay_kind=DECAY_NONE, log_g=None, init_state=N
     value heads j H / Hk and the ones after it); float32 or bfloat16 CUDA
     tensors.  beta [B,H,T] fp32; decay_kind / log_g as chunk_forward;
     init_state [B,H,Dk,Dv] fp32 or None.  Returns (out [B,H,T,Dv],
-    final_state or None).  workspace: None allocates it with torch on the
-    call's stream, or a CUDA uint8 tensor of at least
+    final_state or None).  stream: None, the current one, or a stream that the
+    caller has ordered behind the inputs; the call runs and allocates on it, and
+    tensors may be dropped while it runs.  workspace: None allocates it with
+    torch on that stream, or a CUDA uint8 tensor of at least
     delta_workspace_size(...) bytes."""
     B, H, Hk, T, Dk, Dv = _heads(q, k, v, beta, decay_kind, log_g, token=False)
     dev = q.device
     _need(init_state, "init_state", (B, H, Dk, Dv), torch.float32, dev)
-    if out is None:
-        out = torch.empty_like(v)
-    else:
-        _need(out, "out", v.shape, q.dtype, dev)
-    if final_state is None and return_final:
-        final_state = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
+    _need(out, "out", v.shape, q.dtype, dev)
     _need(final_state, "final_state", (B, H, Dk, Dv), torch.float32, dev)
     d = _decay(decay_kind, log_g)
-    with _device(dev):
-        workspace = _scratch(workspace, delta_workspace_size(B, H, T, Dk, Dv, q.dtype, Hk), dev, stream)
+    with _device(dev, stream, (q, k, v, beta, log_g, init_state, out, final_state, workspace)) as output:
+        if out is None:
+            out = output(torch.empty_like(v))
+        if final_state is None and return_final:
+            final_state = output(torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev))
+        workspace = _scratch(workspace, delta_workspace_size(B, H, T, Dk, Dv, q.dtype, Hk), dev)
         _check(lib().la_delta_forward_ws(
             _ptr(q), _ptr(k), _ptr(v), _ptr(beta), ctypes.byref(d) if d is not None else None, float(q_scale),
             _ptr(init_state), _ptr(out), _ptr(final_state), B, H, Hk, T, Dk, Dv, _dtype_code(q.dtype),
@@ -127,11 +126,7 @@ def delta_backward(q, k, v, beta, dy, decay_kind=DECAY_NONE, log_g=None, init_st
     _need(dy, "dy", (B, H, T, Dv), q.dtype, dev)
     _need(init_state, "init_state", (B, H, Dk, Dv), torch.float32, dev)
     _need(d_final_state, "d_final_state", (B, H, Dk, Dv), torch.float32, dev)
-    if out is None:
-        dq, dk, dv, dbeta = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(beta)
-        d_log_g = torch.empty_like(log_g) if decay_kind != DECAY_NONE and need_log_g else None
-        d_init = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev) if need_init_state else None
-    else:
+    if out is not None:
         dq, dk, dv, dbeta, d_log_g, d_init = out
         if any(x is None for x in (dq, dk, dv, dbeta)):
             raise ValueError("out: dq, dk, dv and dbeta are always written")
@@ -145,9 +140,12 @@ def delta_backward(q, k, v, beta, dy, decay_kind=DECAY_NONE, log_g=None, init_st
             _need(d_log_g, "d_log_g", tuple(log_g.shape), torch.float32, dev)
         _need(d_init, "d_init_state", (B, H, Dk, Dv), torch.float32, dev)
     d = _decay(decay_kind, log_g)
-    with _device(dev):
-        workspace = _scratch(workspace, delta_backward_workspace_size(B, H, T, Dk, Dv, q.dtype, Hk, decay_kind),
-                             dev, stream)
+    with _device(dev, stream, (q, k, v, beta, dy, log_g, init_state, d_final_state, workspace, *(out or ()))) as output:
+        if out is None:
+            dq, dk, dv, dbeta = (output(torch.empty_like(x)) for x in (q, k, v, beta))
+            d_log_g = output(torch.empty_like(log_g)) if decay_kind != DECAY_NONE and need_log_g else None
+            d_init = output(torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)) if need_init_state else None
+        workspace = _scratch(workspace, delta_backward_workspace_size(B, H, T, Dk, Dv, q.dtype, Hk, decay_kind), dev)
         _check(lib().la_delta_backward_ws(
             _ptr(q), _ptr(k), _ptr(v), _ptr(beta), ctypes.byref(d) if d is not None else None, float(q_scale),
             _ptr(init_state), _ptr(dy), _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbeta), _ptr(d_log_g),
@@ -165,12 +163,11 @@ def delta_decode_step(q, k, v, beta, state, decay_kind=DECAY_NONE, log_g=None, q
     if state is None:
         raise ValueError("state is required")
     _need(state, "state", (B, H, Dk, Dv), torch.float32, dev)
-    if out is None:
-        out = torch.empty_like(v)
-    else:
-        _need(out, "out", v.shape, q.dtype, dev)
+    _need(out, "out", v.shape, q.dtype, dev)
     d = _decay(decay_kind, log_g)
-    with _device(dev):
+    with _device(dev, stream, (q, k, v, beta, log_g, state, out)) as output:
+        if out is None:
+            out = output(torch.empty_like(v))
         _check(lib().la_delta_decode_step(
             _ptr(q), _ptr(k), _ptr(v), _ptr(beta), ctypes.byref(d) if d is not None else None, float(q_scale),
             _ptr(state), _ptr(out), B, H, Hk, Dk, Dv, _dtype_code(q.dtype), _raw_stream(stream, dev)))

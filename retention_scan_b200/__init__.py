@@ -226,7 +226,7 @@ class _On(torch.cuda.StreamContext):
         self.caller = torch.cuda.current_stream(dev)
         if self.caller != stream:
             for t in used:
-                if t is not None:
+                if t is not None and t.is_cuda:
                     t.record_stream(stream)
 
     def __enter__(self):
@@ -252,6 +252,8 @@ def _device(dev, stream=None, used=()):
     goes through.  used: the caller's tensors that the call reads or writes (or
     None).  torch's own contexts, which cost a small call's launch again, only
     where they change something."""
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got tensors on {dev}")
     if stream is not None:
         return _On(stream, dev, used)
     return _here if dev.index == torch.cuda.current_device() else _There(dev)
@@ -272,12 +274,10 @@ def workspace_size(B, H, T, Dk, Dv, dtype=torch.bfloat16, normalize=False):
     return int(lib().la_chunk_forward_workspace_size(B, H, T, Dk, Dv, _dtype_code(dtype), int(bool(normalize))))
 
 
-def _workspace(workspace, B, H, T, Dk, Dv, dtype, normalize, stream, dev):
+def _workspace(workspace, B, H, T, Dk, Dv, dtype, normalize, dev):
     if workspace is True:
         nbytes = workspace_size(B, H, T, Dk, Dv, dtype, normalize)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        if workspace is not None and stream is not None:
-            workspace.record_stream(stream)
     elif workspace is False:
         workspace = None
     if workspace is not None:
@@ -301,6 +301,9 @@ def chunk_forward(q, k, v, decay_kind=DECAY_NONE, log_g=None, normalize=False,
     init_state [B,H,Dk,Dv] / init_z [B,H,Dk]: fp32 carried state and key sum.
     Returns (out, final_state, final_z); final_* are None unless requested
     (return_final, or passed in), final_z only when normalize.
+    stream (every call): None, the current one, or a stream that the caller
+    has ordered behind the inputs; the call runs and allocates on it, and
+    tensors may be dropped while it runs.
     workspace: True allocates the scratch that lets short-on-heads inputs run
     as T-segments (a torch allocation on the call's stream), None/False runs
     without, or a CUDA uint8 tensor to use.
@@ -321,18 +324,19 @@ def chunk_forward(q, k, v, decay_kind=DECAY_NONE, log_g=None, normalize=False,
         _need(log_g, "log_g", (B, H, T), torch.float32, dev)
     _need(init_state, "init_state", (B, H, Dk, Dv), torch.float32, dev)
     _need(init_z, "init_z", (B, H, Dk), torch.float32, dev)
-    if out is None:
-        out = torch.empty((B, H, T, Dv), dtype=q.dtype, device=dev)
     _need(out, "out", (B, H, T, Dv), q.dtype, dev)
-    if final_state is None and return_final:
-        final_state = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
-    if final_z is None and return_final and normalize:
-        final_z = torch.empty((B, H, Dk), dtype=torch.float32, device=dev)
     _need(final_state, "final_state", (B, H, Dk, Dv), torch.float32, dev)
     _need(final_z, "final_z", (B, H, Dk), torch.float32, dev)
     d = _decay(decay_kind, log_g)
-    with torch.cuda.device(dev):
-        workspace = _workspace(workspace, B, H, T, Dk, Dv, q.dtype, normalize, stream, dev)
+    with _device(dev, stream, (q, k, v, log_g, init_state, init_z, out, final_state, final_z,
+                               None if isinstance(workspace, bool) else workspace)) as output:
+        if out is None:
+            out = output(torch.empty((B, H, T, Dv), dtype=q.dtype, device=dev))
+        if final_state is None and return_final:
+            final_state = output(torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev))
+        if final_z is None and return_final and normalize:
+            final_z = output(torch.empty((B, H, Dk), dtype=torch.float32, device=dev))
+        workspace = _workspace(workspace, B, H, T, Dk, Dv, q.dtype, normalize, dev)
         nbytes = 0 if workspace is None else workspace.numel()
         if feature_map != FEATURE_NONE or q_scale != 1.0:
             if reverse:
@@ -367,12 +371,12 @@ def bidirectional(q, k, v, decay_kind=DECAY_NONE, log_g=None, normalize=False, o
         _need(log_g, "log_g", (H,), torch.float32, dev)
     elif decay_kind == DECAY_PER_STEP:
         _need(log_g, "log_g", (B, H, T), torch.float32, dev)
-    if out is None:
-        out = torch.empty((B, H, T, Dv), dtype=q.dtype, device=dev)
     _need(out, "out", (B, H, T, Dv), q.dtype, dev)
     d = _decay(decay_kind, log_g)
-    with torch.cuda.device(dev):
-        workspace = _workspace(workspace, B, H, T, Dk, Dv, q.dtype, normalize, stream, dev)
+    with _device(dev, stream, (q, k, v, log_g, out, None if isinstance(workspace, bool) else workspace)) as output:
+        if out is None:
+            out = output(torch.empty((B, H, T, Dv), dtype=q.dtype, device=dev))
+        workspace = _workspace(workspace, B, H, T, Dk, Dv, q.dtype, normalize, dev)
         _check(lib().la_chunk_bidirectional_ws(
             _ptr(q), _ptr(k), _ptr(v), ctypes.byref(d) if d is not None else None, int(bool(normalize)),
             _ptr(out), B, H, T, Dk, Dv, code, _ptr(workspace), 0 if workspace is None else workspace.numel(),
@@ -415,12 +419,7 @@ def chunk_backward(q, k, v, dy, decay_kind=DECAY_NONE, log_g=None, init_state=No
         _need(log_g, "log_g", (B, H, T), torch.float32, dev)
     _need(init_state, "init_state", (B, H, Dk, Dv), torch.float32, dev)
     _need(d_final_state, "d_final_state", (B, H, Dk, Dv), torch.float32, dev)
-    if out is None:
-        dq, dk = torch.empty_like(q), torch.empty_like(k)
-        dv = torch.empty_like(v)
-        d_log_g = torch.empty_like(log_g) if (decay_kind != DECAY_NONE and need_log_g) else None
-        d_init = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev) if need_init_state else None
-    else:
+    if out is not None:
         dq, dk, dv, d_log_g, d_init = out
         _need(dq, "dq", (B, H, T, Dk), q.dtype, dev)
         _need(dk, "dk", (B, H, T, Dk), q.dtype, dev)
@@ -429,12 +428,14 @@ def chunk_backward(q, k, v, dy, decay_kind=DECAY_NONE, log_g=None, init_state=No
             _need(d_log_g, "d_log_g", tuple(log_g.shape), torch.float32, dev)
         _need(d_init, "d_init_state", (B, H, Dk, Dv), torch.float32, dev)
     d = _decay(decay_kind, log_g)
-    with torch.cuda.device(dev):
+    with _device(dev, stream, (q, k, v, dy, log_g, init_state, d_final_state, workspace, *(out or ()))) as output:
+        if out is None:
+            dq, dk, dv = (output(torch.empty_like(x)) for x in (q, k, v))
+            d_log_g = output(torch.empty_like(log_g)) if (decay_kind != DECAY_NONE and need_log_g) else None
+            d_init = output(torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)) if need_init_state else None
         nbytes = backward_workspace_size(B, H, T, Dk, Dv, q.dtype, decay_kind)
         if workspace is None:
             workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-            if stream is not None:
-                workspace.record_stream(stream)
         elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace: expected a contiguous uint8 tensor on the inputs' device")
         _check(lib().la_chunk_backward_ws(
@@ -466,22 +467,21 @@ def chunk_state(k, v, decay_kind=DECAY_NONE, log_g=None, normalize=False, state_
         _need(log_g, "log_g", (H,), torch.float32, dev)
     elif decay_kind == DECAY_PER_STEP:
         _need(log_g, "log_g", (B, H, T), torch.float32, dev)
-    if state_out is None:
-        state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
-    if z_out is None and normalize:
-        z_out = torch.empty((B, H, Dk), dtype=torch.float32, device=dev)
-    if log_g_total is None:
-        log_g_total = torch.empty((B, H), dtype=torch.float32, device=dev)
     _need(state_out, "state_out", (B, H, Dk, Dv), torch.float32, dev)
     _need(z_out, "z_out", (B, H, Dk), torch.float32, dev)
     _need(log_g_total, "log_g_total", (B, H), torch.float32, dev)
     d = _decay(decay_kind, log_g)
-    with torch.cuda.device(dev):
+    with _device(dev, stream, (k, v, log_g, state_out, z_out, log_g_total,
+                               None if isinstance(workspace, bool) else workspace)) as output:
+        if state_out is None:
+            state_out = output(torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev))
+        if z_out is None and normalize:
+            z_out = output(torch.empty((B, H, Dk), dtype=torch.float32, device=dev))
+        if log_g_total is None:
+            log_g_total = output(torch.empty((B, H), dtype=torch.float32, device=dev))
         if workspace is True:
             nbytes = state_workspace_size(B, H, T, Dk, Dv, k.dtype, normalize)
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-            if workspace is not None and stream is not None:
-                workspace.record_stream(stream)
         elif workspace is False:
             workspace = None
         _check(lib().la_chunk_state_ws(
@@ -515,17 +515,17 @@ def state_combine(seg_state, seg_log_g, seg_z=None, init_state=None, init_z=None
     ss = _span_rows(seg_state, "seg_state", (B, H, Dk, Dv))
     ls = _span_rows(seg_log_g, "seg_log_g", (B, H))
     zs = _span_rows(seg_z, "seg_z", (B, H, Dk)) if seg_z is not None else 0
-    if state_out is None:
-        state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
-    if z_out is None and seg_z is not None:
-        z_out = torch.empty((B, H, Dk), dtype=torch.float32, device=dev)
-    if log_g_out is None:
-        log_g_out = torch.empty((B, H), dtype=torch.float32, device=dev)
     for t, name, shape in ((init_state, "init_state", (B, H, Dk, Dv)), (init_z, "init_z", (B, H, Dk)),
                            (state_out, "state_out", (B, H, Dk, Dv)), (z_out, "z_out", (B, H, Dk)),
                            (log_g_out, "log_g_out", (B, H))):
         _need(t, name, shape, torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _device(dev, stream, (seg_state, seg_log_g, seg_z, init_state, init_z, state_out, z_out, log_g_out)) as output:
+        if state_out is None:
+            state_out = output(torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev))
+        if z_out is None and seg_z is not None:
+            z_out = output(torch.empty((B, H, Dk), dtype=torch.float32, device=dev))
+        if log_g_out is None:
+            log_g_out = output(torch.empty((B, H), dtype=torch.float32, device=dev))
         _check(lib().la_state_combine(
             _ptr(seg_state) if n else None, _ptr(seg_z) if n and seg_z is not None else None,
             _ptr(seg_log_g) if n else None, ss, zs, ls, n, _ptr(init_state), _ptr(init_z), _ptr(state_out),
@@ -544,13 +544,13 @@ def ema_scan(x, f, init_state=None, reverse=False, out=None, final_state=None, r
     _need(f, "f", (B, T, C), x.dtype, dev)
     _need(x, "x", (B, T, C), x.dtype, dev)
     _need(init_state, "init_state", (B, C), torch.float32, dev)
-    if out is None:
-        out = torch.empty((B, T, C), dtype=x.dtype, device=dev)
     _need(out, "out", (B, T, C), x.dtype, dev)
-    if final_state is None and return_final:
-        final_state = torch.empty((B, C), dtype=torch.float32, device=dev)
     _need(final_state, "final_state", (B, C), torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _device(dev, stream, (x, f, init_state, out, final_state)) as output:
+        if out is None:
+            out = output(torch.empty((B, T, C), dtype=x.dtype, device=dev))
+        if final_state is None and return_final:
+            final_state = output(torch.empty((B, C), dtype=torch.float32, device=dev))
         _check(lib().la_ema_scan(_ptr(x), _ptr(f), _ptr(init_state), _ptr(out), _ptr(final_state), B, T, C, code,
                                  int(bool(reverse)), _stream(stream, dev)))
     return out, final_state
@@ -581,18 +581,17 @@ def wkv4_forward(k, v, w, u, init_state=None, out=None, final_state=None, return
     _need(w, "w", (C,), torch.float32, dev)
     _need(u, "u", (C,), torch.float32, dev)
     _need(init_state, "init_state", (B, 3, C), torch.float32, dev)
-    if out is None:
-        out = torch.empty((B, T, C), dtype=k.dtype, device=dev)
     _need(out, "out", (B, T, C), k.dtype, dev)
-    if final_state is None and return_final:
-        final_state = torch.empty((B, 3, C), dtype=torch.float32, device=dev)
     _need(final_state, "final_state", (B, 3, C), torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _device(dev, stream, (k, v, w, u, init_state, out, final_state,
+                               None if isinstance(workspace, bool) else workspace)) as output:
+        if out is None:
+            out = output(torch.empty((B, T, C), dtype=k.dtype, device=dev))
+        if final_state is None and return_final:
+            final_state = output(torch.empty((B, 3, C), dtype=torch.float32, device=dev))
         if workspace is True:
             nbytes = wkv4_workspace_size(B, T, C, k.dtype)
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-            if workspace is not None and stream is not None:
-                workspace.record_stream(stream)
         elif workspace is False:
             workspace = None
         _check(lib().la_wkv4_forward_ws(_ptr(k), _ptr(v), _ptr(w), _ptr(u), _ptr(init_state), _ptr(out),
@@ -625,17 +624,15 @@ def chunk_backward_normalized(q, k, v, dy, decay_kind=DECAY_NONE, log_g=None, in
     _need(init_z, "init_z", (B, H, Dk), torch.float32, dev)
     _need(d_final_state, "d_final_state", (B, H, Dk, Dv), torch.float32, dev)
     _need(d_final_z, "d_final_z", (B, H, Dk), torch.float32, dev)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    d_log_g = torch.empty_like(log_g) if (decay_kind != DECAY_NONE and need_log_g) else None
-    d_init = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev) if need_init_state else None
-    d_init_z = torch.empty((B, H, Dk), dtype=torch.float32, device=dev) if need_init_state else None
     d = _decay(decay_kind, log_g)
-    with torch.cuda.device(dev):
+    with _device(dev, stream, (q, k, v, dy, log_g, init_state, init_z, d_final_state, d_final_z, workspace)) as output:
+        dq, dk, dv = (output(torch.empty_like(x)) for x in (q, k, v))
+        d_log_g = output(torch.empty_like(log_g)) if (decay_kind != DECAY_NONE and need_log_g) else None
+        d_init = output(torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)) if need_init_state else None
+        d_init_z = output(torch.empty((B, H, Dk), dtype=torch.float32, device=dev)) if need_init_state else None
         nbytes = int(lib().la_chunk_backward_norm_workspace_size(B, H, T, Dk, Dv, code, int(decay_kind)))
         if workspace is None:
             workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-            if stream is not None:
-                workspace.record_stream(stream)
         elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace: expected a contiguous uint8 tensor on the inputs' device")
         _check(lib().la_chunk_backward_norm_ws(
@@ -667,11 +664,11 @@ def decode_step(q, k, v, state, z=None, decay_kind=DECAY_NONE, log_g=None, norma
         _need(log_g, "log_g", (H,), torch.float32, dev)
     elif decay_kind == DECAY_PER_STEP:
         _need(log_g, "log_g", (B, H), torch.float32, dev)
-    if out is None:
-        out = torch.empty((B, H, Dv), dtype=q.dtype, device=dev)
     _need(out, "out", (B, H, Dv), q.dtype, dev)
     d = _decay(decay_kind, log_g)
-    with torch.cuda.device(dev):
+    with _device(dev, stream, (q, k, v, log_g, state, z, out)) as output:
+        if out is None:
+            out = output(torch.empty((B, H, Dv), dtype=q.dtype, device=dev))
         if feature_map != FEATURE_NONE or q_scale != 1.0:
             pro = _Prologue(int(feature_map), float(q_scale))
             _check(lib().la_decode_step_pro(

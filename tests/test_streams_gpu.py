@@ -23,9 +23,11 @@ def inputs():
     rn = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
     B, H, T, D = 4, 8, 96, 128  # 1.5 MB and more a tensor: blocks of their own
     unit = lambda x: (x / x.norm(dim=-1, keepdim=True)).bfloat16()  # noqa: E731
-    return dict(q=unit(rn(B, H, T, D)), k=unit(rn(B, H, T, D)), v=rn(B, H, T, D).bfloat16(), beta=torch.sigmoid(rn(B, H, T)),
+    i = dict(q=unit(rn(B, H, T, D)), k=unit(rn(B, H, T, D)), v=rn(B, H, T, D).bfloat16(), beta=torch.sigmoid(rn(B, H, T)),
                 lg=torch.nn.functional.logsigmoid(3 + rn(B, H, T)), S=rn(B, H, D, D), w=1 + 0.1 * rn(D),
-                freq=la.rotary_frequencies(D, device="cuda")[0])
+             freq=la.rotary_frequencies(D, device="cuda")[0], beta16=torch.sigmoid(rn(B, H, T, D)).bfloat16())
+    # made here: what a call makes of its inputs on the current stream would not be ordered before a stream's kernels
+    return dict(i, qa=i["q"].abs(), ka=i["k"].abs(), seg=i["S"][None].clone(), seg_lg=i["lg"][None, :, :, 0].clone(), w8=i["w"].repeat(8))
 
 
 def token(t):
@@ -38,6 +40,17 @@ CALLS = {
     "gated_norm": lambda i, **k: la.gated_norm(i["v"], i["q"], i["w"], **k),
     "gated_norm_backward": lambda i, **k: la.gated_norm_backward(i["v"], i["q"], i["k"], i["w"], **k),
     "rotary": lambda i, **k: la.rotary(i["q"], i["freq"], None, i["k"], **k),
+    "chunk_forward": lambda i, **k: la.chunk_forward(i["q"], i["k"], i["v"], 2, i["lg"], init_state=i["S"], **k),
+    "chunk_forward_raw": lambda i, **k: la.chunk_forward(i["q"], i["k"], i["v"], 2, i["lg"], normalize=True,
+                                                         feature_map=la.FEATURE_ELU1, **k),
+    "chunk_reverse": lambda i, **k: la.chunk_forward(i["q"], i["k"], i["v"], 2, i["lg"], reverse=True, **k),
+    "bidirectional": lambda i, **k: la.bidirectional(i["q"], i["k"], i["v"], 2, i["lg"], **k),
+    "chunk_backward": lambda i, **k: la.chunk_backward(i["q"], i["k"], i["v"], i["v"], 2, i["lg"], i["S"], **k),
+    "chunk_backward_normalized": lambda i, **k: la.chunk_backward_normalized(i["qa"], i["ka"], i["v"], i["v"], 2, i["lg"], **k),
+    "chunk_state": lambda i, **k: la.chunk_state(i["k"], i["v"], 2, i["lg"], normalize=True, **k),
+    "state_combine": lambda i, **k: la.state_combine(i["seg"], i["seg_lg"], init_state=i["S"], **k),
+    "ema_scan": lambda i, **k: la.ema_scan(i["v"].view(4, 96, 1024), i["beta16"].view(4, 96, 1024), **k),
+    "wkv4_forward": lambda i, **k: la.wkv4_forward(i["k"].view(4, 96, 1024), i["v"].view(4, 96, 1024), i["w8"], i["w8"], **k),
 }
 
 
@@ -117,6 +130,17 @@ def test_one_token_on_a_busy_stream():
         torch.cuda._sleep(SPIN)
     got = la.delta_decode_step(*args, stream=s)
     del args  # the token's tensors go while the call has yet to read them
+    new = [torch.full_like(want, 7.0) for _ in range(16)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(i["S"], state) and all((t == 7.0).all() for t in new)
+    # and the plain scan's
+    want = la.decode_step(token(i["q"]), token(i["k"]), token(i["v"]), state, None, 2, token(i["lg"]))
+    args = [token(i[n]) for n in ("q", "k", "v")] + [i["S"], None, 2, token(i["lg"])]
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(SPIN)
+    got = la.decode_step(*args, stream=s)
+    del args
     new = [torch.full_like(want, 7.0) for _ in range(16)]
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(i["S"], state) and all((t == 7.0).all() for t in new)

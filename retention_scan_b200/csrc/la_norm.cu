@@ -63,11 +63,23 @@ __device__ __forceinline__ float team_sum(float x, float* red) {
     return x;
 }
 
-// 1 / (1 + e^-z) with the fast exponential and reciprocal; e^-z beyond the range
-// is infinite and gives 0.
+// 1 / (1 + e^-z) = 1 / (1 + 2^t), t = -z log2 e, by the fast exponential and reciprocal;
+// 2^t beyond the range is infinite and gives 0.  t rounded to fp32 is off by more the
+// larger |z| is: 60 steps of 2^-24 of the result at z = -85.  That stays below a bf16
+// step; fp32 tensors take what the rounding left along, 2^(hi + lo) = 2^hi (1 + lo ln 2)
+// (B4 H16 T4096 D128 fp32: forward 67.6 us either way, gradients 128 and 131; by expf and a division 71.7 and 137).
+template <typename T>
 __device__ __forceinline__ float sigmoid(float z) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-1.4426950408889634f * z)));
+    constexpr float kLog2E = 1.44269504088896341f, kLog2ELow = static_cast<float>(1.44269504088896341 - kLog2E);
+    const float hi = -kLog2E * z;
+    float e = ex2_approx(hi), r;
+    if constexpr (sizeof(T) == 4) {
+        const float lo = fmaf(-kLog2E, z, -hi) - kLog2ELow * z;
+        if (fabsf(hi) < 127.f) e = fmaf(e, 0.693147180559945309f * lo, e);  // beyond, 2^t is 0 or infinite, and lo NaN for infinite z
+        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    } else {
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    }
     return r;
 }
 
@@ -167,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(Args a) {
                 float z[V], f[V];
                 zr[u].unpack(z);
 #pragma unroll
-                for (int i = 0; i < V; ++i) f[i] = sigmoid(z[i]);
+                for (int i = 0; i < V; ++i) f[i] = sigmoid<T>(z[i]);
                 if (silu) vmul(f, f, z);
                 vmul(x[u], x[u], f);
             }
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, NV * V > 16 ? 1 : 2) backward_kernel
                     if (silu) {
 #pragma unroll
                         for (int i = 0; i < V; ++i) {
-                            const float s = sigmoid(z[i]), act = z[i] * s, n = x[u][i] * r, t = m[u][i] * w[i];
+                            const float s = sigmoid<T>(z[i]), act = z[i] * s, n = x[u][i] * r, t = m[u][i] * w[i];
                             dg[i] = t * n * fmaf(act, 1.f - s, s);  // silu' = s + z s (1 - s)
                             x[u][i] = n;
                             dw[u][i] = fmaf(m[u][i] * act, n, dw[u][i]);
@@ -338,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, NV * V > 16 ? 1 : 2) backward_kernel
                     } else {
 #pragma unroll
                         for (int i = 0; i < V; ++i) {
-                            const float s = sigmoid(z[i]), n = x[u][i] * r, t = m[u][i] * w[i], d = t * s;
+                            const float s = sigmoid<T>(z[i]), n = x[u][i] * r, t = m[u][i] * w[i], d = t * s;
                             dg[i] = d * n * (1.f - s);  // sigmoid' = s (1 - s)
                             x[u][i] = n;
                             dw[u][i] = fmaf(m[u][i] * s, n, dw[u][i]);

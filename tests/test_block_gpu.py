@@ -449,3 +449,21 @@ def test_rows_outside_a_view_stay_as_they_were():
     q = x.view(3, 1, 5, 64)
     la().rotary(q, freq, out=view.unsqueeze(1))
     assert torch.equal(view.unsqueeze(1), la().rotary(q, freq)) and (wide[mask] == 7.0).all()
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+def test_fp32_gates_far_out_keep_their_digits(act):
+    # Every value to (D + 16) steps of 2^-24 of itself, for gates down to where a(z) is 2^-122: the sum of D squares,
+    # its root, the exponential (2 steps of 2^-23), a sum, a division and the products; no step grows with |z|.
+    g = torch.Generator().manual_seed(8)
+    D = 8
+    x, d = (torch.randn(512, D, generator=g).cuda() for _ in range(2))
+    z = torch.linspace(-84, 84, 512 * D)[torch.randperm(512 * D, generator=g)].view(512, D).cuda()
+    y = f64(la().gated_norm(x, z, **how("rms", act)))
+    ref = oracle.gated_norm(x, z, None, None, "rms", act)
+    assert (np.abs(y - ref) <= (D + 16) * U * np.abs(ref)).all()
+    # the gate's gradient from the same factors, where its two terms do not cancel: silu' = s + z s (1 - s), sigmoid' = s (1 - s)
+    dg = f64(la().gated_norm_backward(d, x, z, **how("rms", act))[1])
+    ref = oracle.gated_norm_backward(d, x, z, None, "rms", act)[1]
+    far = f64(z) < -4
+    assert (np.abs(dg - ref) <= 2 * (D + 16) * U * np.abs(ref))[far].all()

@@ -24,10 +24,11 @@ def inputs():
     B, H, T, D = 4, 8, 96, 128  # 1.5 MB and more a tensor: blocks of their own
     unit = lambda x: (x / x.norm(dim=-1, keepdim=True)).bfloat16()  # noqa: E731
     i = dict(q=unit(rn(B, H, T, D)), k=unit(rn(B, H, T, D)), v=rn(B, H, T, D).bfloat16(), beta=torch.sigmoid(rn(B, H, T)),
-                lg=torch.nn.functional.logsigmoid(3 + rn(B, H, T)), S=rn(B, H, D, D), w=1 + 0.1 * rn(D),
+             lg=torch.nn.functional.logsigmoid(3 + rn(B, H, T)), S=rn(B, H, D, D), w=1 + 0.1 * rn(D),
              freq=la.rotary_frequencies(D, device="cuda")[0], beta16=torch.sigmoid(rn(B, H, T, D)).bfloat16())
     # made here: what a call makes of its inputs on the current stream would not be ordered before a stream's kernels
-    return dict(i, qa=i["q"].abs(), ka=i["k"].abs(), seg=i["S"][None].clone(), seg_lg=i["lg"][None, :, :, 0].clone(), w8=i["w"].repeat(8))
+    return dict(i, qa=i["q"].abs(), ka=i["k"].abs(), seg=i["S"][None].clone(), seg_lg=i["lg"][None, :, :, 0].clone(),
+                w8=i["w"].repeat(8))
 
 
 def token(t):

@@ -826,14 +826,15 @@ typedef enum {
  *
  *     (a, b) <- mscale * (a cos - b sin, a sin + b cos),
  *
- * the other D - R elements are copied.  Angles are reduced in 64 bits.
+ * the other D - R elements are copied.  Angles are reduced modulo 2 pi to 2^-23.
  *
  *   x, out         views of [B,H,T] rows; x2, out2: of [B,H2,T] rows, or NULL with H2 = 0.
  *                  out may be x itself, out2 x2 itself.
  *   freq           [R/2] fp32, whatever scaling for long contexts it carries.
  *   positions      NULL: token t is at start + t; else int64 on the device, position of
  *                  (b, t) at positions[b * positions_stride + t] (stride 0: one for all).
- *                  Magnitudes up to 2^53.
+ *                  Magnitudes up to 2^53 (start .. start + T beyond them is refused,
+ *                  positions on the device cannot be looked at).
  *   backward       0, or 1 for the transposed map (angles negated, mscale kept):
  *                  the gradient with respect to x.
  *

@@ -50,12 +50,30 @@ def gated_norm_backward(dout, x, gate=None, weight=None, kind="rms", activation=
     return dx, dgate, dweight
 
 
+_SHIFT = 240
+_TWO_PI = int("6283185307179586476925286766559005768394338798750211641949889184615632812572417997256") * (1 << _SHIFT) // 10 ** 84
+
+
+def _angles(positions, freq):
+    """positions[..., None] * freq modulo 2 pi: far positions in whole numbers, since a
+    64-bit product at 2^45 is off by 2^-9 already."""
+    if np.abs(positions).max(initial=0) * np.abs(freq).max() < 2 ** 20:
+        return positions[..., None] * freq
+    out = np.empty(positions.shape + freq.shape)
+    for j, f in enumerate(freq):
+        m, d = float(f).as_integer_ratio()
+        for at in np.ndindex(positions.shape):
+            turns = (int(positions[at]) * m << _SHIFT) // d % _TWO_PI
+            out[at + (j,)] = float(turns >> (_SHIFT - 60)) / 2.0 ** 60
+    return out
+
+
 def rotary(x, freq, positions, layout="half", mscale=1.0, backward=False):
     """x [B,H,T,D], freq [R/2], positions broadcastable to [B,T]; pairs as complex numbers."""
     x, freq = _f64(x), _f64(freq)
     B, _, T, _ = x.shape
     R = 2 * freq.shape[0]
-    angle = np.broadcast_to(np.asarray(positions, dtype=np.float64), (B, T))[:, None, :, None] * freq
+    angle = _angles(np.broadcast_to(np.asarray(positions, dtype=np.float64), (B, T)), freq)[:, None]
     turn = mscale * np.exp((-1j if backward else 1j) * angle)
     out = x.copy()
     a, b = (slice(0, R // 2), slice(R // 2, R)) if layout == "half" else (slice(0, R, 2), slice(1, R, 2))

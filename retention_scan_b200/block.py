@@ -162,7 +162,7 @@ def rotary(x, freq, positions=None, x2=None, start=0, layout=ROTARY_HALF, mscale
 
     freq: fp32 [R/2], the pairs' inverse frequencies (rotary_frequencies); the
     first R elements of each row turn, the rest is copied.  positions: None
-    (token t is at start + t), or int64 [T] or [B,T].  layout: ROTARY_HALF or
+    (token t is at start + t), or int64 [T] or [B,T], up to 2^53 either way.  layout: ROTARY_HALF or
     ROTARY_INTERLEAVED.  mscale: factor of the rotated part.  backward: the
     transposed map, which takes the outputs' gradients to the inputs'.
     Returns out, or (out, out2) with x2: contiguous unless given; each may be
@@ -197,6 +197,8 @@ def rotary(x, freq, positions=None, x2=None, start=0, layout=ROTARY_HALF, mscale
         if start != 0:
             raise ValueError("start applies only without positions")
         pstride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    elif not -(1 << 53) <= start <= (1 << 53) - T:
+        raise ValueError(f"start: positions {start} .. {start} + {T} exceed 2^53")
     shape, shape2, dtype = (B, H, T, D), (B, H2, T, D), x.dtype
     views = _Views(shape, dtype, dev)
     views.add(x, "x")

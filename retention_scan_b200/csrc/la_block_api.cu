@@ -114,6 +114,8 @@ la_status la_rotary(const la_view* x, int H, const la_view* x2, int H2, const la
     if (!std::isfinite(mscale) || (dtype != LA_F32 && dtype != LA_BF16)) return LA_ERR_INVALID_ARG;
     if (!x2 && H2 != 0) return LA_ERR_INVALID_ARG;
     if (positions && (!aligned_to(positions, 8) || positions_stride < 0)) return LA_ERR_INVALID_ARG;
+    constexpr long long kFar = 1ll << 53;  // positions are exact in 64-bit floating point up to here
+    if (!positions && (start < -kFar || start > kFar - T)) return LA_ERR_INVALID_ARG;
     if (D > la::norm::kMaxWidth) return LA_ERR_UNSUPPORTED;
     const long long heads = static_cast<long long>(H) + H2, tokens = static_cast<long long>(B) * T;
     // a block's items, heads * tokens * D, and the grid, B * T * heads at most, are counted in 32 bits

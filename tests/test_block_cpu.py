@@ -186,3 +186,24 @@ def test_binding_refuses_before_it_calls():
         la.gated_norm_backward(x, x)
     with pytest.raises(ValueError, match="CUDA"):
         la.rotary(torch.zeros(1, 1, 2, 8), torch.zeros(4))
+
+
+def test_oracle_angles_of_far_positions():
+    # 2^53 - 1 turns of a frequency that is a whole number of 2^-24: the product has 77 bits.  By Euler's formula
+    # the angle of p is that of its halves: exp(i p f) from exp(i 2^26 f) and the rest, in 64-bit steps small enough.
+    f = np.array([1.0, 0.71310001611709595, 2.0 ** -20, 3.5])
+    for p in (2 ** 53 - 1, 2 ** 45 + 1, 2 ** 40 + 3, -5, 2 ** 31 + 11):
+        unit = np.exp(1j * f.astype(np.longdouble))
+        z, n, w = np.ones(4, dtype=np.clongdouble), abs(p), unit
+        while n:  # repeated squaring in 64-bit mantissas: p roundings of 2^-64 of the angle
+            z, w, n = (z * w if n & 1 else z), w * w, n >> 1
+        z = z if p > 0 else z.conj()
+        got = np.exp(1j * oracle.block._angles(np.array([float(p)]), f)[0])
+        assert np.abs(got - z.astype(complex)).max() <= abs(p) * 2.0 ** -62 + 1e-14, p
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(start=(1 << 53) - 1), 1), (dict(start=-(1 << 53) - 1), 1), (dict(start=(1 << 63) - 1), 1), (dict(start=-(1 << 63)), 1),
+], ids=str)
+def test_rotary_refuses_starts_beyond_exact_positions(L, over, status):  # noqa: F811
+    assert rot(L, **over) == status

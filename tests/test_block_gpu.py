@@ -467,3 +467,16 @@ def test_fp32_gates_far_out_keep_their_digits(act):
     ref = oracle.gated_norm_backward(d, x, z, None, "rms", act)[1]
     far = f64(z) < -4
     assert (np.abs(dg - ref) <= 2 * (D + 16) * U * np.abs(ref))[far].all()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rotary_angles_up_to_2_to_the_53(layout):
+    # frequencies of 24 bits: the angle's product has up to 77, and its rounding to 64 bits is 0.25 rad at 2^53
+    q = torch.randn(1, 2, 6, 16, generator=torch.Generator().manual_seed(4)).cuda()
+    freq = torch.tensor([1.0, 0.7131, 0.3333333, 1e-3, 2.0 ** -30, 3.1], device="cuda")
+    for pos in ([2 ** 53 - 1, -(2 ** 53) + 1, 2 ** 52 + 1, 2 ** 50 + 7, 2 ** 48 - 5, 2 ** 47 + 9], [2 ** 45 + 1, 2 ** 44, 2 ** 42 - 1, 2 ** 40 + 3, 0, -1]):
+        check_rotary(q, None, freq, torch.tensor(pos, device="cuda"), layout)
+    check_rotary(q, None, freq, None, layout, start=2 ** 53 - 6)
+    for start in (2 ** 53 - 5, -(2 ** 53) - 1, 2 ** 63, 2 ** 64 + 5, -(2 ** 70)):
+        with pytest.raises(ValueError, match="start"):
+            la().rotary(q, freq, start=start)

@@ -485,7 +485,8 @@ cudaError_t teams(const Args& a, bool backward) {
     if (vecs <= 1024) return run<T, V, kThreads, 4>(a, backward);
     if constexpr (V < 8) {
         if (vecs <= 2048) return run<T, V, kThreads, 8>(a, backward);
-        if constexpr (V < 4) return vecs <= 4096 ? run<T, V, kThreads, 16>(a, backward) : run<T, V, kThreads, 32>(a, backward);
+        if constexpr (V == 2) return run<T, V, kThreads, 16>(a, backward);  // 4096 vectors at most
+        if constexpr (V == 1) return vecs <= 4096 ? run<T, V, kThreads, 16>(a, backward) : run<T, V, kThreads, 32>(a, backward);
     }
     return cudaErrorNotSupported;
 }

@@ -57,8 +57,10 @@ class _Views:
         n = len(shape)
         if n == 4:
             self.words += (t.data_ptr(), lead[0], lead[1], lead[2])
-        else:  # fewer leading dimensions: padded to three in front
-            self.words += (t.data_ptr(), *((0,) * (4 - n)), *lead[:-1])
+        elif n == 3:  # a batch of rows: its stride may be any, as the first of three
+            self.words += (t.data_ptr(), lead[0], 0, lead[1])
+        else:
+            self.words += (t.data_ptr(), 0, 0, lead[0] if n == 2 else 0)
 
     def addresses(self):
         """Addresses of the records in the order they were added (None: absent); the buffer lives as long as self."""
@@ -74,7 +76,8 @@ def _rows(x, name="x"):
         raise ValueError(f"{name}: expected a CUDA tensor, got {x.device}")
     if x.shape[-1] < 1:
         raise ValueError(f"{name}: the last dimension is empty")
-    return (1,) * (4 - x.dim()) + tuple(x.shape[:-1])
+    lead = tuple(x.shape[:-1])
+    return lead if len(lead) == 3 else (lead[0], 1, lead[1]) if len(lead) == 2 else (1, 1, *lead) if lead else (1, 1, 1)
 
 
 def gated_norm(x, gate=None, weight=None, residual=None, kind=NORM_RMS, activation=GATE_SILU, eps=1e-5, scale=1.0,

@@ -480,3 +480,22 @@ def test_rotary_angles_up_to_2_to_the_53(layout):
     for start in (2 ** 53 - 5, -(2 ** 53) - 1, 2 ** 63, 2 ** 64 + 5, -(2 ** 70)):
         with pytest.raises(ValueError, match="start"):
             la().rotary(q, freq, start=start)
+
+
+def test_norm_of_a_batch_far_apart():
+    # sequences 2^32 elements and more apart (one layer of a long cache): offsets and strides beyond 32 bits
+    m, apart = la(), 2 ** 32 + 64
+    wide = torch.empty(apart + 8 * 64, dtype=torch.bfloat16, device="cuda")
+    x = wide.as_strided((2, 3, 64), (apart, 128, 1))
+    x.copy_(torch.randn(2, 3, 64, generator=torch.Generator().manual_seed(2)))
+    near_by = x.contiguous()
+    d = torch.randn(2, 3, 64, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    w = torch.ones(64, device="cuda")
+    assert torch.equal(m.gated_norm(x, x, w), m.gated_norm(near_by, near_by, w))
+    for a, b in zip(m.gated_norm_backward(d, x, x, w), m.gated_norm_backward(d, near_by, near_by, w)):
+        assert torch.equal(a, b)
+    want = m.gated_norm(near_by)
+    assert torch.equal(m.gated_norm(x, out=x), want) and torch.equal(x, want)
+    # four dimensions: the batch's stride may be any, the inner two are below 2^32
+    q, freq = x.unsqueeze(1), m.rotary_frequencies(64, device="cuda")[0]
+    assert torch.equal(m.rotary(q, freq), m.rotary(q.contiguous(), freq))

@@ -207,3 +207,14 @@ def test_oracle_angles_of_far_positions():
 ], ids=str)
 def test_rotary_refuses_starts_beyond_exact_positions(L, over, status):  # noqa: F811
     assert rot(L, **over) == status
+
+
+def test_yarn_values():
+    # by hand: 64 / 2 pi = 10.19 turns of the first pair, 1.92 of the second (base 28.2), .36 of the third
+    f, m = la.rotary_frequencies(6, base=28.2, scaling="yarn", factor=4.0, trained_length=64, fast=8.0, slow=1.5)
+    b = [28.2 ** (-i / 3) for i in range(3)]
+    turns = [64 * x / (2 * math.pi) for x in b]
+    assert turns[0] > 8 and 1.5 < turns[1] < 8 and turns[2] < 1.5
+    share = (turns[1] - 1.5) / (8 - 1.5)  # of the trained frequency; the rest of a quarter of it
+    want = [b[0], b[1] * share + b[1] / 4 * (1 - share), b[2] / 4]
+    assert np.allclose(f.double(), want, rtol=2.0 ** -23) and math.isclose(m, 0.1 * math.log(4.0) + 1)

@@ -499,3 +499,64 @@ def test_norm_of_a_batch_far_apart():
     # four dimensions: the batch's stride may be any, the inner two are below 2^32
     q, freq = x.unsqueeze(1), m.rotary_frequencies(64, device="cuda")[0]
     assert torch.equal(m.rotary(q, freq), m.rotary(q.contiguous(), freq))
+
+
+# ------------------------------------------------------------------ gradients over many rows a team
+def closed_norm_backward(d, x, z, w, kind, act, eps, scale):
+    """oracle.gated_norm_backward without the Jacobian: dx = r (dn - n <dn, n> / K - [layer] mean dn)."""
+    D = x.shape[-1]
+    n, r = oracle.block._normalised(x, kind, eps)
+    w = np.ones(D) if w is None else w
+    a, da = (1.0, None) if z is None else oracle.block._activation(z, act)
+    m = scale * d
+    dn = m * w * a
+    dx = r * (dn - n * (dn * n).sum(-1, keepdims=True) / (1 if kind == "l2" else D)
+              - (dn.mean(-1, keepdims=True) if kind == "layer" else 0))
+    return dx, None if z is None else m * n * w * da, (m * a * n).reshape(-1, D).sum(0)
+
+
+@pytest.mark.parametrize("kind,act", list(itertools.product(KINDS, ACTS)))
+def test_closed_norm_gradients_are_the_oracles(kind, act):
+    r = np.random.default_rng(1)
+    d, x, w = r.standard_normal((2, 3, 9)), r.standard_normal((2, 3, 9)), r.standard_normal(9)
+    z = r.standard_normal((2, 3, 9)) if act != "none" else None
+    for a, b in zip(closed_norm_backward(d, x, z, w, kind, act, 1e-3, 0.7),
+                    oracle.gated_norm_backward(d, x, z, w, kind, act, 1e-3, 0.7)):
+        assert (a is None and b is None) or np.allclose(a, b, rtol=1e-12, atol=1e-13)
+
+
+# rows: more than one a team for every team size (296 blocks of 256 threads), with an innermost size that
+# wraps within a team's run, and block-wide teams of several rows
+@pytest.mark.parametrize("dtype,shape", [
+    (torch.bfloat16, (2, 1700, 7, 32)), (torch.bfloat16, (3, 1003, 7, 64)), (torch.bfloat16, (2, 1100, 5, 128)),
+    (torch.bfloat16, (2, 700, 5, 256)), (torch.bfloat16, (2, 401, 7, 512)), (torch.bfloat16, (1, 903, 3, 1024)),
+    (torch.bfloat16, (2, 167, 3, 2048)), (torch.bfloat16, (1, 301, 3, 4096)), (torch.bfloat16, (1, 201, 3, 8192)),
+    (torch.bfloat16, (2, 1500, 3, 33)), (torch.bfloat16, (1, 301, 3, 2050)), (torch.bfloat16, (1, 301, 2, 4099)),
+    (torch.float32, (2, 1700, 7, 32)), (torch.float32, (2, 700, 5, 128)), (torch.float32, (1, 903, 3, 512)),
+    (torch.float32, (1, 301, 3, 1024)), (torch.float32, (1, 301, 3, 2052)), (torch.float32, (1, 301, 3, 4096)),
+    (torch.float32, (1, 201, 3, 8192)), (torch.float32, (1, 301, 2, 2049)), (torch.float32, (1, 151, 2, 8191)),
+])
+def test_norm_gradients_of_many_rows(dtype, shape):
+    x, gate, w, _, d = tensors(shape, dtype, shape[-1], "silu", True, False)
+    x = x.transpose(1, 2).contiguous().transpose(1, 2)  # the scan's layout under the projection's
+    D = shape[-1]
+    for kind, act, z in (("layer", "silu", gate), ("rms", "sigmoid", gate), ("l2", "none", None)):
+        got = la().gated_norm_backward(d, x, z, w, **how(kind, act, scale=0.7))
+        dd, xx, zz, ww = (f64(t) for t in (d, x, z, w))
+        ref = closed_norm_backward(dd, xx, zz, ww, kind, act, 1e-5, 0.7)
+        # the bars of check_norm_backward
+        terms, steps, r, big = norm_terms(xx, zz, ww, kind, act, 1e-5, 0.7)
+        a = 1.0 if zz is None else np.abs(oracle.block._activation(zz, act)[0])
+        dn = np.abs(0.7 * dd) * np.abs(ww) * a
+        t = r * (dn + big * (dn * big).sum(-1, keepdims=True) / (1 if kind == "l2" else D)
+                 + (dn.mean(-1, keepdims=True) if kind == "layer" else 0))
+        worst = np.max(steps, axis=-1, keepdims=True) if np.ndim(steps) else steps
+        near(got[0], ref[0], t, 3 * worst, dtype, "dx")
+        if zz is not None:
+            s = oracle.block._activation(zz, "sigmoid")[0]
+            near(got[1], ref[1], np.abs(0.7 * dd) * big * np.abs(ww) * (s * (1 + np.abs(zz)) if act == "silu" else s), 2 * steps + 8,
+                 dtype, "dgate")
+        col = (np.abs(0.7 * dd) * a * big).reshape(-1, D).sum(0)
+        near(got[2], ref[2], col, dd.reshape(-1, D).shape[0] + np.max(steps), torch.float32, "dweight")
+        again = la().gated_norm_backward(d, x, z, w, **how(kind, act, scale=0.7))
+        assert all(torch.equal(p, q) for p, q in zip(got, again) if p is not None)

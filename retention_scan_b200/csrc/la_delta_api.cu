@@ -256,6 +256,17 @@ la_status la_delta_backward_ws(const void* q, const void* k, const void* v, cons
             workspace_bytes < la_delta_backward_workspace_size(B, H, Hk, T, Dk, Dv, dtype, kind))
             return LA_ERR_INVALID_ARG;
     }
+    if (H == 0 && (!fits_int(static_cast<long long>(B) * Hk) || static_cast<long long>(B) * Hk > LLONG_MAX / 1024 / (T + 1LL)))
+        return LA_ERR_UNSUPPORTED;
+    const long long keys = H == 0 ? static_cast<long long>(B) * Hk * T : 0;
+    if (keys > 0) {  // key heads that serve no value head: dq and dk are sums over nothing
+        if (!dq || !aligned16(dq) || !dk || !aligned16(dk)) return LA_ERR_INVALID_ARG;
+        if (launch_fault_injected()) return LA_ERR_CUDA;
+        const size_t bytes = (dtype == LA_BF16 ? 2 : 4) * static_cast<size_t>(keys) * Dk;
+        const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        return cudaMemsetAsync(dq, 0, bytes, s) == cudaSuccess && cudaMemsetAsync(dk, 0, bytes, s) == cudaSuccess ? LA_OK
+                                                                                                                : LA_ERR_CUDA;
+    }
     if (H == 0 || (BH == 0 && !(d_log_g && kind == LA_DECAY_PER_HEAD))) return LA_OK;
     if (launch_fault_injected()) return LA_ERR_CUDA;
     a.stream = reinterpret_cast<cudaStream_t>(stream);

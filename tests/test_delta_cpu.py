@@ -211,3 +211,10 @@ def test_binding_refuses_before_it_calls():
         la.delta_forward(**dict(ok, q=z(2, 3, 16)))
     with pytest.raises(ValueError, match="CUDA"):
         la.delta_decode_step(z(1, 2, 16), z(1, 2, 16), z(1, 4, 16), z(1, 4), z(1, 4, 16, 16))
+
+
+def test_key_heads_without_value_heads(L):  # noqa: F811
+    # their gradients are written (zeros), so they have to have an address
+    assert bwd(L, H=0, dq=None) == 1 and bwd(L, H=0, dk=8) == 1
+    assert bwd(L, H=0, Hk=0, dq=None, dk=None) == 0 and bwd(L, H=0, T=0, dq=None) == 0 and bwd(L, H=0, B=0, dq=None) == 0
+    assert bwd(L, H=0, B=1 << 20, Hk=1 << 20) == 2 and bwd(L, H=0, B=1 << 30, T=1 << 30) == 2

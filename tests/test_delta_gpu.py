@@ -574,3 +574,14 @@ def test_long_gradients_of_states_do_not_drift(Dk, Dv, dtype, unit):
     assert abs(bias) <= bar / 10 + 24 * 2.0 ** -24
     for x, r in zip(got[:3], want[:3]):
         assert slice_err(x, r) <= bar + unit + (2.0 ** -8 if dtype == torch.bfloat16 else 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_key_heads_that_serve_no_value_head(dtype):
+    q, k, v, beta, lg, S0 = dev(*make(2, 4, 2, 70, 32, 16, dtype))
+    none = [t[:, :0].contiguous() for t in (v, beta, lg, S0)]
+    y, S = la().delta_forward(q, k, none[0], none[1], 2, none[2], none[3])
+    assert y.shape == (2, 0, 70, 16) and S.shape == (2, 0, 32, 16)
+    outs = (torch.full_like(q, 7.0), torch.full_like(k, 7.0), *(torch.empty_like(t) for t in none))
+    got = la().delta_backward(q, k, none[0], none[1], none[0], 2, none[2], none[3], out=outs)
+    assert got[0] is outs[0] and not got[0].any() and not got[1].any()

@@ -654,8 +654,8 @@ LA_API la_status la_decode_step(const void* q, const void* k, const void* v,
  *   v, out         [B,H,T,Dv], `dtype`.
  *   beta           [B,H,T] fp32, finite.
  *   decay          NULL or a descriptor as for la_chunk_forward.  A log g below
- *                  -128 (-infinity included) counts as -128: e^-128 is zero next to anything an
- *                  fp32 state can hold.
+ *                  -128 (-infinity included) counts as -128: e^-128 is zero next to
+ *                  anything an fp32 state can hold.
  *   q_scale        finite factor of the output.
  *   init_state     NULL (zeros) or S_0; final_state NULL or S_T: [B,H,Dk,Dv] fp32.
  *   workspace      la_delta_workspace_size(...) bytes of device memory, 16-byte
@@ -674,10 +674,14 @@ LA_API la_status la_decode_step(const void* q, const void* k, const void* v,
  * off as its own rounding makes it (1.7e-3, 2-norm), also where keys and queries
  * close to one another make the chunk's terms cancel.  A system far from
  * the identity amplifies that: one key repeated with beta = 1, 3e-5; repeated
- * with alternating sign and beta = 1.9, 4e-3 (fp32 inputs: 1e-5).  The gradients
- * in fp32 are within 1e-5 of the rule's in 64 bits, 2-norm, for such keys; a
- * decay per head of a single head can be further off (2e-5), its gradient being
- * what is left of one long sum of terms of both signs.
+ * with alternating sign and beta = 1.9, 4e-3 (fp32 inputs: 1e-5).
+ * The gradients in fp32 are within 1.3e-5 of the rule's in 64 bits (2-norm of the
+ * whole tensor, for such keys and dy that is not zero but for a few tokens), 3e-6
+ * where three planes are taken (la_delta_backward_ws, workspace); so a sequence's
+ * last digits can differ with the size of its batch.  A decay per head of a single
+ * head can be off by 2e-5, its gradient being what is left of one long sum of
+ * terms of both signs.  Where dy is zero but for a few tokens, dbeta and d log g are
+ * as exact relative to the terms that they sum, not to what those leave.
  *
  * Inputs are finite (log g may be -infinity).  A NaN or an infinity spoils the
  * outputs of the whole 64-token chunk it lies in and everything after it, so fill
@@ -782,7 +786,9 @@ typedef enum {
  *   eps            >= 0; with 0 a row of zeros gives NaN, as 0 / 0.
  *   scale          finite; applies to the normalised part only.
  *
- * D up to 8192.  n0 n1 n2 == 0 is a no-op.  Errors (synchronous):
+ * D up to 8192.  The statistics are fp32: where the sum of squares passes its range
+ * (values beyond 2e17 to 2e19, by D) the normalised part is 0.
+ * n0 n1 n2 == 0 is a no-op.  Errors (synchronous):
  * LA_ERR_INVALID_ARG for a NULL view or data, an address that is not a multiple
  * of the element, strides outside their range, an output with stride 0 along a
  * size above 1, bad sizes, kinds or numbers; LA_ERR_UNSUPPORTED for D > 8192 or

@@ -4,8 +4,10 @@ la_gated_norm).  Argument checks and output allocation only; every step runs
 in the library's kernels.
 
 Tensors are read and written through their strides (the last dimension dense),
-so projections laid out [B,T,H,D] and the scans' [B,H,T,D] need no copy
-between them: pass x.transpose(1, 2).
+so queries and keys go from projections laid out [B,T,H,D] to the scans'
+[B,H,T,D], and the scan's output back, without a copy: pass x.transpose(1, 2).
+The scans themselves take contiguous [B,H,T,D]: values, beta, log g and the
+gradient of the output are the caller's to lay out.
 
 stream (every call): None, the current one, or a stream that the caller has
 ordered behind the inputs; the call runs and allocates on it, and tensors may

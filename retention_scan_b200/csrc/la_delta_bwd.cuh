@@ -31,7 +31,7 @@ namespace {
 // ---------------------------------------------------------------- reverse scan
 // Warp = 16 value columns, dS^T in its accumulators, as in the forward scan; bound
 // as that by the tensor rate with eight warps an SM, by its chain with fewer (2.5 us
-// a chunk at B2 H16 T4096 D128, four warps a slice: 160 us).
+// a chunk at B2 H16 T4096 D128, four warps a slice: 167 us by itself, cold).
 struct RevArgs {
     const void* dy;
     const unsigned char* records;
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(32 * G * NS + 32) group_reverse_kernel(const _
 // contraction over the value columns streams 16 of them at a time (S, dS, E, dR,
 // dY) through a ring of bulk copies; then the C x C gradients go through shared
 // memory as A operands of the products with K and Q.  At B2 H16 T4096 D128 (2048
-// chunks) 255 us.  Of a block's 32 000 cycles 4 000 are its first loads, 16 000 the
+// chunks) 255 to 261 us.  Of a block's 32 000 cycles 4 000 are its first loads, 16 000 the
 // slices (the tensor pipe's 11 000 and as many of shared memory's reads), 3 000 the
 // scores, 1 500 dP' and dA', 5 000 their products, 2 500 the outputs; nothing
 // overlaps between blocks with one an SM (16 warps hold all registers).  8 warps took

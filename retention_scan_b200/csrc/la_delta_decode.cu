@@ -8,7 +8,8 @@
 // between the read and the write (8 float4 a thread at Dk = 128): the
 // state crosses HBM once each way, and y comes from the same sums (the last
 // line above substitutes the updated state), not from a second pass.
-// B256 H32 Dk = Dv = 128: 181 us, 0.92 of the measured copy rate.  Blocks of 32
+// B256 H32 Dk = Dv = 128: 181 to 191 us, 0.88 to 0.92 of the measured copy rate (967 at
+// Dv = 127, a column at a time).  Blocks of 32
 // columns, ten and more an SM, so that one's loads run while another stores: with a
 // whole head a block (two an SM) the same took 268 us.
 #include <cuda_bf16.h>

@@ -39,7 +39,7 @@ __global__ void split_kernel(const float* __restrict__ x, __nv_bfloat16* __restr
 // these steps with five blocks an SM.  A substitution of the whole 64 x 64 matrix
 // by one thread a column was bound by fetching its 2700 unrolled instructions for
 // two warps (766 us at B1 H32 T65536 D128); K and Q by cp.async spent 5000 of a
-// block's 17 800 cycles on addresses (531 us); now 350 us.
+// block's 17 800 cycles on addresses (531 us); now 350 to 369 us.
 constexpr int kPrepThreads = 128;
 constexpr int kBS = 24;                // row stride of a 16 x 16 bf16 block: ldmatrix without bank conflicts
 constexpr int kBlock = 16 * kBS;       // elements of such a block
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
 // and the errors E of every chunk, as bf16 planes.
 // Bound by the tensor core's rate for mma.sync: 504 instructions a warp and chunk
 // at D128 (bf16), 8 cycles each on a scheduler, 8 060 cycles a chunk with eight warps
-// an SM (B8 H16 T4096: 376 us with P in one plane and 484 instructions, 392 with two).
+// an SM (9 300 measured; B8 H16 T4096: 402 us by itself, cold).
 template <int DKP, int NI, int NM, int NP, int NW, bool kOut, typename TIn>
 __global__ void __launch_bounds__(32 * NW) scan_kernel(const __grid_constant__ CUtensorMap mk,
                                                              const __grid_constant__ CUtensorMap mq,
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(32 * NW) scan_kernel(const __grid_constant__ C
 // The same scan with G warps a slice (la_delta.cuh), for few (b, h): NS slices a
 // block and a warp that feeds the stages.  Per chunk and slice three barriers:
 // the state's parts, the right-hand sides R, and U are exchanged.  At B1 H32
-// T65536 D128 (256 slices): one warp a slice 3.3 us a chunk, two 2.2 us.
+// T65536 D128 (256 slices): one warp a slice 3.3 us a chunk, two 2.3 us.
 template <int DKP, int NM, int G>
 struct GroupSpace {  // a slice's exchange, in 16-byte words
     static constexpr int kSteps = DKP / 16 / G;       // k-steps of a warp's part of the key width
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(32 * G * NS + 32) group_scan_kernel(const __gr
     const int tq = (lane & 3) * 2;
     const LaneOffsets oc = swz_cols(lane), orow = swz_rows(lane);
     // two warps a slice: a body for each, whose block indices are constants (2258 us at the
-    // size above against 2530); four run one body (four would not fit the instruction cache)
+    // size above against 2530, with P in one plane; 2343 with its second); four run one body (four would not fit the instruction cache)
     auto scan = [&](auto which) {
     const int w = which;
     float S[kCols / 8][4];

@@ -100,18 +100,20 @@ inline ScanArgs scan_args(const Plan& p, const Args& a) {
 
 bool supports(int Dk, int Dv, la_dtype dtype);
 
-// bf16 planes of an fp32 operand.  Two keep 16 bits, enough for states and for
-// gradients of many values, whose errors average: 4e-6 of their norm, 7e-6 at worst.
-// fp32 inputs take three, and so do three kinds of bf16 backward whose fp32 outputs
-// (dbeta, the decay's gradient) two planes leave above 1e-5 of 64 bits:
+// bf16 planes of an fp32 operand.  Two keep 16 bits, enough for states: 4e-6 of their
+// norm.  fp32 inputs take three, and so do three kinds of bf16 backward, for their fp32
+// outputs (dbeta, the decay's gradient).  Off 64 bits by (2-norm of the tensor; median
+// and worst of 544 random cases, or worst) and us, with two planes and with three:
 // - a decay per head, whose gradient sums over the whole sequence terms of both signs
-//   that leave a small rest (7.6e-5 with two planes, 8e-6 with three, and 2e-5 where
-//   the output is one head's only);
-// - few tokens times heads, where one cancelling value can be the norm (up to 5e-5
-//   below 64 of them, 9.2e-6 at 566);
-// - keys of at most 32 dimensions, which average little (8.8e-6 at 1206 of them).
-// Three planes take 1.3 to 1.45 times as long: 573 and 827 us at B2 H16 T4096 D128, 63
-// and 88 at B1 H8 T512 D128, 123 and 172 at B2 H8 T2048 Dk32 Dv64.
+//   that leave a small rest: 1.1e-4 and 9e-6 (one head), 2.3e-5 and 2e-6 (four);
+//   575 and 818 us at B2 H16 T4096 D128.
+// - fewer than 4096 tokens times heads, calls so small that the third plane costs
+//   little: 3e-6 to 6e-6, worst 1.3e-5, and 5e-7 to 1.2e-6, worst 2e-6; 43 and 41 us at
+//   64 of them, 48 and 60 at 1024, 83 and 108 at 4092 (D128).  At 4096 and more,
+//   6e-6, worst 1.0e-5, and 1.3e-6; 60 and 76 us at B1 H8 T512, 568 and 810 at B2
+//   H16 T4096.
+// - keys of at most 32 dimensions: 8e-6 and 1.2e-6; 121 and 168 us at B2 H8 T2048
+//   Dk32 Dv64.
 constexpr int kNarrowKeys = 32;
 constexpr long long kFewTokens = 4096;
 inline int operand_planes(const Args& a, bool backward) {

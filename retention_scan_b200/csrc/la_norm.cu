@@ -469,7 +469,7 @@ cudaError_t run(const Args& a, bool backward) {
 // Threads a row: two vectors each, so that a row's index arithmetic and
 // reductions are shared by 16 bf16 elements (forward, B8 H16 T4096 D128: one
 // vector a lane took 38 instructions an element and 122 us, two, with two fp32
-// values an instruction, 19 and 65 us), up to a warp with four; wider rows take
+// values an instruction, 19 and 65 to 69 us), up to a warp with four; wider rows take
 // the block, 1 to 32 vectors a thread.
 template <typename T, int V>
 cudaError_t teams(const Args& a, bool backward) {

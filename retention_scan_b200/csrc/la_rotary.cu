@@ -12,7 +12,7 @@
 // Angles are taken modulo 2 pi in 64 bits with what the product's rounding left: at
 // position 10^6 an fp32 product would be off by 0.03 rad, at 2^45 a 64-bit one by
 // 0.002; here the angle is off by 2^-23 up to 2^53.
-// B8 H16+16 T4096 D128 bf16: 89 us, 0.94 of the measured copy rate (143 us with the
+// B8 H16+16 T4096 D128 bf16: 89 to 92 us, 0.90 to 0.94 of the measured copy rate (143 us with the
 // sines read from shared memory for every head and one row in flight a thread).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -155,3 +155,22 @@ def test_a_stream_of_another_device_is_refused():
     for name, call in CALLS.items():
         with pytest.raises(ValueError, match="stream"):
             call(i, stream=Elsewhere())
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_capture_that_forks_to_a_stream_of_its_own(name):
+    # the call's allocations come from the graph's pool, on the forked stream; what is dropped is not the next call's
+    i = inputs()
+    CALLS[name](i)
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        CALLS[name](i, stream=s)  # dropped
+        got = flat(CALLS[name](i, stream=s))
+        torch.cuda.current_stream().wait_stream(s)
+        new = torch.full((1 << 20,), 7.0, device="cuda")
+    for scale in (1.0, -0.5):
+        i["v"].mul_(scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, flat(CALLS[name](i)))) and (new == 7.0).all()

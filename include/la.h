@@ -689,9 +689,9 @@ LA_API la_status la_decode_step(const void* q, const void* k, const void* v,
  *
  * Errors (synchronous, nothing enqueued): LA_ERR_INVALID_ARG for a NULL or
  * misaligned pointer (16 bytes; 4 for beta and log_g), bad sizes (H not a
- * multiple of Hk among them), a bad decay or dtype, a q_scale that is not
- * finite, a workspace that is NULL or too small; LA_ERR_UNSUPPORTED for other
- * widths or more than 2^31 - 1 blocks; LA_ERR_CUDA if a launch fails.
+ * multiple of Hk, B H of 2^28 or more, T above 2^30 among them), a bad decay or
+ * dtype, a q_scale that is not finite, a workspace that is NULL or too small;
+ * LA_ERR_UNSUPPORTED for other widths or more than 2^31 - 1 blocks; LA_ERR_CUDA if a launch fails.
  */
 LA_API la_status la_delta_forward_ws(const void* q, const void* k, const void* v, const float* beta,
                                      const la_decay* decay, float q_scale, const float* init_state,

@@ -673,8 +673,8 @@ LA_API la_status la_decode_step(const void* q, const void* k, const void* v,
  * norm 1 and beta in (0, 1)) or 24 (fp32 inputs: 1e-6 to 3e-6).  A bf16 y is as far
  * off as its own rounding makes it (1.7e-3, 2-norm), also where keys and queries
  * close to one another make the chunk's terms cancel.  A system far from
- * the identity amplifies that: one key repeated with beta = 1, 3e-5; repeated
- * with alternating sign and beta = 1.9, 4e-3 (fp32 inputs: 1e-5).
+ * the identity amplifies that: one key repeated or nearly so with beta = 1, 5e-5;
+ * with beta = 1.9, 7e-4, and 4e-3 at worst where its sign alternates (fp32 inputs: 1e-5).
  * The gradients in fp32 are within 1.3e-5 of the rule's in 64 bits (2-norm of the
  * whole tensor, for such keys and dy that is not zero but for a few tokens), 3e-6
  * where three planes are taken (la_delta_backward_ws, workspace); so a sequence's
